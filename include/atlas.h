@@ -480,6 +480,225 @@ atlas_status atlas_out_proj_unorder(const void *o, const void *w, int64_t batch,
                                     int32_t c_out, atlas_dtype dtype, void *y,
                                     atlas_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions, general form.
+ * ------------------------------------------------------------------------ */
+
+/* Channels of pair k of an axis segment of width d: INTERLEAVED (2k, 2k+1),
+ * HALF (k, k + d/2). */
+typedef enum { ATLAS_ROTARY_INTERLEAVED = 0, ATLAS_ROTARY_HALF = 1 } atlas_rotary_layout;
+
+/* Frequencies of a segment of width d, extension factor s (of its axis):
+ *   PLAIN     omega_k = theta^(-2k/d)
+ *   NTK       omega_k = (theta * s^(d/(d-2)))^(-2k/d)   (d = 2: as PLAIN)
+ *   BY_PARTS  omega'_k = omega_k * (g + (1-g)/s), g = clamp((turns_k -
+ *             beta_slow) / (beta_fast - beta_slow), 0, 1), turns_k = original
+ *             * omega_k / (2 pi): pairs that turn often over the trained
+ *             `original` positions keep their frequency, slow ones are
+ *             interpolated by s.
+ * Linear interpolation is PLAIN with the axis' scale divided by s. */
+typedef enum {
+    ATLAS_ROTARY_PLAIN = 0,
+    ATLAS_ROTARY_NTK = 1,
+    ATLAS_ROTARY_BY_PARTS = 2
+} atlas_rotary_scaling;
+
+/* Rows of the result: in the input's raster order, moved from raster to cube
+ * order (as atlas_cube_reorder), or from cube to raster order (as
+ * atlas_cube_unorder). */
+typedef enum {
+    ATLAS_ORDER_RASTER = 0,
+    ATLAS_ORDER_REORDER = 1,
+    ATLAS_ORDER_UNORDER = 2
+} atlas_order;
+
+/* The first d_t + d_h + d_w channels of a head rotate (each even, >= 0; their
+ * sum at most head_dim), in contiguous segments of the axes t, h, w; the
+ * channels behind them pass bit-exactly. The angle of pair k of an axis is
+ * position * scale * omega_k; the result is multiplied by `magnitude` (rotated
+ * channels only). transpose != 0 rotates by the negative angle: the transpose of
+ * the same map, which takes output gradients to input gradients. */
+typedef struct {
+    double theta;
+    int32_t d_t, d_h, d_w;
+    double scale_t, scale_h, scale_w;
+    int32_t layout;                              /* atlas_rotary_layout  */
+    int32_t scaling;                             /* atlas_rotary_scaling */
+    double factor_t, factor_h, factor_w;         /* >= 1 (NTK, BY_PARTS) */
+    double original_t, original_h, original_w;   /* > 0 (BY_PARTS)       */
+    double beta_fast, beta_slow;                 /* fast > slow (BY_PARTS) */
+    double magnitude;
+    int32_t transpose;
+} atlas_rotary;
+
+/* One tensor of a call: rows of heads * head_dim elements, src_stride and
+ * dst_stride elements apart (0: contiguous), e.g. the Q columns of a fused
+ * projection's output. rotate == 0: the rows are only moved, bit-exactly. */
+typedef struct {
+    const void *src;
+    void *dst;
+    int64_t src_stride, dst_stride;
+    int32_t heads;
+    int32_t rotate;
+} atlas_rotary_tensor;
+
+/*
+ * atlas_rotary_apply -- rotary positions of up to 8 tensors of the same tokens in
+ * one launch, with the cube reorder (or its inverse) on the way.
+ *
+ * Passages: as atlas_cube_reorder and atlas_rope3d, whose rotation is the
+ * INTERLEAVED layout with the whole head rotated and PLAIN frequencies.
+ * Every tensor has batch * T*H*W rows. A token's position is its grid index
+ * (t, h, w), or row r of `positions`, a DEVICE int32 array [batch * T*H*W,
+ * n_axes] indexed by the token's raster row (n_axes 1, with d_h = d_w = 0, or
+ * 3; any int32 values). cube is read for REORDER and UNORDER only.
+ * cos and sin are formed per token in the call (angles reduced in fp64, then
+ * fp32): nothing is allocated or cached, and any stream, graph or number of
+ * overlapping calls may use it. Rotation in fp32, one rounding to dtype (RNE).
+ * src may equal dst (with equal strides, order RASTER: in place); the
+ * destinations may share no element with another tensor of the call.
+ * head_dim <= 512, heads <= 65535.
+ * Errors: NULL tensors, src, dst or rot, or NULL cube with an order that reads it
+ * (NULL); extents, batch, heads, n_tensors outside 1..8, a stride shorter than a
+ * row, more than 2^31-1 rows (SHAPE); pointers, rows or strides not multiples of
+ * 16 bytes, positions not 4-byte aligned (ALIGN); dtype, widths, layout, scaling
+ * or its parameters, n_axes (UNSUPPORTED); overlap (ALIAS).
+ */
+atlas_status atlas_rotary_apply(const atlas_rotary_tensor *tensors, int32_t n_tensors,
+                                int64_t batch, atlas_grid3 grid, const atlas_cube3 *cube,
+                                atlas_order order, const int32_t *positions, int32_t n_axes,
+                                int32_t head_dim, atlas_dtype dtype, const atlas_rotary *rot,
+                                atlas_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Differential attention.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * atlas_diff_lambda -- the weight of the second map from four learned vectors:
+ *   lambda_i = exp(<q1_i, k1_i>) - exp(<q2_i, k2_i>) + lambda_init.
+ * q1, k1, q2, k2: [n, d] of dtype, contiguous. lambda: fp32 [n] (n = heads, or
+ * 1 for a weight that all heads share). Dot products and exp in fp32.
+ * atlas_diff_lambda_bwd: their gradients (same shape and dtype) from dlambda.
+ * Errors: NULL; n or d < 1 (SHAPE); pointers not aligned to their element
+ * (ALIGN); dtype (UNSUPPORTED); an output overlapping another argument (ALIAS).
+ */
+atlas_status atlas_diff_lambda(const void *q1, const void *k1, const void *q2, const void *k2,
+                               int32_t n, int32_t d, double lambda_init, atlas_dtype dtype,
+                               float *lambda, atlas_stream_t stream);
+atlas_status atlas_diff_lambda_bwd(const void *q1, const void *k1, const void *q2,
+                                   const void *k2, int32_t n, int32_t d, const float *dlambda,
+                                   atlas_dtype dtype, void *dq1, void *dk1, void *dq2, void *dk2,
+                                   atlas_stream_t stream);
+
+/*
+ * atlas_diff_attn -- differential attention over the windows and global tokens
+ * of atlas_local_global_attn_ex (same tensors, layout and mask).
+ *
+ * The two halves of a head's channels are two maps of width head_dim/2: with
+ * q = [q1 | q2], k = [k1 | k2] and s_m = scale * <q_m, k_m> over a query's
+ * allowed keys,
+ *   o = (softmax(s_1) - lambda_h * softmax(s_2)) v,   v of width head_dim.
+ * A rotary embedding of such a head turns each map by itself: call
+ * atlas_rotary_apply with twice the heads of half the width.
+ * lambda: DEVICE fp32 [n_lambda], n_lambda = heads or 1 (shared by all heads).
+ * softmax_scale <= 0 selects 1/sqrt(head_dim/2).
+ * o_d, o_g: as q_d, q_g. s_d, s_g: same shapes, the second map's own output
+ * softmax(s_2) v, which the backward pass needs (NULL to skip, both or none).
+ * lse: optional fp32 [batch, heads, 2, n_detail + n_global], the natural log of
+ * both maps' softmax denominators.
+ * BF16: tcgen05 kernel, both maps' softmax and both outputs in fp32, each map's
+ * unnormalised weights rounded to bf16 before their product with v, o rounded
+ * once. FP32: exact fp32 products. head_dim 64 or 128.
+ * A row's result depends on no key outside its problem's allowed range, whatever
+ * those keys hold, except (BF16) that a non-finite value of v in a window
+ * shorter than 128 rows may reach the rows of the neighbouring windows that share
+ * its 128 rows.
+ * Errors: as atlas_local_global_attn_ex; NULL lambda (NULL), n_lambda neither 1
+ * nor heads (SHAPE), lambda not 4-byte aligned (ALIGN).
+ */
+atlas_status atlas_diff_attn(const void *q_d, const void *k_d, const void *v_d,
+                             int64_t n_detail, const void *q_g, const void *k_g,
+                             const void *v_g, int64_t n_global,
+                             const atlas_attn_layout *layout, int32_t heads, int32_t head_dim,
+                             float softmax_scale, atlas_dtype dtype, const float *lambda,
+                             int32_t n_lambda, void *o_d, void *o_g, void *s_d, void *s_g,
+                             float *lse, atlas_stream_t stream);
+
+/*
+ * atlas_diff_attn_bwd -- gradients of atlas_diff_attn. With P_m the two maps'
+ * weights, dP = <do_i, v_j> and D_m = <do_i, o_m,i> (o_2 = s, o_1 = o + lambda s):
+ *   dS_1 = P_1 (dP - D_1),  dS_2 = -lambda P_2 (dP - D_2),
+ *   dq_m = scale dS_m k_m,  dk_m = scale dS_m^T q_m,
+ *   dv = (P_1 - lambda P_2)^T do,  dlambda = -sum D_2
+ * (summed over the heads as well when n_lambda is 1).
+ * o_*, s_*, lse: the forward's. workspace: DEVICE fp32, 16-byte aligned, of
+ * atlas_diff_attn_bwd_workspace bytes, overwritten; calls that overlap on the
+ * GPU need one each. dq_*, dk_*, dv_*: as q_*; dlambda: fp32 [n_lambda]. All sums
+ * have a fixed order: the same call gives the same bits.
+ * Errors: as atlas_diff_attn; NULL or overlapping outputs and workspace.
+ */
+atlas_status atlas_diff_attn_bwd(
+    const void *q_d, const void *k_d, const void *v_d, const void *o_d, const void *s_d,
+    const void *do_d, int64_t n_detail, const void *q_g, const void *k_g, const void *v_g,
+    const void *o_g, const void *s_g, const void *do_g, int64_t n_global,
+    const atlas_attn_layout *layout, int32_t heads, int32_t head_dim, float softmax_scale,
+    atlas_dtype dtype, const float *lambda, int32_t n_lambda, const float *lse, void *workspace,
+    void *dq_d, void *dk_d, void *dv_d, void *dq_g, void *dk_g, void *dv_g, float *dlambda,
+    atlas_stream_t stream);
+
+/* Bytes of atlas_diff_attn_bwd's workspace (host; 0 for invalid sizes). */
+int64_t atlas_diff_attn_bwd_workspace(int64_t batch, int64_t n_detail, int64_t n_global,
+                                      int32_t heads);
+
+/* ------------------------------------------------------------------------
+ * Group norm, channels last, with an activation.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { ATLAS_ACT_NONE = 0, ATLAS_ACT_SILU = 1 } atlas_activation;
+
+/*
+ * atlas_group_norm -- y = act(gamma * (x - mean) * rstd + beta).
+ *
+ * x, y: [samples, rows, channels] of dtype, contiguous; group g holds channels
+ * [g * channels/groups, (g+1) * channels/groups); mean and variance (biased) run
+ * over a sample's rows and the group's channels, rstd = 1/sqrt(var + eps).
+ * samples = batch, rows = T*H*W normalises latents; samples = tokens, rows = 1,
+ * groups = heads normalises each head of an attention output by itself.
+ * gamma, beta: fp32 [channels], NULL for 1 and 0. act: NONE or SILU (z
+ * sigmoid(z)). stats: fp32 [samples, groups, 2], receives (mean, rstd); NULL to
+ * skip (the backward pass needs it). workspace: DEVICE, 16-byte aligned, of
+ * atlas_group_norm_workspace bytes (NULL when that is 0); calls that overlap on
+ * the GPU need one each. y may equal x. Statistics and arithmetic in fp32
+ * (partial statistics joined in fp64), one rounding to dtype.
+ * Errors: NULL; samples, rows, channels or groups < 1, channels not a multiple of
+ * groups, samples*rows or channels above 2^31-1 (SHAPE); x or y not 16-byte
+ * aligned, fp32 arrays not 4-byte aligned (ALIGN); dtype, act, eps < 0 or not
+ * finite (UNSUPPORTED); partial overlaps (ALIAS).
+ */
+atlas_status atlas_group_norm(const void *x, const float *gamma, const float *beta, void *y,
+                              int64_t samples, int64_t rows, int64_t channels, int32_t groups,
+                              double eps, atlas_activation act, atlas_dtype dtype, float *stats,
+                              void *workspace, atlas_stream_t stream);
+
+/*
+ * atlas_group_norm_bwd -- dx, dgamma, dbeta from dy, the forward's x and stats.
+ * With z = gamma xhat + beta, dz = dy act'(z), dh = dz gamma and the means over the
+ * group's elements: dx = rstd (dh - mean(dh) - xhat mean(dh xhat)),
+ * dgamma = sum dz xhat, dbeta = sum dz (over samples and rows; fp32, either may
+ * be NULL). dx may equal dy or x. Sums have a fixed order. Errors as the forward.
+ */
+atlas_status atlas_group_norm_bwd(const void *dy, const void *x, const float *gamma,
+                                  const float *beta, const float *stats, void *dx,
+                                  float *dgamma, float *dbeta, int64_t samples, int64_t rows,
+                                  int64_t channels, int32_t groups, atlas_activation act,
+                                  atlas_dtype dtype, void *workspace, atlas_stream_t stream);
+
+/* Bytes of the workspace of atlas_group_norm (backward 0) or
+ * atlas_group_norm_bwd (backward 1); host; 0 for invalid sizes. */
+int64_t atlas_group_norm_workspace(int64_t samples, int64_t rows, int64_t channels,
+                                   int32_t groups, atlas_dtype dtype, int32_t backward);
+
 /* Human-readable name of a status. Never NULL. */
 const char *atlas_status_string(atlas_status status);
 

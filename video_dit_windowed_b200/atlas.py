@@ -45,6 +45,43 @@ class AttnLayout(ctypes.Structure):
                 ("global_window_offsets", ctypes.c_void_p)]
 
 
+class Rotary(ctypes.Structure):
+    _fields_ = [("theta", ctypes.c_double), ("d_t", ctypes.c_int32), ("d_h", ctypes.c_int32),
+                ("d_w", ctypes.c_int32), ("scale_t", ctypes.c_double),
+                ("scale_h", ctypes.c_double), ("scale_w", ctypes.c_double),
+                ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("factor_t", ctypes.c_double), ("factor_h", ctypes.c_double),
+                ("factor_w", ctypes.c_double), ("original_t", ctypes.c_double),
+                ("original_h", ctypes.c_double), ("original_w", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("magnitude", ctypes.c_double), ("transpose", ctypes.c_int32)]
+
+
+class RotaryTensor(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
+                ("src_stride", ctypes.c_int64), ("dst_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("rotate", ctypes.c_int32)]
+
+
+ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}
+ROTARY_SCALINGS = {"none": 0, "ntk": 1, "by_parts": 2}
+ORDERS = {"raster": 0, "reorder": 1, "unorder": 2}
+ACTIVATIONS = {"none": 0, "silu": 1}
+
+
+def make_rotary(theta, split, scales=(1.0, 1.0, 1.0), *, layout="interleaved", scaling="none",
+                factor=(1.0, 1.0, 1.0), original=(0.0, 0.0, 0.0), beta_fast=32.0, beta_slow=1.0,
+                magnitude=1.0) -> Rotary:
+    """Parameters of ``rotary``: ``split`` (d_t, d_h, d_w) channels rotate (the
+    first ones of a head), positions are multiplied by ``scales``; ``layout``
+    "interleaved" or "half"; ``scaling`` "none", "ntk" or "by_parts" with the
+    axes' extension ``factor`` and trained lengths ``original``."""
+    return Rotary(float(theta), *(int(v) for v in split), *(float(v) for v in scales),
+                  ROTARY_LAYOUTS[layout], ROTARY_SCALINGS[scaling], *(float(v) for v in factor),
+                  *(float(v) for v in original), float(beta_fast), float(beta_slow),
+                  float(magnitude), 0)
+
+
 def make_rope(theta, split, scales) -> Rope:
     d_t, d_h, d_w = (int(v) for v in split)
     s_t, s_h, s_w = (float(v) for v in scales)
@@ -121,6 +158,33 @@ def _declare(lib):
     lib.atlas_rope3d_batched.restype = ctypes.c_int
     lib.atlas_rope3d_batched.argtypes = [_vp, _vp, _i64, Grid3, _i32, _i32, ctypes.c_int,
                                          ctypes.POINTER(Rope), _vp]
+    lib.atlas_rotary_apply.restype = ctypes.c_int
+    lib.atlas_rotary_apply.argtypes = [ctypes.POINTER(RotaryTensor), _i32, _i64, Grid3,
+                                       ctypes.POINTER(Cube3), ctypes.c_int, _vp, _i32, _i32,
+                                       ctypes.c_int, ctypes.POINTER(Rotary), _vp]
+    lib.atlas_diff_lambda.restype = ctypes.c_int
+    lib.atlas_diff_lambda.argtypes = [_vp] * 4 + [_i32, _i32, ctypes.c_double, ctypes.c_int, _vp,
+                                                  _vp]
+    lib.atlas_diff_lambda_bwd.restype = ctypes.c_int
+    lib.atlas_diff_lambda_bwd.argtypes = [_vp] * 4 + [_i32, _i32, _vp, ctypes.c_int] + [_vp] * 5
+    lib.atlas_diff_attn.restype = ctypes.c_int
+    lib.atlas_diff_attn.argtypes = [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64,
+                                    ctypes.POINTER(AttnLayout), _i32, _i32, ctypes.c_float,
+                                    ctypes.c_int, _vp, _i32] + [_vp] * 6
+    lib.atlas_diff_attn_bwd.restype = ctypes.c_int
+    lib.atlas_diff_attn_bwd.argtypes = (
+        [_vp] * 6 + [_i64] + [_vp] * 6 + [_i64, ctypes.POINTER(AttnLayout), _i32, _i32,
+                                         ctypes.c_float, ctypes.c_int, _vp, _i32] + [_vp] * 10)
+    lib.atlas_diff_attn_bwd_workspace.restype = _i64
+    lib.atlas_diff_attn_bwd_workspace.argtypes = [_i64, _i64, _i64, _i32]
+    lib.atlas_group_norm.restype = ctypes.c_int
+    lib.atlas_group_norm.argtypes = [_vp] * 4 + [_i64, _i64, _i64, _i32, ctypes.c_double,
+                                                 ctypes.c_int, ctypes.c_int, _vp, _vp, _vp]
+    lib.atlas_group_norm_bwd.restype = ctypes.c_int
+    lib.atlas_group_norm_bwd.argtypes = [_vp] * 8 + [_i64, _i64, _i64, _i32, ctypes.c_int,
+                                                     ctypes.c_int, _vp, _vp]
+    lib.atlas_group_norm_workspace.restype = _i64
+    lib.atlas_group_norm_workspace.argtypes = [_i64, _i64, _i64, _i32, ctypes.c_int, _i32]
     lib.atlas_cube_window_offsets.restype = ctypes.c_int
     lib.atlas_cube_window_offsets.argtypes = [Grid3, Cube3, _vp, _i64, ctypes.POINTER(_i64)]
     lib.atlas_status_string.restype = ctypes.c_char_p
@@ -469,6 +533,271 @@ def rope3d_batched(src, dst, batch, grid, rope: Rope, stream=None):
                                     _dtype_code(src), ctypes.byref(rope), _stream(src, stream))
     _check(st, "atlas_rope3d_batched")
     return dst
+
+
+# ---------------------------------------------------------------------------
+# Differential-attention layer: rotary positions, attention, group norm.
+# These calls check shapes, types and devices here (the C-ABI cannot see
+# them), run on the tensors' device whatever the current one is, and take
+# `stream` as the stream of that device to enqueue on.
+# ---------------------------------------------------------------------------
+
+def _require(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _same_device(ref, *tensors):
+    """Every tensor (None skipped) on ref's CUDA device."""
+    _require(ref.is_cuda, "tensors must live on a CUDA device")
+    for t in tensors:
+        _require(t is None or t.device == ref.device, "tensors must live on one device")
+
+
+def _fp32(n, what, *tensors):
+    import torch
+    for t in tensors:
+        _require(t is None or (t.dtype == torch.float32 and t.numel() == n),
+                 f"{what}: fp32 of {n} elements expected")
+
+
+def _run(where, ref, stream, call):
+    """call(stream pointer) with ref's device current; raises on a status."""
+    import torch
+    if ref.device.index == torch.cuda.current_device():
+        _check(call(_stream(ref, stream)), where)
+        return
+    with torch.cuda.device(ref.device):
+        _check(call(_stream(ref, stream)), where)
+
+
+def _scratch(ref, stream, nbytes):
+    """A workspace whose memory goes back to the pool of the stream using it."""
+    import torch
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=ref.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=ref.device)
+
+
+def _work(workspace, ref, stream, nbytes):
+    """The caller's workspace once checked, or a new one."""
+    if workspace is None:
+        return _scratch(ref, stream, nbytes)
+    _same_device(ref, workspace)
+    _require(workspace.numel() * workspace.element_size() >= nbytes,
+             f"workspace of {nbytes} bytes expected")
+    return workspace
+
+
+def _rows(t):
+    """(pointer, row stride in elements) of [rows, heads, head_dim] whose rows
+    are contiguous, as a slice of a wider buffer's columns is."""
+    _require(t.is_cuda, "tensors must live on a CUDA device")
+    _require(t.dim() == 3 and (t.shape[2] == 1 or t.stride(2) == 1) and
+             (t.shape[1] == 1 or t.stride(1) == t.shape[2]),
+             "tensors must be [rows, heads, head_dim] with contiguous rows")
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return t.data_ptr(), stride
+
+
+def rotary(tensors, grid, rot: Rotary, *, cube=None, order="raster", positions=None,
+           transpose=False, batch=1, stream=None):
+    """Rotary positions of several tensors of the same tokens in one launch.
+
+    tensors: (src, dst) or (src, dst, rotate) of [batch*T*H*W, heads,
+    head_dim] each (the heads may differ; rows may be strided); rotate False
+    only moves the rows. order "reorder" / "unorder" also takes the rows from
+    raster to cube order or back (``cube``). positions: int32 [batch*T*H*W]
+    or [.., 1 or 3], by raster row, instead of the grid index. transpose
+    rotates back: the gradient's map. Returns the destinations."""
+    import torch
+    _require(len(tensors) > 0, "at least one tensor")
+    ref = tensors[0][0]
+    rows = int(batch) * grid[0] * grid[1] * grid[2]
+    items = (RotaryTensor * len(tensors))()
+    for item, t in zip(items, tensors):
+        src, dst = t[0], t[1]
+        _same_device(ref, src, dst)
+        _require(src.shape == dst.shape and src.shape[0] == rows and
+                 src.shape[2] == ref.shape[2], "rotary: src and dst of [batch*T*H*W, heads, "
+                 "head_dim], one head_dim for all")
+        _require(src.dtype == ref.dtype and dst.dtype == ref.dtype, "rotary: one dtype for all")
+        item.src, item.src_stride = _rows(src)
+        item.dst, item.dst_stride = _rows(dst)
+        item.heads, item.rotate = src.shape[1], int(bool(t[2]) if len(t) > 2 else True)
+    axes = 0
+    if positions is not None:
+        _same_device(ref, positions)
+        _require(positions.dtype == torch.int32 and positions.shape[0] == rows and
+                 positions.dim() <= 2, "rotary: positions are int32 [batch*T*H*W(, axes)]")
+        axes = positions.shape[1] if positions.dim() == 2 else 1
+    if bool(rot.transpose) != bool(transpose):
+        rot = Rotary.from_buffer_copy(rot)
+        rot.transpose = int(bool(transpose))
+    c = ctypes.byref(Cube3(*cube)) if cube is not None else None
+    _run("atlas_rotary_apply", ref, stream, lambda s: lib().atlas_rotary_apply(
+        items, len(tensors), int(batch), Grid3(*grid), c, ORDERS[order], _ptr(positions), axes,
+        ref.shape[2], _dtype_code(ref), ctypes.byref(rot), s))
+    return [t[1] for t in tensors]
+
+
+def diff_lambda(q1, k1, q2, k2, lambda_init, lam, stream=None):
+    """lam [n] = exp<q1,k1> - exp<q2,k2> + lambda_init from vectors [n, d]."""
+    _same_device(q1, k1, q2, k2, lam)
+    _require(q1.dim() == 2 and all(t.shape == q1.shape and t.dtype == q1.dtype
+                                   for t in (k1, q2, k2)), "diff_lambda: four [n, d] of one dtype")
+    _fp32(q1.shape[0], "diff_lambda lam", lam)
+    _run("atlas_diff_lambda", q1, stream, lambda s: lib().atlas_diff_lambda(
+        _ptr(q1), _ptr(k1), _ptr(q2), _ptr(k2), q1.shape[0], q1.shape[1], float(lambda_init),
+        _dtype_code(q1), _ptr(lam), s))
+    return lam
+
+
+def diff_lambda_bwd(q1, k1, q2, k2, dlam, dq1, dk1, dq2, dk2, stream=None):
+    """Gradients of ``diff_lambda``'s vectors from dlam [n]."""
+    _same_device(q1, k1, q2, k2, dlam, dq1, dk1, dq2, dk2)
+    _require(q1.dim() == 2 and all(t.shape == q1.shape and t.dtype == q1.dtype
+                                   for t in (k1, q2, k2, dq1, dk1, dq2, dk2)),
+             "diff_lambda_bwd: eight [n, d] of one dtype")
+    _fp32(q1.shape[0], "diff_lambda_bwd dlam", dlam)
+    _run("atlas_diff_lambda_bwd", q1, stream, lambda s: lib().atlas_diff_lambda_bwd(
+        _ptr(q1), _ptr(k1), _ptr(q2), _ptr(k2), q1.shape[0], q1.shape[1], _ptr(dlam),
+        _dtype_code(q1), _ptr(dq1), _ptr(dk1), _ptr(dq2), _ptr(dk2), s))
+    return dq1, dk1, dq2, dk2
+
+
+def _diff_sides(batch, detail, glob, window_offsets, global_window_offsets, window_len, lam):
+    """Shapes shared by diff_attn and its backward: (reference tensor, detail
+    rows and global rows of one problem, layout). None stands for no rows."""
+    import torch
+    ref = next((t for t in (*detail, *glob) if t is not None and t.shape[0] > 0), None)
+    _require(ref is not None and ref.dim() == 3 and int(batch) >= 1,
+             "diff_attn: [rows, heads, head_dim] tensors and batch >= 1")
+    counts = []
+    for side in (detail, glob):
+        n = side[0].shape[0] if side[0] is not None else 0
+        for t in side:
+            _require(n == 0 or t is None or (tuple(t.shape) == (n, *ref.shape[1:]) and
+                                             t.dtype == ref.dtype),
+                     "diff_attn: tensors of one side have one shape and dtype")
+        _require(n % int(batch) == 0, "diff_attn: rows are not a multiple of batch")
+        _same_device(ref, *(t for t in side if n > 0))
+        counts.append(n // int(batch))
+    _same_device(ref, lam, window_offsets, global_window_offsets)
+    _require(lam.numel() in (1, ref.shape[1]), "diff_attn: lam has one entry or one per head")
+    _fp32(lam.numel(), "diff_attn lam", lam)
+    for off in (window_offsets, global_window_offsets):
+        _require(off is None or (off.dtype == torch.int32 and off.numel() >= 2),
+                 "diff_attn: offsets are int32 [n_windows + 1]")
+    if window_offsets is not None and global_window_offsets is not None:
+        _require(window_offsets.numel() == global_window_offsets.numel(),
+                 "diff_attn: one global range per window")
+    first = window_offsets if window_offsets is not None else global_window_offsets
+    address = lambda t: _ptr(t).value if t is not None else None
+    ly = AttnLayout(int(batch), int(window_len), address(window_offsets),
+                    first.numel() - 1 if first is not None else 0, address(global_window_offsets))
+    return ref, counts[0], counts[1], ly
+
+
+def diff_attn(q_d, k_d, v_d, q_g, k_g, v_g, lam, o_d, o_g, s_d=None, s_g=None, lse=None, *,
+              batch=1, window_len=0, window_offsets=None, global_window_offsets=None,
+              softmax_scale: float = 0.0, stream=None):
+    """Differential attention o = (softmax(q1 k1) - lam softmax(q2 k2)) v over
+    the layouts of ``local_global_attn_ex``; the halves of a head are the two
+    maps. lam: fp32, one entry or one per head. For ``diff_attn_bwd`` pass s_d
+    and s_g (the second map's output) and lse (fp32 [batch, heads, 2, N+G])."""
+    ref, n_d, n_g, ly = _diff_sides(batch, (q_d, k_d, v_d, o_d, s_d), (q_g, k_g, v_g, o_g, s_g),
+                                    window_offsets, global_window_offsets, window_len, lam)
+    heads, hd = ref.shape[1], ref.shape[2]
+    _same_device(ref, lse)
+    _fp32(2 * int(batch) * heads * (n_d + n_g), "diff_attn lse", lse)
+    nz = lambda t, n: _ptr(t) if n > 0 else None
+    _run("atlas_diff_attn", ref, stream, lambda s: lib().atlas_diff_attn(
+        nz(q_d, n_d), nz(k_d, n_d), nz(v_d, n_d), n_d, nz(q_g, n_g), nz(k_g, n_g), nz(v_g, n_g),
+        n_g, ctypes.byref(ly), heads, hd, float(softmax_scale), _dtype_code(ref), _ptr(lam),
+        lam.numel(), nz(o_d, n_d), nz(o_g, n_g), nz(s_d, n_d), nz(s_g, n_g), _ptr(lse), s))
+    return o_d, o_g
+
+
+def diff_attn_bwd(q_d, k_d, v_d, o_d, s_d, do_d, q_g, k_g, v_g, o_g, s_g, do_g, lam, lse,
+                  dq_d, dk_d, dv_d, dq_g, dk_g, dv_g, dlam, workspace=None, *, batch=1,
+                  window_len=0, window_offsets=None, global_window_offsets=None,
+                  softmax_scale: float = 0.0, stream=None):
+    """Gradients of ``diff_attn`` (same layout arguments): dq_*, dk_*, dv_* and
+    dlam (as lam). workspace: any dtype, of at least
+    ``diff_attn_bwd_workspace`` bytes; allocated here when not given."""
+    ref, n_d, n_g, ly = _diff_sides(
+        batch, (q_d, k_d, v_d, o_d, s_d, do_d, dq_d, dk_d, dv_d),
+        (q_g, k_g, v_g, o_g, s_g, do_g, dq_g, dk_g, dv_g), window_offsets, global_window_offsets,
+        window_len, lam)
+    heads, hd = ref.shape[1], ref.shape[2]
+    _same_device(ref, lse, dlam)
+    _fp32(2 * int(batch) * heads * (n_d + n_g), "diff_attn_bwd lse", lse)
+    _fp32(lam.numel(), "diff_attn_bwd dlam", dlam)
+    work = _work(workspace, ref, stream, diff_attn_bwd_workspace(batch, n_d, n_g, heads))
+    nz = lambda t, n: _ptr(t) if n > 0 else None
+    _run("atlas_diff_attn_bwd", ref, stream, lambda s: lib().atlas_diff_attn_bwd(
+        nz(q_d, n_d), nz(k_d, n_d), nz(v_d, n_d), nz(o_d, n_d), nz(s_d, n_d), nz(do_d, n_d), n_d,
+        nz(q_g, n_g), nz(k_g, n_g), nz(v_g, n_g), nz(o_g, n_g), nz(s_g, n_g), nz(do_g, n_g), n_g,
+        ctypes.byref(ly), heads, hd, float(softmax_scale), _dtype_code(ref), _ptr(lam),
+        lam.numel(), _ptr(lse), _ptr(work), nz(dq_d, n_d), nz(dk_d, n_d), nz(dv_d, n_d),
+        nz(dq_g, n_g), nz(dk_g, n_g), nz(dv_g, n_g), _ptr(dlam), s))
+    return dq_d, dk_d, dv_d, dq_g, dk_g, dv_g, dlam
+
+
+def diff_attn_bwd_workspace(batch, n_detail, n_global, heads) -> int:
+    """Bytes of ``diff_attn_bwd``'s workspace (rows of one problem)."""
+    return int(lib().atlas_diff_attn_bwd_workspace(int(batch), int(n_detail), int(n_global),
+                                                   int(heads)))
+
+
+def _norm_sizes(x, rows, groups, tensors, vectors, stats):
+    _require(x.dim() == 2 and int(rows) >= 1 and x.shape[0] % int(rows) == 0,
+             "group_norm: x is [samples*rows, channels]")
+    _same_device(x, *tensors, *vectors, stats)
+    _require(all(t.shape == x.shape and t.dtype == x.dtype for t in tensors),
+             "group_norm: tensors of x's shape and dtype")
+    _fp32(x.shape[1], "group_norm gamma and beta", *vectors)
+    samples = x.shape[0] // int(rows)
+    _fp32(2 * samples * int(groups), "group_norm stats", stats)
+    return samples
+
+
+def group_norm(x, gamma, beta, y, rows, groups, *, eps=1e-5, activation="none", stats=None,
+               workspace=None, stream=None):
+    """y = act(group norm of x [samples*rows, channels]); a sample is ``rows``
+    consecutive rows (rows 1, groups = heads: each head of a token by itself).
+    gamma, beta: fp32 [channels] or None. stats: fp32 [samples, groups, 2],
+    needed by ``group_norm_bwd``. activation "none" or "silu"."""
+    samples = _norm_sizes(x, rows, groups, (y,), (gamma, beta), stats)
+    work = _work(workspace, x, stream, group_norm_workspace(x, rows, groups, False))
+    _run("atlas_group_norm", x, stream, lambda s: lib().atlas_group_norm(
+        _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), samples, int(rows), x.shape[1], int(groups),
+        float(eps), ACTIVATIONS[activation], _dtype_code(x), _ptr(stats), _ptr(work), s))
+    return y
+
+
+def group_norm_bwd(dy, x, gamma, beta, stats, dx, dgamma, dbeta, rows, groups, *,
+                   activation="none", workspace=None, stream=None):
+    """dx, and dgamma and dbeta (fp32 [channels], or None), of ``group_norm``
+    from dy and the forward's x and stats."""
+    _require(stats is not None, "group_norm_bwd: the forward's stats")
+    samples = _norm_sizes(x, rows, groups, (dy, dx), (gamma, beta, dgamma, dbeta), stats)
+    work = _work(workspace, x, stream, group_norm_workspace(x, rows, groups, True))
+    _run("atlas_group_norm_bwd", x, stream, lambda s: lib().atlas_group_norm_bwd(
+        _ptr(dy), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(stats), _ptr(dx), _ptr(dgamma),
+        _ptr(dbeta), samples, int(rows), x.shape[1], int(groups), ACTIVATIONS[activation],
+        _dtype_code(x), _ptr(work), s))
+    return dx, dgamma, dbeta
+
+
+def group_norm_workspace(x, rows, groups, backward) -> int:
+    """Bytes of the workspace of ``group_norm`` or ``group_norm_bwd``."""
+    return int(lib().atlas_group_norm_workspace(x.shape[0] // int(rows), int(rows), x.shape[1],
+                                                int(groups), _dtype_code(x), int(bool(backward))))
 
 
 def last_device_error(stream=None) -> int:

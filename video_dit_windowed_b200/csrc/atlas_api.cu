@@ -648,6 +648,403 @@ ATLAS_API atlas_status atlas_out_proj_unorder(const void *o, const void *w, int6
     return atlas::launch_out_proj(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+namespace atlas {
+namespace {
+
+// Rows of `width` bytes, `stride` bytes apart.
+struct Strided {
+    uintptr_t at;
+    int64_t rows, width, stride;
+};
+Strided strided(const void *p, int64_t rows, int64_t width, int64_t stride, int eb) {
+    return {reinterpret_cast<uintptr_t>(p), rows, width * eb, (stride ? stride : width) * eb};
+}
+bool strided_overlap(const Strided &a, const Strided &b) {
+    const uintptr_t a_end = a.at + static_cast<uintptr_t>(a.stride * (a.rows - 1) + a.width);
+    const uintptr_t b_end = b.at + static_cast<uintptr_t>(b.stride * (b.rows - 1) + b.width);
+    if (a.at >= b_end || b.at >= a_end) return false;
+    // Interleaved rows of one buffer: equal strides and disjoint columns.
+    if (a.stride == b.stride) {
+        const int64_t s = a.stride;
+        int64_t d = static_cast<int64_t>(b.at - a.at) % s;
+        if (d < 0) d += s;
+        if (d >= a.width && d + b.width <= s) return false;
+    }
+    return true;
+}
+
+atlas_status check_rotary(const atlas_rotary &r, int32_t head_dim) {
+    const int32_t d[3] = {r.d_t, r.d_h, r.d_w};
+    for (int i = 0; i < 3; ++i)
+        if (d[i] < 0 || d[i] > head_dim || (d[i] & 1)) return ATLAS_ERR_UNSUPPORTED;
+    if (d[0] + d[1] + d[2] > head_dim) return ATLAS_ERR_UNSUPPORTED;
+    if (!(r.theta > 0.0) || !std::isfinite(r.theta) || !std::isfinite(r.magnitude))
+        return ATLAS_ERR_UNSUPPORTED;
+    if (!std::isfinite(r.scale_t) || !std::isfinite(r.scale_h) || !std::isfinite(r.scale_w))
+        return ATLAS_ERR_UNSUPPORTED;
+    if (r.layout != ATLAS_ROTARY_INTERLEAVED && r.layout != ATLAS_ROTARY_HALF)
+        return ATLAS_ERR_UNSUPPORTED;
+    if (r.scaling == ATLAS_ROTARY_PLAIN) return ATLAS_OK;
+    if (r.scaling != ATLAS_ROTARY_NTK && r.scaling != ATLAS_ROTARY_BY_PARTS)
+        return ATLAS_ERR_UNSUPPORTED;
+    const double factor[3] = {r.factor_t, r.factor_h, r.factor_w};
+    const double original[3] = {r.original_t, r.original_h, r.original_w};
+    for (int i = 0; i < 3; ++i) {
+        if (d[i] == 0) continue;
+        if (!(factor[i] >= 1.0) || !std::isfinite(factor[i])) return ATLAS_ERR_UNSUPPORTED;
+        if (r.scaling == ATLAS_ROTARY_BY_PARTS &&
+            (!(original[i] > 0.0) || !std::isfinite(original[i])))
+            return ATLAS_ERR_UNSUPPORTED;
+    }
+    if (r.scaling == ATLAS_ROTARY_BY_PARTS &&
+        (!(r.beta_fast > r.beta_slow) || !std::isfinite(r.beta_fast) ||
+         !std::isfinite(r.beta_slow)))
+        return ATLAS_ERR_UNSUPPORTED;
+    return ATLAS_OK;
+}
+
+}  // namespace
+}  // namespace atlas
+
+ATLAS_API atlas_status atlas_rotary_apply(const atlas_rotary_tensor *tensors, int32_t n_tensors,
+                                          int64_t batch, atlas_grid3 grid,
+                                          const atlas_cube3 *cube, atlas_order order,
+                                          const int32_t *positions, int32_t n_axes,
+                                          int32_t head_dim, atlas_dtype dtype,
+                                          const atlas_rotary *rot, atlas_stream_t stream) {
+    ATLAS_TRACE();
+    if (!tensors || !rot) return ATLAS_ERR_NULL;
+    if (n_tensors < 1 || n_tensors > kRotaryMaxTensors) return ATLAS_ERR_SHAPE;
+    atlas_status st = check_grid(grid, 1, head_dim, dtype);
+    if (st != ATLAS_OK) return st;
+    if (head_dim > kRotaryMaxHeadDim) return ATLAS_ERR_UNSUPPORTED;
+    if (order != ATLAS_ORDER_RASTER && order != ATLAS_ORDER_REORDER &&
+        order != ATLAS_ORDER_UNORDER)
+        return ATLAS_ERR_UNSUPPORTED;
+    if (order != ATLAS_ORDER_RASTER) {
+        if (!cube) return ATLAS_ERR_NULL;
+        if ((st = check_cube(grid, *cube)) != ATLAS_OK) return st;
+    }
+    const int64_t n = grid.T * grid.H * grid.W;
+    if (batch < 1 || batch > kMaxRows || n > kMaxRows / batch) return ATLAS_ERR_SHAPE;
+    if ((st = check_rotary(*rot, head_dim)) != ATLAS_OK) return st;
+    if (positions) {
+        if (n_axes != 3 && (n_axes != 1 || rot->d_h != 0 || rot->d_w != 0))
+            return ATLAS_ERR_UNSUPPORTED;
+        if (reinterpret_cast<uintptr_t>(positions) & 3u) return ATLAS_ERR_ALIGN;
+    }
+    const int64_t rows = batch * n;
+    const int eb = elem_bytes(dtype);
+    for (int i = 0; i < n_tensors; ++i) {
+        const atlas_rotary_tensor &x = tensors[i];
+        if (!x.src || !x.dst) return ATLAS_ERR_NULL;
+        if (x.heads < 1 || x.heads > 65535) return ATLAS_ERR_SHAPE;
+        const int64_t width = static_cast<int64_t>(x.heads) * head_dim;
+        for (int64_t s : {x.src_stride, x.dst_stride}) {
+            if (s != 0 && (s < width || s > (1ll << 40))) return ATLAS_ERR_SHAPE;
+            if (s * eb % 16 != 0) return ATLAS_ERR_ALIGN;
+        }
+        if (!aligned16(x.src) || !aligned16(x.dst)) return ATLAS_ERR_ALIGN;
+    }
+    for (int i = 0; i < n_tensors; ++i) {
+        const atlas_rotary_tensor &x = tensors[i];
+        const Strided dst = strided(x.dst, rows, static_cast<int64_t>(x.heads) * head_dim,
+                                    x.dst_stride, eb);
+        if (positions && strided_overlap(dst, {reinterpret_cast<uintptr_t>(positions), 1,
+                                               rows * n_axes * 4, rows * n_axes * 4}))
+            return ATLAS_ERR_ALIAS;
+        for (int j = 0; j < n_tensors; ++j) {
+            const atlas_rotary_tensor &y = tensors[j];
+            const int64_t width = static_cast<int64_t>(y.heads) * head_dim;
+            if (j != i && strided_overlap(dst, strided(y.dst, rows, width, y.dst_stride, eb)))
+                return ATLAS_ERR_ALIAS;
+            const Strided src = strided(y.src, rows, width, y.src_stride, eb);
+            const bool in_place = j == i && order == ATLAS_ORDER_RASTER && src.at == dst.at &&
+                                  src.stride == dst.stride;
+            if (!in_place && strided_overlap(dst, src)) return ATLAS_ERR_ALIAS;
+        }
+    }
+    RotaryArgs a{tensors, n_tensors, batch, grid.T, grid.H, grid.W,
+                 cube ? cube->ct : 1, cube ? cube->ch : 1, cube ? cube->cw : 1,
+                 order, positions, n_axes, head_dim, eb, rot};
+    if (order == ATLAS_ORDER_RASTER) a.ct = a.ch = a.cw = 1;
+    return launch_rotary(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace atlas {
+namespace {
+
+bool aligned_to(const void *p, int bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) == 0;
+}
+
+atlas_status diff_lambda(DiffLambdaArgs a, atlas_dtype dtype, bool bwd, atlas_stream_t stream) {
+    const void *scalars = bwd ? static_cast<const void *>(a.dlambda) : a.lambda;
+    if (!scalars) return ATLAS_ERR_NULL;
+    for (int i = 0; i < 4; ++i)
+        if (!a.v[i] || (bwd && !a.dv[i])) return ATLAS_ERR_NULL;
+    if (a.n < 1 || a.d < 1) return ATLAS_ERR_SHAPE;
+    const int eb = elem_bytes(dtype);
+    if (eb == 0 || !std::isfinite(a.init)) return ATLAS_ERR_UNSUPPORTED;
+    if (!aligned_to(scalars, 4)) return ATLAS_ERR_ALIGN;
+    for (int i = 0; i < 4; ++i)
+        if (!aligned_to(a.v[i], eb) || (bwd && !aligned_to(a.dv[i], eb))) return ATLAS_ERR_ALIGN;
+    const size_t bytes = static_cast<size_t>(a.n) * a.d * eb, small = sizeof(float) * a.n;
+    Span all[9];
+    int n = 0;
+    all[n++] = {scalars, small};
+    if (bwd)
+        for (int i = 0; i < 4; ++i) all[n++] = {a.dv[i], bytes};
+    for (int i = 0; i < 4; ++i) all[n++] = {a.v[i], bytes};
+    for (int i = bwd ? 1 : 0; i < (bwd ? 5 : 1); ++i)
+        if (overlaps_any(all[i], all, n)) return ATLAS_ERR_ALIAS;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return ATLAS_ERR_DEVICE;
+    a.elem_bytes = eb;
+    return launch_diff_lambda(a, bwd, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// What atlas_diff_attn and its backward pass share: atlas_local_global_attn_ex's
+// checks, the two maps' softmax scale, and lambda.
+atlas_status diff_layout(const void *q_d, const void *k_d, const void *v_d, int64_t n_detail,
+                         const void *q_g, const void *k_g, const void *v_g, int64_t n_global,
+                         const atlas_attn_layout *layout, int32_t heads, int32_t head_dim,
+                         float softmax_scale, atlas_dtype dtype, const float *lambda,
+                         int32_t n_lambda, DiffArgs *d, size_t *bd, size_t *bg) {
+    if (!layout || !lambda) return ATLAS_ERR_NULL;
+    if (!(softmax_scale > 0.f) && head_dim > 1)
+        softmax_scale = 1.f / std::sqrt(static_cast<float>(head_dim / 2));
+    if (!std::isfinite(softmax_scale)) return ATLAS_ERR_UNSUPPORTED;
+    atlas_status st = attn_layout(q_d, k_d, v_d, n_detail, q_g, k_g, v_g, n_global, *layout, heads,
+                                  head_dim, softmax_scale, dtype, &d->attn, bd, bg);
+    if (st != ATLAS_OK) return st;
+    if (n_lambda != 1 && n_lambda != heads) return ATLAS_ERR_SHAPE;
+    if (!aligned_to(lambda, 4)) return ATLAS_ERR_ALIGN;
+    d->lambda = lambda;
+    d->n_lambda = n_lambda;
+    d->elem_bytes = elem_bytes(dtype);
+    return ATLAS_OK;
+}
+
+// The offset arrays a call reads, as spans.
+int layout_spans(const DiffArgs &d, Span *out) {
+    const AttnArgs &a = d.attn;
+    int n = 0;
+    out[n++] = {d.lambda, sizeof(float) * static_cast<size_t>(d.n_lambda)};
+    if (a.win_off) out[n++] = {a.win_off, 4 * static_cast<size_t>(a.n_win + 1)};
+    if (a.gwin_off) out[n++] = {a.gwin_off, 4 * static_cast<size_t>(a.n_gwin + 1)};
+    return n;
+}
+
+size_t diff_lse_bytes(const AttnArgs &a) {
+    return 2 * sizeof(float) * static_cast<size_t>(a.batch) * a.heads *
+           static_cast<size_t>(a.n_detail + a.n_global);
+}
+
+}  // namespace
+}  // namespace atlas
+
+ATLAS_API atlas_status atlas_diff_lambda(const void *q1, const void *k1, const void *q2,
+                                         const void *k2, int32_t n, int32_t d,
+                                         double lambda_init, atlas_dtype dtype, float *lambda,
+                                         atlas_stream_t stream) {
+    ATLAS_TRACE();
+    return diff_lambda(DiffLambdaArgs{{q1, k1, q2, k2}, {}, nullptr, lambda, lambda_init, n, d, 0},
+                       dtype, false, stream);
+}
+
+ATLAS_API atlas_status atlas_diff_lambda_bwd(const void *q1, const void *k1, const void *q2,
+                                             const void *k2, int32_t n, int32_t d,
+                                             const float *dlambda, atlas_dtype dtype, void *dq1,
+                                             void *dk1, void *dq2, void *dk2,
+                                             atlas_stream_t stream) {
+    ATLAS_TRACE();
+    return diff_lambda(DiffLambdaArgs{{q1, k1, q2, k2}, {dq1, dk1, dq2, dk2}, dlambda, nullptr,
+                                      0.0, n, d, 0},
+                       dtype, true, stream);
+}
+
+ATLAS_API atlas_status atlas_diff_attn(const void *q_d, const void *k_d, const void *v_d,
+                                       int64_t n_detail, const void *q_g, const void *k_g,
+                                       const void *v_g, int64_t n_global,
+                                       const atlas_attn_layout *layout, int32_t heads,
+                                       int32_t head_dim, float softmax_scale, atlas_dtype dtype,
+                                       const float *lambda, int32_t n_lambda, void *o_d,
+                                       void *o_g, void *s_d, void *s_g, float *lse,
+                                       atlas_stream_t stream) {
+    ATLAS_TRACE();
+    DiffArgs d{};
+    size_t bd = 0, bg = 0;
+    atlas_status st = diff_layout(q_d, k_d, v_d, n_detail, q_g, k_g, v_g, n_global, layout, heads,
+                                  head_dim, softmax_scale, dtype, lambda, n_lambda, &d, &bd, &bg);
+    if (st != ATLAS_OK) return st;
+    if ((n_detail > 0 && !o_d) || (n_global > 0 && !o_g)) return ATLAS_ERR_NULL;
+    if (n_detail > 0 && n_global > 0 && !s_d != !s_g) return ATLAS_ERR_NULL;
+    const void *outs[] = {o_d, o_g, s_d, s_g};
+    for (const void *p : outs)
+        if (p && !aligned16(p)) return ATLAS_ERR_ALIGN;
+    if (lse && !aligned_to(lse, 4)) return ATLAS_ERR_ALIGN;
+    Span all[14] = {{o_d, bd}, {o_g, bg}, {s_d, bd}, {s_g, bg}, {lse, diff_lse_bytes(d.attn)},
+                    {q_d, bd}, {k_d, bd}, {v_d, bd}, {q_g, bg}, {k_g, bg}, {v_g, bg}};
+    const int n = 11 + layout_spans(d, all + 11);
+    for (int i = 0; i < 5; ++i)
+        if (overlaps_any(all[i], all, n)) return ATLAS_ERR_ALIAS;
+    if (n_detail + n_global == 0) return ATLAS_OK;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return ATLAS_ERR_DEVICE;
+    d.attn.o_d = o_d;
+    d.attn.o_g = o_g;
+    d.attn.lse = lse;
+    d.s_d = s_d;
+    d.s_g = s_g;
+    return launch_diff_attn_simt(d, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ATLAS_API int64_t atlas_diff_attn_bwd_workspace(int64_t batch, int64_t n_detail,
+                                                int64_t n_global, int32_t heads) {
+    if (batch < 1 || batch > kMaxRows || n_detail < 0 || n_global < 0 ||
+        n_detail > kMaxRows / batch || n_global > kMaxRows / batch || heads < 1 || heads > 65535)
+        return 0;
+    return 4 * (2 * batch * heads * (n_detail + n_global) +
+                static_cast<int64_t>(heads) * kDiffLambdaParts);
+}
+
+ATLAS_API atlas_status atlas_diff_attn_bwd(
+    const void *q_d, const void *k_d, const void *v_d, const void *o_d, const void *s_d,
+    const void *do_d, int64_t n_detail, const void *q_g, const void *k_g, const void *v_g,
+    const void *o_g, const void *s_g, const void *do_g, int64_t n_global,
+    const atlas_attn_layout *layout, int32_t heads, int32_t head_dim, float softmax_scale,
+    atlas_dtype dtype, const float *lambda, int32_t n_lambda, const float *lse, void *workspace,
+    void *dq_d, void *dk_d, void *dv_d, void *dq_g, void *dk_g, void *dv_g, float *dlambda,
+    atlas_stream_t stream) {
+    ATLAS_TRACE();
+    DiffArgs d{};
+    size_t bd = 0, bg = 0;
+    atlas_status st = diff_layout(q_d, k_d, v_d, n_detail, q_g, k_g, v_g, n_global, layout, heads,
+                                  head_dim, softmax_scale, dtype, lambda, n_lambda, &d, &bd, &bg);
+    if (st != ATLAS_OK) return st;
+    if (!lse || !workspace || !dlambda) return ATLAS_ERR_NULL;
+    const void *side_d[] = {o_d, s_d, do_d, dq_d, dk_d, dv_d};
+    const void *side_g[] = {o_g, s_g, do_g, dq_g, dk_g, dv_g};
+    for (int i = 0; i < 6; ++i) {
+        if ((n_detail > 0 && !side_d[i]) || (n_global > 0 && !side_g[i])) return ATLAS_ERR_NULL;
+        if ((side_d[i] && !aligned16(side_d[i])) || (side_g[i] && !aligned16(side_g[i])))
+            return ATLAS_ERR_ALIGN;
+    }
+    if (!aligned16(workspace) || !aligned_to(lse, 4) || !aligned_to(dlambda, 4))
+        return ATLAS_ERR_ALIGN;
+    const size_t bw = static_cast<size_t>(
+        atlas_diff_attn_bwd_workspace(layout->batch, n_detail, n_global, heads));
+    Span all[24] = {{dq_d, bd}, {dk_d, bd}, {dv_d, bd}, {dq_g, bg}, {dk_g, bg}, {dv_g, bg},
+                    {workspace, bw}, {dlambda, sizeof(float) * static_cast<size_t>(n_lambda)},
+                    {lse, diff_lse_bytes(d.attn)},
+                    {q_d, bd}, {k_d, bd}, {v_d, bd}, {o_d, bd}, {s_d, bd}, {do_d, bd},
+                    {q_g, bg}, {k_g, bg}, {v_g, bg}, {o_g, bg}, {s_g, bg}, {do_g, bg}};
+    const int n = 21 + layout_spans(d, all + 21);
+    for (int i = 0; i < 8; ++i)
+        if (overlaps_any(all[i], all, n)) return ATLAS_ERR_ALIAS;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return ATLAS_ERR_DEVICE;
+    d.attn.o_d = const_cast<void *>(o_d);
+    d.attn.o_g = const_cast<void *>(o_g);
+    d.attn.lse = const_cast<float *>(lse);
+    d.s_d = const_cast<void *>(s_d);
+    d.s_g = const_cast<void *>(s_g);
+    float *delta = static_cast<float *>(workspace);
+    const int64_t rows = layout->batch * (n_detail + n_global);
+    DiffBwdArgs b{d, do_d, do_g, delta, delta + 2 * rows * heads, dq_d, dk_d, dv_d,
+                  dq_g, dk_g, dv_g, dlambda};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (rows > 0) {
+        if ((st = launch_diff_bwd_delta(b, s)) != ATLAS_OK) return st;
+        if ((st = launch_diff_bwd_simt(b, s)) != ATLAS_OK) return st;
+    }
+    return launch_diff_dlambda(b, s);
+}
+
+namespace atlas {
+namespace {
+
+// Checks of the group norm's calls; a.out, a.x (and, backward, a.dy) are set.
+atlas_status group_norm(NormArgs a, atlas_dtype dtype, bool bwd, atlas_stream_t stream) {
+    if (!a.x || !a.out || (bwd && (!a.dy || !a.stats))) return ATLAS_ERR_NULL;
+    if (a.samples < 1 || a.rows < 1 || a.channels < 1 || a.groups < 1 ||
+        a.channels % a.groups != 0 || a.channels > kMaxRows || a.samples > kMaxRows ||
+        a.rows > kMaxRows / a.samples || a.groups > kMaxRows / a.samples)
+        return ATLAS_ERR_SHAPE;
+    a.elem_bytes = elem_bytes(dtype);
+    if (a.elem_bytes == 0 || (a.act != ATLAS_ACT_NONE && a.act != ATLAS_ACT_SILU) ||
+        !(a.eps >= 0.0) || !std::isfinite(a.eps))
+        return ATLAS_ERR_UNSUPPORTED;
+    const size_t need = static_cast<size_t>(group_norm_workspace(a, bwd));
+    if (need && !a.workspace) return ATLAS_ERR_NULL;
+    const void *floats[] = {a.gamma, a.beta, a.stats, a.dgamma, a.dbeta};
+    for (const void *p : floats)
+        if (p && !aligned_to(p, 4)) return ATLAS_ERR_ALIGN;
+    const void *tensors[] = {a.x, a.dy, a.out, a.workspace};
+    for (const void *p : tensors)
+        if (p && !aligned16(p)) return ATLAS_ERR_ALIGN;
+    const size_t bytes = static_cast<size_t>(a.samples * a.rows) * a.channels * a.elem_bytes;
+    const size_t bc = sizeof(float) * static_cast<size_t>(a.channels);
+    const size_t bs = 2 * sizeof(float) * static_cast<size_t>(a.samples) * a.groups;
+    const Span all[] = {{a.out, bytes}, {a.workspace, need}, {a.dgamma, bc}, {a.dbeta, bc},
+                        {a.stats, bs}, {a.x, bytes}, {a.dy, bytes}, {a.gamma, bc}, {a.beta, bc}};
+    // Written: out, the workspace, dgamma, dbeta, and stats in the forward
+    // pass. out may be exactly x or dy.
+    for (int i = 0; i < (bwd ? 4 : 5); ++i)
+        for (int j = 0; j < 9; ++j) {
+            if (i == j || !all[i].p || !all[i].bytes || !all[j].p || !all[j].bytes) continue;
+            if (i == 0 && j >= 5 && j <= 6 && all[j].p == a.out) continue;
+            if (ranges_overlap(all[i].p, all[i].bytes, all[j].p, all[j].bytes))
+                return ATLAS_ERR_ALIAS;
+        }
+    DeviceInfo dev;
+    if (!current_device(&dev)) return ATLAS_ERR_DEVICE;
+    return launch_group_norm(a, bwd, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+}  // namespace atlas
+
+ATLAS_API atlas_status atlas_group_norm(const void *x, const float *gamma, const float *beta,
+                                        void *y, int64_t samples, int64_t rows, int64_t channels,
+                                        int32_t groups, double eps, atlas_activation act,
+                                        atlas_dtype dtype, float *stats, void *workspace,
+                                        atlas_stream_t stream) {
+    ATLAS_TRACE();
+    return group_norm(NormArgs{x, nullptr, y, gamma, beta, stats, nullptr, nullptr, samples, rows,
+                               channels, groups, eps, act, 0, workspace},
+                      dtype, false, stream);
+}
+
+ATLAS_API atlas_status atlas_group_norm_bwd(const void *dy, const void *x, const float *gamma,
+                                            const float *beta, const float *stats, void *dx,
+                                            float *dgamma, float *dbeta, int64_t samples,
+                                            int64_t rows, int64_t channels, int32_t groups,
+                                            atlas_activation act, atlas_dtype dtype,
+                                            void *workspace, atlas_stream_t stream) {
+    ATLAS_TRACE();
+    return group_norm(NormArgs{x, dy, dx, gamma, beta, const_cast<float *>(stats), dgamma, dbeta,
+                               samples, rows, channels, groups, 0.0, act, 0, workspace},
+                      dtype, true, stream);
+}
+
+ATLAS_API int64_t atlas_group_norm_workspace(int64_t samples, int64_t rows, int64_t channels,
+                                             int32_t groups, atlas_dtype dtype,
+                                             int32_t backward) {
+    if (samples < 1 || rows < 1 || channels < 1 || groups < 1 || channels % groups != 0 ||
+        channels > kMaxRows || samples > kMaxRows || rows > kMaxRows / samples ||
+        groups > kMaxRows / samples || elem_bytes(dtype) == 0)
+        return 0;
+    NormArgs a{};
+    a.samples = samples;
+    a.rows = rows;
+    a.channels = channels;
+    a.groups = groups;
+    a.elem_bytes = elem_bytes(dtype);
+    return group_norm_workspace(a, backward != 0);
+}
+
 ATLAS_API atlas_status atlas_aligned_global_cube(atlas_grid3 grid, atlas_cube3 cube,
                                                  atlas_grid3 global_grid,
                                                  atlas_cube3 *global_cube) {

@@ -160,4 +160,69 @@ atlas_status launch_attn_bwd_delta(const AttnBwdArgs &a, cudaStream_t stream);
 atlas_status launch_attn_bwd_simt_f32(const AttnBwdArgs &a, cudaStream_t stream);
 atlas_status launch_attn_bwd_tc_bf16(const AttnBwdArgs &a, cudaStream_t stream);
 
+// Rotary positions (rotary.cu).
+constexpr int kRotaryMaxTensors = 8;
+constexpr int kRotaryMaxHeadDim = 512;
+struct RotaryArgs {
+    const atlas_rotary_tensor *tensors;
+    int32_t n_tensors;
+    int64_t batch, T, H, W;
+    int32_t ct, ch, cw;
+    int32_t order;              // atlas_order
+    const int32_t *positions;   // NULL: the grid index
+    int32_t n_axes;
+    int32_t head_dim, elem_bytes;
+    const atlas_rotary *rot;
+};
+atlas_status launch_rotary(const RotaryArgs &a, cudaStream_t stream);
+
+// Differential attention (diff_attn.cu): attn.o_* receive (or, in the
+// backward pass, hold) o, s_* the second map's output; attn.lse is [batch,
+// heads, 2, N+G].
+struct DiffArgs {
+    AttnArgs attn;
+    const float *lambda;
+    int32_t n_lambda;
+    void *s_d, *s_g;            // may be NULL in the forward pass
+    int elem_bytes;
+};
+struct DiffBwdArgs {
+    DiffArgs fwd;
+    const void *do_d, *do_g;
+    float *delta;               // [batch, heads, 2, N+G]: D_1, D_2
+    float *part;                // [heads, kDiffLambdaParts]
+    void *dq_d, *dk_d, *dv_d, *dq_g, *dk_g, *dv_g;
+    float *dlambda;
+};
+struct DiffLambdaArgs {
+    const void *v[4];           // q1, k1, q2, k2 [n, d]
+    void *dv[4];
+    const float *dlambda;
+    float *lambda;
+    double init;
+    int32_t n, d, elem_bytes;
+};
+constexpr int kDiffLambdaParts = 64;
+atlas_status launch_diff_lambda(const DiffLambdaArgs &a, bool bwd, cudaStream_t stream);
+atlas_status launch_diff_attn_simt(const DiffArgs &a, cudaStream_t stream);
+atlas_status launch_diff_bwd_delta(const DiffBwdArgs &a, cudaStream_t stream);
+atlas_status launch_diff_dlambda(const DiffBwdArgs &a, cudaStream_t stream);
+atlas_status launch_diff_bwd_simt(const DiffBwdArgs &a, cudaStream_t stream);
+
+// Group norm (group_norm.cu).
+struct NormArgs {
+    const void *x, *dy;         // dy: backward only
+    void *out;                  // y or dx
+    const float *gamma, *beta;
+    float *stats;               // forward: may be NULL
+    float *dgamma, *dbeta;      // backward, may be NULL
+    int64_t samples, rows, channels;
+    int32_t groups;
+    double eps;
+    int32_t act, elem_bytes;
+    void *workspace;
+};
+int64_t group_norm_workspace(const NormArgs &a, bool bwd);
+atlas_status launch_group_norm(const NormArgs &a, bool bwd, cudaStream_t stream);
+
 }  // namespace atlas
