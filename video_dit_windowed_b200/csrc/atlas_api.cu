@@ -897,7 +897,8 @@ ATLAS_API atlas_status atlas_diff_attn(const void *q_d, const void *k_d, const v
     d.attn.lse = lse;
     d.s_d = s_d;
     d.s_g = s_g;
-    return launch_diff_attn_simt(d, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == ATLAS_BF16 ? launch_diff_attn_tc(d, cs) : launch_diff_attn_simt(d, cs);
 }
 
 ATLAS_API int64_t atlas_diff_attn_bwd_workspace(int64_t batch, int64_t n_detail,

@@ -204,6 +204,7 @@ struct DiffLambdaArgs {
 };
 constexpr int kDiffLambdaParts = 64;
 atlas_status launch_diff_lambda(const DiffLambdaArgs &a, bool bwd, cudaStream_t stream);
+atlas_status launch_diff_attn_tc(const DiffArgs &a, cudaStream_t stream);   // bf16
 atlas_status launch_diff_attn_simt(const DiffArgs &a, cudaStream_t stream);
 atlas_status launch_diff_bwd_delta(const DiffBwdArgs &a, cudaStream_t stream);
 atlas_status launch_diff_dlambda(const DiffBwdArgs &a, cudaStream_t stream);

@@ -1,0 +1,634 @@
+// diff_attn_tc.cu -- differential attention, bf16, tcgen05 + TMA + TMEM.
+//
+// o = (softmax(s_1) - lambda softmax(s_2)) v with s_m = scale <q_m, k_m>, the
+// maps being the halves of a head's channels. Each map keeps its own running
+// maximum, sum and fp32 accumulator O_m = sum exp(s_m - max) v; the epilogue
+// joins them: o = O_1 / l_1 - lambda O_2 / l_2.
+//
+// Why one pass over the keys with two accumulators: the joint weights need both
+// sums, so a single accumulator would take a second pass over the logits, and
+// the exponentials, not the products, are what bounds the kernel: two per (query,
+// key) pair at 16 a clock and SM are 2048 clk per 128 x 128 tile, against 1536
+// clk of products (2 D of logits and 4 D with v per pair, D = 128).
+//
+// A unit is 128 query rows of one head (attn_units.cuh); a Q, K or V tile is
+// the same 128 x D tile an ordinary head has, its channel halves being the maps,
+// so K and V are read once for both maps. Persistent CTAs walk the units
+// head-major. Warps (384 threads):
+//   0-3 / 4-7  softmax of map 1 / 2 (thread = query row = TMEM lane); in the
+//              epilogue each group joins half of the output's columns,
+//   8          TMA producer, 9  MMA issuer (one thread), 10-11  idle.
+// Tensor memory: S_1 | S_2 (128 columns each) | O_1 | O_2 (D each); P (bf16) goes
+// over the first half of its S. Issue order per key tile j:
+//   O_1 += P_1(j) V(j), S_1(j+1), O_2 += P_2(j) V(j), S_2(j+1);
+// one thread's MMAs run in order, so S_m(j+1) overwrites P_m(j) only after it
+// was read. Keys past the unit's range: their logits are set to -inf whatever
+// they hold, and their V rows are zeroed in shared memory before the product
+// (0 * NaN would reach every row).
+// Every wait is bounded: on expiry a bit is set in the device error word, the
+// CTA drains its copies and MMAs, frees its tensor memory and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "attn_units.cuh"
+#include "sm100_ptx.cuh"
+
+namespace atlas {
+namespace {
+
+using units::Sched;
+using units::Shape;
+using units::Unit;
+
+constexpr int kBM = units::kRows;   // query rows of a unit
+constexpr int kBN = units::kRows;   // keys of a tile
+constexpr int kMaps = 2;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kThreads = 384;
+// Register split: 384 x 168 at launch; 256 x 200 + 128 x 104 after.
+constexpr uint32_t kRegsSoftmax = 200;
+constexpr uint32_t kRegsOther = 104;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * 168, "register split");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8
+
+template <int HD>
+struct Smem {
+    static constexpr int kTileBytes = kBM * HD * 2;
+    static constexpr int kSlots = (160 * 1024) / kTileBytes < 8 ? (160 * 1024) / kTileBytes : 8;
+    alignas(1024) uint8_t q[kTileBytes];
+    alignas(1024) uint8_t kv[kSlots][kTileBytes];
+    float inv_l[2][kMaps][kBM];  // by unit parity
+    uint64_t q_full, q_empty;
+    uint64_t kv_full[kSlots], kv_empty[kSlots];
+    uint64_t s_full[kMaps];      // S_m(j) in TMEM, O_m += P_m(j-1) V done  (commit)
+    uint64_t p_full[kMaps];      // P_m(j) in TMEM, O_m rescaled            (128 arrivals)
+    uint64_t o_final;            // every MMA of the unit done              (commit)
+    uint64_t joined;             // both maps' inv_l written                (256 arrivals)
+    uint64_t o_empty;            // both accumulators read                  (256 arrivals)
+    uint64_t drain;
+    uint32_t tmem_base;
+    int32_t max_len;
+    volatile int abort;
+    uint32_t *err_word;
+};
+
+struct Params {
+    CUtensorMap tm_q[2], tm_k[2], tm_v[2];   // [0] detail, [1] global
+    __nv_bfloat16 *o[2], *s[2];
+    float *lse;
+    const float *lambda;
+    int32_t n_lambda;
+    uint32_t *err_word;
+    float scale_log2;
+    int32_t stall_unit;   // test hook: this unit's first K tile is never loaded (-1: off)
+    int32_t o_v8;         // every output 32-byte aligned: 32-byte stores
+    Shape shape;
+};
+
+template <int HD>
+__device__ __forceinline__ bool wait_phase(Smem<HD> &sm, uint64_t &bar, uint32_t parity,
+                                           uint32_t err, bool honor_abort = true) {
+    const uint32_t a = ptx::smem_addr(&bar);
+    if (ptx::mbar_try_wait(a, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t spin = 1;; ++spin) {
+        if (ptx::mbar_try_wait(a, parity)) return true;
+        if ((spin & 63u) == 0) {
+            if (honor_abort && sm.abort) return false;
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+                atomicOr(sm.err_word, err);
+                sm.abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// Columns of key tile j that can hold an allowed key: its MMAs take 32, 64 or
+// all kBN of them; the S columns beyond are stale and never used.
+__device__ __forceinline__ int32_t tile_cols(const Unit &U, int32_t j) {
+    const int32_t n = units::tile_rows(U, j);
+    return n <= 32 ? 32 : (n <= 64 ? 64 : kBN);
+}
+
+// ---------------------------------------------------------------------------
+// Producer: Q once per unit, then K(0), V(0), K(1), V(1), ...
+// ---------------------------------------------------------------------------
+template <int HD>
+__device__ void producer(const Params &p, const Sched &S, Smem<HD> &sm) {
+    constexpr uint32_t kBytes = Smem<HD>::kTileBytes;
+    constexpr int kSlots = Smem<HD>::kSlots;
+    uint32_t it = 0, unit_iter = 0, q_armed = 0;
+    uint32_t armed[kSlots];
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) armed[s] = 0;
+    bool ok = true;
+    auto load = [&](const CUtensorMap *map, int32_t head, int32_t row) -> bool {
+        const uint32_t slot = it % kSlots, round = it / kSlots;
+        if (round > 0 &&
+            !wait_phase(sm, sm.kv_empty[slot], (round - 1) & 1, kErrTimeoutProducer))
+            return false;
+        const uint32_t bar = ptx::smem_addr(&sm.kv_full[slot]);
+        ptx::mbar_arrive_expect_tx(bar, kBytes);
+#pragma unroll
+        for (int db = 0; db < HD / 64; ++db)
+            ptx::tma_load_3d(ptx::smem_addr(sm.kv[slot] + db * kBN * 128), map, bar, db * 64,
+                             head, row);
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s)
+            if (s == static_cast<int>(slot)) armed[s] = round + 1;
+        ++it;
+        return true;
+    };
+    for (int32_t u = blockIdx.x; u < S.n_units && ok; u += gridDim.x) {
+        const Unit U = units::query_unit(p.shape, S, u);
+        const int32_t n = U.n_a + U.n_b;
+        if (n == 0) continue;
+        if (unit_iter > 0 && !(ok = wait_phase(sm, sm.q_empty, (unit_iter - 1) & 1,
+                                               kErrTimeoutProducer)))
+            break;
+        const int32_t base[2] = {U.b * p.shape.N, U.b * p.shape.G};
+        const int side = U.detail ? 0 : 1;
+        const uint32_t bar = ptx::smem_addr(&sm.q_full);
+        ptx::mbar_arrive_expect_tx(bar, kBytes);
+#pragma unroll
+        for (int db = 0; db < HD / 64; ++db)
+            ptx::tma_load_3d(ptx::smem_addr(sm.q + db * kBM * 128), &p.tm_q[side], bar, db * 64,
+                             U.head, base[side] + U.r0);
+        q_armed = ++unit_iter;
+        for (int32_t j = 0; j < n && ok; ++j) {
+            const int kind = j < U.n_a ? 0 : 1;
+            const int32_t row = base[kind] + units::tile_row(U, j);
+            if (j == 0 && u == p.stall_unit) {
+                // Failure-path test: this slot stays unarmed, so the waits
+                // on it expire.
+                ++it;
+                ok = load(&p.tm_v[kind], U.head, row);
+                continue;
+            }
+            ok = load(&p.tm_k[kind], U.head, row) && load(&p.tm_v[kind], U.head, row);
+        }
+    }
+    if (!ok) {
+        // Let every copy already issued land before the CTA can exit.
+        if (q_armed) wait_phase(sm, sm.q_full, (q_armed - 1) & 1, kErrTimeoutTeardown, false);
+        for (int s = 0; s < kSlots; ++s)
+            if (armed[s])
+                wait_phase(sm, sm.kv_full[s], (armed[s] - 1) & 1, kErrTimeoutTeardown, false);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// MMA issuer (one thread).
+// ---------------------------------------------------------------------------
+template <int HD>
+__device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm, uint32_t tmem) {
+    constexpr int kSlots = Smem<HD>::kSlots;
+    constexpr int kMapSteps = HD / 32;   // K = 16 steps of one map's channels
+    constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, kBN, 0);
+    constexpr uint32_t kIdescQK64 = ptx::idesc_bf16_f32(kBM, 64, 0);
+    constexpr uint32_t kIdescQK32 = ptx::idesc_bf16_f32(kBM, 32, 0);
+    constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, HD, 1);
+    constexpr uint32_t kHi = ptx::desc_sw128_hi(1024);
+    constexpr uint32_t kTile16 = Smem<HD>::kTileBytes >> 4;
+    const uint32_t q_lo = ptx::desc_sw128_lo(ptx::smem_addr(sm.q), 16);
+    const uint32_t k_lo0 = ptx::desc_sw128_lo(ptx::smem_addr(sm.kv[0]), 16);
+    const uint32_t v_lo0 = ptx::desc_sw128_lo(ptx::smem_addr(sm.kv[0]), kBN * 128);
+    uint32_t it = 0, unit_iter = 0, p_cnt = 0;
+    bool ok = true;
+
+    auto next_slot = [&](uint32_t &slot) -> bool {
+        slot = it % kSlots;
+        const bool r = wait_phase(sm, sm.kv_full[slot], (it / kSlots) & 1, kErrTimeoutMma);
+        ++it;
+        ptx::tc_fence_after();
+        return r;
+    };
+    // S_m = Q_m K_m^T for the tile's first nc keys: map m's channels are the
+    // K = 16 steps m * kMapSteps .. of the tile (64-channel panels of 128-byte
+    // rows, four steps each).
+    auto issue_s = [&](int m, uint32_t k_slot, int32_t nc) {
+        const uint32_t k_lo = k_lo0 + k_slot * kTile16, d_s = tmem + m * kBN;
+        const uint32_t idesc = nc == kBN ? kIdescQK : (nc == 64 ? kIdescQK64 : kIdescQK32);
+#pragma unroll
+        for (int i = 0; i < kMapSteps; ++i) {
+            const int ks = m * kMapSteps + i;
+            const uint32_t off = ((ks / 4) * (kBM * 128) + (ks % 4) * 32) >> 4;
+            ptx::mma_ss(d_s, ptx::desc_join(q_lo + off, kHi), ptx::desc_join(k_lo + off, kHi),
+                        idesc, i > 0);
+        }
+        ptx::mma_commit(ptx::smem_addr(&sm.s_full[m]));
+    };
+    // O_m += P_m V, P_m from tensor memory; the tile's first nc keys.
+    auto issue_pv = [&](int m, uint32_t v_slot, bool first, int32_t nc) -> bool {
+        if (!wait_phase(sm, sm.p_full[m], p_cnt & 1, kErrTimeoutMma)) return false;
+        ptx::tc_fence_after();
+        const uint32_t v_lo = v_lo0 + v_slot * kTile16;
+        const uint32_t d_o = tmem + kMaps * kBN + m * HD, a_p = tmem + m * kBN;
+        ptx::mma_ts(d_o, a_p, ptx::desc_join(v_lo, kHi), kIdescPV, first ? 0u : 1u);
+        if (nc == kBN) {
+#pragma unroll
+            for (int ks = 1; ks < kBN / 16; ++ks)
+                ptx::mma_ts(d_o, a_p + ks * 8,
+                            ptx::desc_join(v_lo + ((ks * 16 * 128) >> 4), kHi), kIdescPV, 1u);
+        } else {
+#pragma unroll 1
+            for (int ks = 1; ks * 16 < nc; ++ks)
+                ptx::mma_ts(d_o, a_p + ks * 8,
+                            ptx::desc_join(v_lo + ((ks * 16 * 128) >> 4), kHi), kIdescPV, 1u);
+        }
+        return true;
+    };
+
+    for (int32_t u = blockIdx.x; u < S.n_units && ok; u += gridDim.x) {
+        const Unit U = units::query_unit(p.shape, S, u);
+        const int32_t n = U.n_a + U.n_b;
+        if (n == 0) continue;
+        if (!(ok = wait_phase(sm, sm.q_full, unit_iter & 1, kErrTimeoutMma))) break;
+        ptx::tc_fence_after();
+        uint32_t k_slot, v_slot;
+        if (!(ok = next_slot(k_slot))) break;
+        int32_t nc = tile_cols(U, 0);
+        issue_s(0, k_slot, nc);
+        issue_s(1, k_slot, nc);
+        ptx::mma_commit(ptx::smem_addr(&sm.kv_empty[k_slot]));
+        // Only the S MMAs read Q: after the unit's last one it is free.
+        if (n == 1) ptx::mma_commit(ptx::smem_addr(&sm.q_empty));
+        // The accumulators of the previous unit have been read.
+        if (unit_iter > 0 &&
+            !(ok = wait_phase(sm, sm.o_empty, (unit_iter - 1) & 1, kErrTimeoutMma)))
+            break;
+        for (int32_t j = 0; j < n && ok; ++j) {
+            const bool more = j + 1 < n;
+            const int32_t nc_next = more ? tile_cols(U, j + 1) : 0;
+            if (!(ok = next_slot(v_slot)) || !(ok = issue_pv(0, v_slot, j == 0, nc))) break;
+            if (more) {
+                if (!(ok = next_slot(k_slot))) break;
+                issue_s(0, k_slot, nc_next);
+            }
+            if (!(ok = issue_pv(1, v_slot, j == 0, nc))) break;
+            if (more) {
+                issue_s(1, k_slot, nc_next);
+                ptx::mma_commit(ptx::smem_addr(&sm.kv_empty[k_slot]));
+                if (j + 2 == n) ptx::mma_commit(ptx::smem_addr(&sm.q_empty));
+            }
+            nc = nc_next;
+            ptx::mma_commit(ptx::smem_addr(&sm.kv_empty[v_slot]));
+            ++p_cnt;
+        }
+        if (!ok) break;
+        ptx::mma_commit(ptx::smem_addr(&sm.o_final));
+        ++unit_iter;
+    }
+    // Drain: every MMA issued must finish before tensor memory is freed.
+    ptx::mma_commit(ptx::smem_addr(&sm.drain));
+    wait_phase(sm, sm.drain, 0, kErrTimeoutTeardown, false);
+}
+
+// ---------------------------------------------------------------------------
+// Softmax of map `map`, and the epilogue; 128 threads, thread = row = lane.
+// ---------------------------------------------------------------------------
+template <int HD>
+__device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, uint32_t tmem,
+                                 int map) {
+    constexpr int kSlots = Smem<HD>::kSlots;
+    const uint32_t r = threadIdx.x & 127;
+    const uint32_t lane_sel = ((threadIdx.x / 32) & 3) * (32u << 16);
+    const uint32_t t_s = tmem + map * kBN + lane_sel;      // S, then P over its first half
+    const uint32_t t_o = tmem + kMaps * kBN + map * HD + lane_sel;
+    const uint32_t err = kErrTimeoutSoftmax;
+    const float sc = p.scale_log2;
+
+    // P = exp2(S*scale*log2e - m) as bf16 pairs into tensor memory; returns the
+    // row sum of the fp32 P (rounding P to bf16 halves the product's operand
+    // and is 2^-8 of each weight; the sum keeps fp32). with_max: the row maximum
+    // of the raw S, taken in the same pass, into mx.
+    auto exp_store = [&](auto with_max, const uint32_t (&sr)[kBN], float m, float &mx,
+                         auto &&between) -> float {
+        constexpr bool kWithMax = decltype(with_max)::value;
+        float sum8[8], m8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            sum8[k] = 0.f;
+            m8[k] = kNegInf;
+        }
+#pragma unroll
+        for (int g = 0; g < kBN / 64; ++g) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const int c = g * 64 + 2 * e;
+                const float s0 = __uint_as_float(sr[c]), s1 = __uint_as_float(sr[c + 1]);
+                if constexpr (kWithMax) m8[e & 7] = ptx::max3(m8[e & 7], s0, s1);
+                const float p0 = ptx::ex2(fmaf(s0, sc, -m));
+                const float p1 = ptx::ex2(fmaf(s1, sc, -m));
+                sum8[e & 7] += p0 + p1;
+                pk[e] = ptx::pack_bf16x2(p0, p1);
+            }
+            ptx::tmem_st32_nowait(t_s + g * 32, pk);
+            if (g == 0) between();
+        }
+        ptx::tmem_wait_st();
+#pragma unroll
+        for (int w = 4; w >= 1; w >>= 1)
+#pragma unroll
+            for (int k = 0; k < w; ++k) {
+                sum8[k] += sum8[k + w];
+                if constexpr (kWithMax) m8[k] = fmaxf(m8[k], m8[k + w]);
+            }
+        if constexpr (kWithMax) mx = m8[0];
+        return sum8[0];
+    };
+    auto row_max = [&](const uint32_t (&sr)[kBN]) -> float {
+        float m8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m8[k] = __uint_as_float(sr[k]);
+#pragma unroll
+        for (int c = 8; c + 16 <= kBN; c += 16)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                m8[k] = ptx::max3(m8[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m8[k] = fmaxf(m8[k], __uint_as_float(sr[kBN - 8 + k]));
+        return ptx::max3(ptx::max3(m8[0], m8[1], m8[2]), ptx::max3(m8[3], m8[4], m8[5]),
+                         fmaxf(m8[6], m8[7]));
+    };
+    // O *= alpha, in warps where some row moved its reference. The P*V of the
+    // previous tile is done: the commit that signalled this S covers it.
+    auto rescale_o = [&](bool need, float alpha) {
+        if (!__any_sync(kAll, need)) return;
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+            uint32_t o[32];
+            ptx::tmem_ld32(t_o + c * 32, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            ptx::tmem_st32(t_o + c * 32, o);
+        }
+    };
+
+    uint32_t cnt = 0, unit_iter = 0;   // key tiles, units
+    for (int32_t u = blockIdx.x; u < S.n_units; u += gridDim.x) {
+        const Unit U = units::query_unit(p.shape, S, u);
+        const int32_t n = U.n_a + U.n_b;
+        if (n == 0) continue;
+        const int32_t row = U.r0 + static_cast<int32_t>(r);
+        const bool valid = row < U.rend;
+        int32_t da, db, ga, gb;   // keys of this row
+        units::query_ranges(p.shape, U, row, da, db, ga, gb);
+        const float lam = __ldg(p.lambda + (p.n_lambda == 1 ? 0 : U.head));
+        float m_run = kNegInf, l_run = 0.f;
+        for (int32_t j = 0; j < n; ++j, ++cnt) {
+            if (!__all_sync(kAll, wait_phase(sm, sm.s_full[map], cnt & 1, err))) return;
+            ptx::tc_fence_after();
+            const int32_t k0 = units::tile_row(U, j);
+            const int32_t klo = j < U.n_a ? da : ga, khi = j < U.n_a ? db : gb;
+            const bool masked = k0 < klo || k0 + kBN > khi;
+            uint32_t sr[kBN];
+            ptx::tmem_ld64(t_s, *reinterpret_cast<uint32_t(*)[64]>(&sr[0]));
+            ptx::tmem_ld64_nowait(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&sr[64]));
+            auto wait_hi = [&] { ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[64]>(&sr[64])); };
+            float sum, mx;
+            if (__any_sync(kAll, m_run == kNegInf || masked)) {
+                wait_hi();
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < kBN; ++c)
+                        if (k0 + c < klo || k0 + c >= khi) sr[c] = __float_as_uint(kNegInf);
+                }
+                // The reference moves only when the tile's maximum exceeds it
+                // by more than the threshold (exact either way: O and l share
+                // it).
+                const float mx2 = row_max(sr) * sc;
+                const bool need = m_run == kNegInf ? mx2 != kNegInf
+                                                   : mx2 > m_run + kRescaleThreshold;
+                float alpha = 1.f;
+                if (need) {
+                    alpha = m_run == kNegInf ? 0.f : ptx::ex2(m_run - mx2);
+                    m_run = mx2;
+                }
+                l_run *= alpha;
+                if (j > 0) rescale_o(need, alpha);
+                sum = exp_store(std::false_type{}, sr, m_run == kNegInf ? 0.f : m_run, mx, [] {});
+                // V rows that no row of the unit may see: zeroed once, by map
+                // 0's threads (its product is issued first). V(j) is load
+                // 2 cnt + 1 of the ring, and stays until both products ran.
+                const int32_t seen = units::tile_rows(U, j);
+                if (map == 0 && seen < kBN) {
+                    const uint32_t it = 2 * cnt + 1, slot = it % kSlots;
+                    if (!__all_sync(kAll, wait_phase(sm, sm.kv_full[slot], (it / kSlots) & 1, err)))
+                        return;
+                    if (static_cast<int32_t>(r) >= seen && static_cast<int32_t>(r) < tile_cols(U, j)) {
+#pragma unroll
+                        for (int i = 0; i < HD / 64 * 8; ++i)
+                            ptx::st_shared_v4(sm.kv[slot] + (i / 8) * kBN * 128 + r * 128 +
+                                                  (i % 8) * 16, 0, 0, 0, 0);
+                    }
+                    ptx::fence_proxy_async_smem();
+                }
+            } else {
+                // Exponentials against the running reference right away, the
+                // tile's maximum in the same pass; the (rare) rows whose
+                // maximum moved past the threshold are redone.
+                sum = exp_store(std::true_type{}, sr, m_run, mx, wait_hi);
+                const float mx2 = mx * sc;
+                const bool need = mx2 > m_run + kRescaleThreshold;
+                if (__any_sync(kAll, need)) {
+                    const float alpha = need ? ptx::ex2(m_run - mx2) : 1.f;
+                    if (need) m_run = mx2;
+                    l_run *= alpha;
+                    rescale_o(need, alpha);
+                    sum = exp_store(std::false_type{}, sr, m_run, mx, [] {});
+                }
+            }
+            l_run += sum;
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(ptx::smem_addr(&sm.p_full[map]));
+        }
+        // Epilogue: both maps' 1/l through shared memory; this group joins
+        // columns [map * D/2, +D/2) of O_1 and O_2.
+        const uint32_t par = unit_iter & 1;
+        sm.inv_l[par][map][r] = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
+        ptx::mbar_arrive(ptx::smem_addr(&sm.joined));
+        if (p.lse != nullptr && valid) {
+            const int64_t rows = static_cast<int64_t>(p.shape.N) + p.shape.G;
+            p.lse[((static_cast<int64_t>(U.b) * p.shape.heads + U.head) * 2 + map) * rows +
+                  (U.detail ? row : static_cast<int64_t>(p.shape.N) + row)] =
+                (m_run + __log2f(l_run)) * 0.69314718055994531f;
+        }
+        if (!__all_sync(kAll, wait_phase(sm, sm.joined, par, err) &&
+                                  wait_phase(sm, sm.o_final, par, err)))
+            return;
+        ptx::tc_fence_after();
+        const float f1 = sm.inv_l[par][0][r], f2 = sm.inv_l[par][1][r];
+        constexpr int kHalf = HD / 2;
+        uint32_t o1[kHalf], o2[kHalf];
+        const uint32_t t_o1 = tmem + kMaps * kBN + lane_sel + map * kHalf, t_o2 = t_o1 + HD;
+        if constexpr (kHalf == 64) {
+            ptx::tmem_ld64(t_o1, o1);
+            ptx::tmem_ld64(t_o2, o2);
+        } else {
+            ptx::tmem_ld32(t_o1, o1);
+            ptx::tmem_ld32(t_o2, o2);
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_addr(&sm.o_empty));
+        ++unit_iter;
+        if (!valid) continue;
+        const int side = U.detail ? 0 : 1;
+        const int64_t at = ((static_cast<int64_t>(U.b) * (U.detail ? p.shape.N : p.shape.G) + row) *
+                                p.shape.heads + U.head) * HD + map * kHalf;
+#pragma unroll
+        for (int e = 0; e < kHalf; ++e) {
+            const float b = __uint_as_float(o2[e]) * f2;
+            o1[e] = __float_as_uint(fmaf(-lam, b, __uint_as_float(o1[e]) * f1));
+            o2[e] = __float_as_uint(b);
+        }
+        auto store = [&](__nv_bfloat16 *out, const uint32_t (&v)[kHalf]) {
+            uint8_t *dst = reinterpret_cast<uint8_t *>(out + at);
+#pragma unroll
+            for (int i = 0; i < kHalf / 16; ++i) {
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    w[e] = ptx::pack_bf16x2(__uint_as_float(v[16 * i + 2 * e]),
+                                            __uint_as_float(v[16 * i + 2 * e + 1]));
+                if (p.o_v8) {
+                    ptx::st_global_v8(dst + i * 32, w);
+                } else {
+                    reinterpret_cast<uint4 *>(dst)[2 * i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    reinterpret_cast<uint4 *>(dst)[2 * i + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
+        };
+        store(p.o[side], o1);
+        if (p.s[side] != nullptr) store(p.s[side], o2);
+    }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_constant__ Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem<HD> &sm = *reinterpret_cast<Smem<HD> *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(ptx::smem_addr(&sm.q_full), 1);
+        ptx::mbar_init(ptx::smem_addr(&sm.q_empty), 1);
+        for (int s = 0; s < Smem<HD>::kSlots; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&sm.kv_full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&sm.kv_empty[s]), 1);
+        }
+        for (int m = 0; m < kMaps; ++m) {
+            ptx::mbar_init(ptx::smem_addr(&sm.s_full[m]), 1);
+            ptx::mbar_init(ptx::smem_addr(&sm.p_full[m]), kBM);
+        }
+        ptx::mbar_init(ptx::smem_addr(&sm.o_final), 1);
+        ptx::mbar_init(ptx::smem_addr(&sm.joined), kMaps * kBM);
+        ptx::mbar_init(ptx::smem_addr(&sm.o_empty), kMaps * kBM);
+        ptx::mbar_init(ptx::smem_addr(&sm.drain), 1);
+        sm.abort = 0;
+        sm.max_len = 0;
+        sm.err_word = p.err_word;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        ptx::tmem_alloc(ptx::smem_addr(&sm.tmem_base), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        for (int i = 0; i < 2; ++i) {
+            ptx::prefetch_tmap(&p.tm_q[i]);
+            ptx::prefetch_tmap(&p.tm_k[i]);
+            ptx::prefetch_tmap(&p.tm_v[i]);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (p.shape.upw < 0) {
+        units::longest_window(p.shape, &sm.max_len);
+        __syncthreads();
+    }
+    const Sched S = units::make_sched(p.shape, sm.max_len);
+    const uint32_t tmem = sm.tmem_base;
+    const bool tmem_ok = tmem == 0;   // a 512-column allocation starts at column 0
+    if (!tmem_ok && threadIdx.x == 0) atomicOr(p.err_word, kErrTmemAlloc);
+    if (warp < 8) {
+        ptx::setmaxnreg_inc<kRegsSoftmax>();
+        if (tmem_ok) softmax_epilogue<HD>(p, S, sm, tmem, warp / 4);
+    } else {
+        ptx::setmaxnreg_dec<kRegsOther>();
+        if (tmem_ok && lane == 0) {
+            if (warp == kProducerWarp) producer<HD>(p, S, sm);
+            if (warp == kMmaWarp) mma_issuer<HD>(p, S, sm, tmem);
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int HD>
+atlas_status launch_hd(const DiffArgs &d, const DeviceInfo &dev, cudaStream_t stream) {
+    const AttnArgs &a = d.attn;
+    Params p{};
+    int64_t n_units = 0;
+    if (!units::make_shape(a, dev.sm_count, &p.shape, &n_units)) return ATLAS_ERR_SHAPE;
+    const void *src[2][3] = {{a.q_d, a.k_d, a.v_d}, {a.q_g, a.k_g, a.v_g}};
+    const int64_t rows[2] = {a.n_detail * a.batch, a.n_global * a.batch};
+    CUtensorMap *maps[3] = {p.tm_q, p.tm_k, p.tm_v};
+    for (int side = 0; side < 2; ++side) {
+        // Maps of an absent side point at the other side; they are never used.
+        const int use = rows[side] > 0 ? side : 1 - side;
+        for (int t = 0; t < 3; ++t)
+            if (!make_rows_map(&maps[t][side], src[use][t], rows[use], a.heads, HD))
+                return ATLAS_ERR_CUDA;
+    }
+    p.o[0] = static_cast<__nv_bfloat16 *>(a.o_d);
+    p.o[1] = static_cast<__nv_bfloat16 *>(a.o_g);
+    p.s[0] = static_cast<__nv_bfloat16 *>(d.s_d);
+    p.s[1] = static_cast<__nv_bfloat16 *>(d.s_g);
+    uintptr_t bits = 0;
+    for (int side = 0; side < 2; ++side)
+        bits |= reinterpret_cast<uintptr_t>(p.o[side]) | reinterpret_cast<uintptr_t>(p.s[side]);
+    p.o_v8 = (bits & 31) == 0;
+    p.lse = a.lse;
+    p.lambda = d.lambda;
+    p.n_lambda = d.n_lambda;
+    p.err_word = device_error_word();
+    if (!p.err_word) return ATLAS_ERR_CUDA;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.stall_unit = take_stall_request() ? 0 : -1;
+    const size_t smem = sizeof(Smem<HD>) + 1024;
+    if (!set_smem_limit(reinterpret_cast<const void *>(diff_tc_kernel<HD>),
+                        static_cast<int>(smem)))
+        return ATLAS_ERR_CUDA;
+    const int grid = static_cast<int>(n_units < dev.sm_count ? n_units : dev.sm_count);
+    if (log_enabled())
+        log_launch("diff_tc_kernel", grid, kThreads, smem,
+                   "head_dim %d units %lld batch %d heads %d n_detail %d window %d n_global %d", HD,
+                   static_cast<long long>(n_units), p.shape.batch, p.shape.heads, p.shape.N,
+                   p.shape.L, p.shape.G);
+    diff_tc_kernel<HD><<<grid, kThreads, smem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
+}
+
+}  // namespace
+
+atlas_status launch_diff_attn_tc(const DiffArgs &d, cudaStream_t stream) {
+    DeviceInfo dev;
+    if (!current_device(&dev)) return ATLAS_ERR_DEVICE;
+    return d.attn.head_dim == 128 ? launch_hd<128>(d, dev, stream)
+                                  : launch_hd<64>(d, dev, stream);
+}
+
+}  // namespace atlas
