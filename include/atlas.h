@@ -610,10 +610,9 @@ atlas_status atlas_diff_lambda_bwd(const void *q1, const void *k1, const void *q
  * BF16: tcgen05 kernel, both maps' softmax and both outputs in fp32, each map's
  * unnormalised weights rounded to bf16 before their product with v, o rounded
  * once. FP32: exact fp32 products. head_dim 64 or 128.
- * A row's result depends on no key outside its problem's allowed range, whatever
- * those keys hold, except (BF16) that a non-finite value of v in a window
- * shorter than 128 rows may reach the rows of the neighbouring windows that share
- * its 128 rows.
+ * A row's result depends on no key that it does not see, whatever that key holds
+ * (infinities and NaN included). BF16, windows below 128 rows: a row that sees a
+ * key whose v is not finite is NaN in all its channels.
  * Errors: as atlas_local_global_attn_ex; NULL lambda (NULL), n_lambda neither 1
  * nor heads (SHAPE), lambda not 4-byte aligned (ALIGN).
  */
@@ -631,7 +630,9 @@ atlas_status atlas_diff_attn(const void *q_d, const void *k_d, const void *v_d,
  *   dS_1 = P_1 (dP - D_1),  dS_2 = -lambda P_2 (dP - D_2),
  *   dq_m = scale dS_m k_m,  dk_m = scale dS_m^T q_m,
  *   dv = (P_1 - lambda P_2)^T do,  dlambda = -sum D_2
- * (summed over the heads as well when n_lambda is 1).
+ * (summed over the heads as well when n_lambda is 1). As in the forward pass, a row
+ * that is not met by a query or key does not reach its gradients; a query whose
+ * do is not finite makes the whole dv rows (BF16) of the keys it sees NaN.
  * o_*, s_*, lse: the forward's. workspace: DEVICE fp32, 16-byte aligned, of
  * atlas_diff_attn_bwd_workspace bytes, overwritten; calls that overlap on the
  * GPU need one each. dq_*, dk_*, dv_*: as q_*; dlambda: fp32 [n_lambda]. All sums

@@ -203,6 +203,48 @@ def test_masked_garbage_changes_nothing(hd, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("aligned", [False, True])
+def test_masked_garbage_in_short_windows(hd, dtype, aligned):
+    """The same for windows that share a 128-row tile: only the rows of the window
+    that holds the garbage, and the global keys it meets, are touched; those are."""
+    B, N, L, G, H = 1, 200, 20, 60, 1
+    shares = [0, 10, 10, 16, 22, 28, 34, 40, 46, 52, 60]
+    kw = {"window_len": L}
+    if aligned:
+        kw["global_window_offsets"] = torch.tensor(shares, dtype=torch.int32, device=DEV)
+    lam = torch.tensor([0.6], device=DEV)
+    t = make(B, N, G, H, hd, dtype)
+    clean = run(t, lam, B, N, G, H, **kw)
+    for name, row, value in (("v_d", 45, float("inf")), ("k_d", 59, float("nan")), ("q_d", 40, float("inf")),
+                             ("do_d", 51, float("nan")), ("v_d", 199, float("nan"))):
+        w = row // L
+        mine = slice(w * L, (w + 1) * L)
+        bad = {n: x.clone() for n, x in t.items()}
+        bad[name][row, 0, 3] = value
+        out = run(bad, lam, B, N, G, H, **kw)
+        rest = torch.ones(N, dtype=torch.bool, device=DEV)
+        rest[mine] = False
+        for n in ("o", "s") + GRADS:
+            assert torch.equal(out[n + "_d"][rest], clean[n + "_d"][rest]), (name, n)
+        for n in ("o", "s", "dq"):
+            assert torch.equal(out[n + "_g"], clean[n + "_g"]), (name, n)
+        if aligned:
+            unseen = torch.ones(G, dtype=torch.bool, device=DEV)
+            unseen[shares[w]:shares[w + 1]] = False
+            for n in ("dk", "dv"):
+                assert torch.equal(out[n + "_g"][unseen], clean[n + "_g"][unseen]), (name, n)
+        # and the rows that do see it show it
+        if name in ("v_d", "k_d"):
+            assert not bool(torch.isfinite(out["o_d"][mine, 0, 3]).any()), name
+        if name == "q_d":
+            assert not bool(torch.isfinite(out["o_d"][row]).any())
+        if name == "do_d":
+            assert not bool(torch.isfinite(out["dv_d"][mine, 0, 3]).any())
+            assert not bool(torch.isfinite(out["dk_d"][mine]).any())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_bits_streams_and_graph(dtype):
     """The same call gives the same bits: eager twice, on a side stream, and
     replayed from a graph that two captures share the inputs of."""

@@ -958,7 +958,8 @@ ATLAS_API atlas_status atlas_diff_attn_bwd(
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (rows > 0) {
         if ((st = launch_diff_bwd_delta(b, s)) != ATLAS_OK) return st;
-        if ((st = launch_diff_bwd_simt(b, s)) != ATLAS_OK) return st;
+        st = dtype == ATLAS_BF16 ? launch_diff_bwd_tc(b, s) : launch_diff_bwd_simt(b, s);
+        if (st != ATLAS_OK) return st;
     }
     return launch_diff_dlambda(b, s);
 }

@@ -208,6 +208,7 @@ atlas_status launch_diff_attn_tc(const DiffArgs &a, cudaStream_t stream);   // b
 atlas_status launch_diff_attn_simt(const DiffArgs &a, cudaStream_t stream);
 atlas_status launch_diff_bwd_delta(const DiffBwdArgs &a, cudaStream_t stream);
 atlas_status launch_diff_dlambda(const DiffBwdArgs &a, cudaStream_t stream);
+atlas_status launch_diff_bwd_tc(const DiffBwdArgs &a, cudaStream_t stream);      // bf16
 atlas_status launch_diff_bwd_simt(const DiffBwdArgs &a, cudaStream_t stream);
 
 // Group norm (group_norm.cu).

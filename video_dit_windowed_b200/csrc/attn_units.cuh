@@ -17,7 +17,7 @@
 namespace atlas {
 namespace units {
 
-constexpr int kRows = 128;   // rows of a unit, keys of a streamed tile
+constexpr int kRows = 128;   // rows of a unit
 
 struct Shape {
     int32_t N, L, G, heads, batch;   // N, G: rows of ONE problem
@@ -99,17 +99,19 @@ __device__ __forceinline__ int32_t window_of_global(const Shape &p, int32_t g) {
 }
 
 // A work unit: rows r0 .. rend-1 (within problem b) of one head; the streamed
-// rows: n_a tiles of detail rows from a0 (up to a_end), then n_b tiles of
+// rows: n_a tiles of TILE detail rows from a0 (up to a_end), then n_b tiles of
 // global rows from b0 (up to b_end). win >= 0: all rows meet the same ranges.
 // n_a + n_b == 0: an empty slot.
 struct Unit {
     int32_t head, b, detail, r0, rend, a0, n_a, a_end, b0, n_b, b_end, win;
 };
 
-__device__ __forceinline__ int32_t tiles(int32_t n) { return (n + kRows - 1) / kRows; }
+template <int TILE>
+__device__ __forceinline__ int32_t tiles(int32_t n) { return (n + TILE - 1) / TILE; }
 
 // Slot lu of one problem's detail rows, window form; the window's rows are
 // streamed and, for queries, its global keys.
+template <int TILE>
 __device__ __forceinline__ void window_unit(const Shape &p, const Sched &S, int32_t lu,
                                             bool queries, Unit &U) {
     const int32_t w = lu / S.upw, sub = lu - w * S.upw;
@@ -120,16 +122,17 @@ __device__ __forceinline__ void window_unit(const Shape &p, const Sched &S, int3
     U.rend = min(U.r0 + kRows, e);
     U.a0 = s;
     U.a_end = e;
-    U.n_a = tiles(e - s);
+    U.n_a = tiles<TILE>(e - s);
     U.b0 = U.n_b = U.b_end = 0;
     if (queries) {
         global_keys(p, w, U.b0, U.b_end);
-        U.n_b = tiles(U.b_end - U.b0);
+        U.n_b = tiles<TILE>(U.b_end - U.b0);
     }
     if (U.rend <= U.r0) U.n_a = U.n_b = 0;
 }
 
 // Packed detail rows or global rows, tile lu of one problem (forward, dQ).
+template <int TILE>
 __device__ __forceinline__ Unit query_unit(const Shape &p, const Sched &S, int32_t u) {
     Unit U;
     U.win = -1;
@@ -139,7 +142,7 @@ __device__ __forceinline__ Unit query_unit(const Shape &p, const Sched &S, int32
     lu -= U.b * S.per_prob;
     U.detail = lu < S.n_dunits;
     if (U.detail && S.upw > 0) {
-        window_unit(p, S, lu, true, U);
+        window_unit<TILE>(p, S, lu, true, U);
         return U;
     }
     U.r0 = (U.detail ? lu : lu - S.n_dunits) * kRows;
@@ -150,7 +153,7 @@ __device__ __forceinline__ Unit query_unit(const Shape &p, const Sched &S, int32
         const int32_t last = U.rend - 1, w0 = window_of(p, U.r0), w1 = window_of(p, last);
         U.a0 = window_start(p, w0, U.r0);
         U.a_end = window_end(p, w1, last);
-        U.n_a = tiles(U.a_end - U.a0);
+        U.n_a = tiles<TILE>(U.a_end - U.a0);
         if (p.gwin_off != nullptr) {
             int32_t unused;
             global_keys(p, w0, g0, unused);
@@ -160,12 +163,13 @@ __device__ __forceinline__ Unit query_unit(const Shape &p, const Sched &S, int32
     }
     U.b0 = g0;
     U.b_end = g1;
-    U.n_b = tiles(g1 - g0);
+    U.n_b = tiles<TILE>(g1 - g0);
     return U;
 }
 
 // Key rows and the queries that see them (dK/dV). Units over global keys come
 // first: they stream every query that sees them.
+template <int TILE>
 __device__ __forceinline__ Unit key_unit(const Shape &p, const Sched &S, int32_t u) {
     Unit U;
     U.win = -1;
@@ -178,7 +182,7 @@ __device__ __forceinline__ Unit key_unit(const Shape &p, const Sched &S, int32_t
     lv -= U.b * span;
     U.detail = !global_keys_unit;
     if (U.detail && S.upw > 0) {
-        window_unit(p, S, lv, false, U);
+        window_unit<TILE>(p, S, lv, false, U);
         return U;
     }
     U.r0 = lv * kRows;
@@ -208,19 +212,21 @@ __device__ __forceinline__ Unit key_unit(const Shape &p, const Sched &S, int32_t
         U.a0 = q0;
         U.a_end = q1;
         U.b_end = p.G;
-        U.n_b = p.tiles_g;
+        U.n_b = tiles<TILE>(p.G);
     }
-    U.n_a = tiles(U.a_end - U.a0);
+    U.n_a = tiles<TILE>(U.a_end - U.a0);
     return U;
 }
 
 // Streamed tile j of U: its first row (within the problem), and the rows behind
 // it that the unit meets.
+template <int TILE>
 __device__ __forceinline__ int32_t tile_row(const Unit &U, int32_t j) {
-    return j < U.n_a ? U.a0 + j * kRows : U.b0 + (j - U.n_a) * kRows;
+    return j < U.n_a ? U.a0 + j * TILE : U.b0 + (j - U.n_a) * TILE;
 }
+template <int TILE>
 __device__ __forceinline__ int32_t tile_rows(const Unit &U, int32_t j) {
-    return (j < U.n_a ? U.a_end : U.b_end) - tile_row(U, j);
+    return (j < U.n_a ? U.a_end : U.b_end) - tile_row<TILE>(U, j);
 }
 
 // The rows that row r of unit U may meet: detail [da, db), global [ga, gb).

@@ -78,12 +78,15 @@ __global__ void __launch_bounds__(kWarps * 32) lambda_kernel(const LambdaPtr p) 
 
 // ---------------------------------------------------------------------------
 // Row sums of the backward pass: D_2 = <do, s>, D_1 = <do, o> + lambda D_2
-// (o + lambda s is the first map's output), fp32 [batch, heads, 2, N+G].
+// (o + lambda s is the first map's output), fp32 [batch, heads, 2, N+G]. Both are
+// NaN where the row's lse is not finite (as <do, .> is where do is not), so a NaN
+// here marks every query row that holds a non-finite value: the tensor-core
+// kernel tells such a row from its neighbours in a tile by it.
 // ---------------------------------------------------------------------------
 template <typename T>
 struct DeltaPtr {
     const T *o_d, *s_d, *do_d, *o_g, *s_g, *do_g;
-    const float *lambda;
+    const float *lambda, *lse;
     int32_t n_lambda;
     float *delta;
 };
@@ -111,10 +114,13 @@ __global__ void __launch_bounds__(kWarps * 32) diff_delta_kernel(const DeltaPtr<
     if (lane == 0) {
         const float lam = p.lambda[p.n_lambda == 1 ? 0 : head];
         const int64_t rows = g.N + g.G;
-        float *out = p.delta + (at.b * g.heads + head) * 2 * rows +
-                     (at.detail ? at.local : g.N + at.local);
-        out[0] = fmaf(lam, sum_s, sum_o);
-        out[rows] = sum_s;
+        const int64_t col = (at.b * g.heads + head) * 2 * rows +
+                            (at.detail ? at.local : g.N + at.local);
+        const float d1 = fmaf(lam, sum_s, sum_o);
+        // 0 for finite values, NaN otherwise
+        const float mark = 0.f * p.lse[col] + 0.f * p.lse[col + rows] + 0.f * d1 + 0.f * sum_s;
+        p.delta[col] = d1 + mark;
+        p.delta[col + rows] = sum_s + mark;
     }
 }
 
@@ -409,6 +415,7 @@ atlas_status delta_hd(const DiffBwdArgs &b, cudaStream_t stream) {
     p.do_g = static_cast<const T *>(b.do_g);
     p.lambda = b.fwd.lambda;
     p.n_lambda = b.fwd.n_lambda;
+    p.lse = a.lse;
     p.delta = b.delta;
     log_rows("diff_delta_kernel", a);
     diff_delta_kernel<T, HD><<<row_grid(a), kWarps * 32, 0, stream>>>(p, attn_geom_of(a));

@@ -22,9 +22,11 @@
 // over the first half of its S. Issue order per key tile j:
 //   O_1 += P_1(j) V(j), S_1(j+1), O_2 += P_2(j) V(j), S_2(j+1);
 // one thread's MMAs run in order, so S_m(j+1) overwrites P_m(j) only after it
-// was read. Keys past the unit's range: their logits are set to -inf whatever
-// they hold, and their V rows are zeroed in shared memory before the product
-// (0 * NaN would reach every row).
+// was read. Masked keys: their logits are set to -inf whatever they hold; 0 * NaN
+// would still reach a row through P V, so the V rows past the unit's range are
+// zeroed in shared memory before the product. In packed units (PACK), whose rows
+// see different windows, so are V rows with a non-finite value, and the rows that
+// do see such a key become NaN in the epilogue.
 // Every wait is bounded: on expiry a bit is set in the device error word, the
 // CTA drains its copies and MMAs, frees its tensor memory and returns.
 #include <cuda.h>
@@ -43,7 +45,7 @@ using units::Shape;
 using units::Unit;
 
 constexpr int kBM = units::kRows;   // query rows of a unit
-constexpr int kBN = units::kRows;   // keys of a tile
+constexpr int kBN = 128;            // keys of a tile
 constexpr int kMaps = 2;
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
@@ -64,6 +66,7 @@ struct Smem {
     alignas(1024) uint8_t q[kTileBytes];
     alignas(1024) uint8_t kv[kSlots][kTileBytes];
     float inv_l[2][kMaps][kBM];  // by unit parity
+    uint32_t bad[4][4];          // PACK: non-finite V rows of the last four tiles
     uint64_t q_full, q_empty;
     uint64_t kv_full[kSlots], kv_empty[kSlots];
     uint64_t s_full[kMaps];      // S_m(j) in TMEM, O_m += P_m(j-1) V done  (commit)
@@ -110,10 +113,20 @@ __device__ __forceinline__ bool wait_phase(Smem<HD> &sm, uint64_t &bar, uint32_t
     }
 }
 
+// Whether one of eight bf16 values is infinite or NaN.
+__device__ __forceinline__ bool not_finite(const uint4 &v) {
+    bool bad = false;
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        bad |= (u[i] & 0x7f80u) == 0x7f80u || (u[i] & 0x7f800000u) == 0x7f800000u;
+    return bad;
+}
+
 // Columns of key tile j that can hold an allowed key: its MMAs take 32, 64 or
 // all kBN of them; the S columns beyond are stale and never used.
 __device__ __forceinline__ int32_t tile_cols(const Unit &U, int32_t j) {
-    const int32_t n = units::tile_rows(U, j);
+    const int32_t n = units::tile_rows<kBN>(U, j);
     return n <= 32 ? 32 : (n <= 64 ? 64 : kBN);
 }
 
@@ -147,7 +160,7 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD> &sm) {
         return true;
     };
     for (int32_t u = blockIdx.x; u < S.n_units && ok; u += gridDim.x) {
-        const Unit U = units::query_unit(p.shape, S, u);
+        const Unit U = units::query_unit<kBN>(p.shape, S, u);
         const int32_t n = U.n_a + U.n_b;
         if (n == 0) continue;
         if (unit_iter > 0 && !(ok = wait_phase(sm, sm.q_empty, (unit_iter - 1) & 1,
@@ -164,7 +177,7 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD> &sm) {
         q_armed = ++unit_iter;
         for (int32_t j = 0; j < n && ok; ++j) {
             const int kind = j < U.n_a ? 0 : 1;
-            const int32_t row = base[kind] + units::tile_row(U, j);
+            const int32_t row = base[kind] + units::tile_row<kBN>(U, j);
             if (j == 0 && u == p.stall_unit) {
                 // Failure-path test: this slot stays unarmed, so the waits
                 // on it expire.
@@ -247,7 +260,7 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm, uint32
     };
 
     for (int32_t u = blockIdx.x; u < S.n_units && ok; u += gridDim.x) {
-        const Unit U = units::query_unit(p.shape, S, u);
+        const Unit U = units::query_unit<kBN>(p.shape, S, u);
         const int32_t n = U.n_a + U.n_b;
         if (n == 0) continue;
         if (!(ok = wait_phase(sm, sm.q_full, unit_iter & 1, kErrTimeoutMma))) break;
@@ -294,7 +307,7 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm, uint32
 // ---------------------------------------------------------------------------
 // Softmax of map `map`, and the epilogue; 128 threads, thread = row = lane.
 // ---------------------------------------------------------------------------
-template <int HD>
+template <int HD, bool PACK>
 __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, uint32_t tmem,
                                  int map) {
     constexpr int kSlots = Smem<HD>::kSlots;
@@ -373,9 +386,24 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
         }
     };
 
+    // PACK: tiles whose keys not every row of the unit sees.
+    auto scanned = [&](const Unit &U, int32_t j) {
+        return PACK && U.detail && U.win < 0 && (j < U.n_a || p.shape.gwin_off != nullptr);
+    };
+    // Whether keys [klo, khi) of the tile at k0, tile count c, hold a bad V row.
+    auto sees_bad = [&](int32_t k0, int32_t klo, int32_t khi, uint32_t c) {
+        uint32_t hit = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int32_t a = max(klo - k0 - 32 * w, 0), b = min(khi - k0 - 32 * w, 32);
+            if (a < b) hit |= sm.bad[c & 3][w] & (kAll >> (32 - b)) & (kAll << a);
+        }
+        return hit != 0;
+    };
+
     uint32_t cnt = 0, unit_iter = 0;   // key tiles, units
     for (int32_t u = blockIdx.x; u < S.n_units; u += gridDim.x) {
-        const Unit U = units::query_unit(p.shape, S, u);
+        const Unit U = units::query_unit<kBN>(p.shape, S, u);
         const int32_t n = U.n_a + U.n_b;
         if (n == 0) continue;
         const int32_t row = U.r0 + static_cast<int32_t>(r);
@@ -384,10 +412,19 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
         units::query_ranges(p.shape, U, row, da, db, ga, gb);
         const float lam = __ldg(p.lambda + (p.n_lambda == 1 ? 0 : U.head));
         float m_run = kNegInf, l_run = 0.f;
+        bool bad = false;
+        // The marks of tile j (tile count c): map 0's threads wrote them before
+        // its product was issued, which S of the next tile and o_final follow.
+        auto check_bad = [&](int32_t j, uint32_t c) {
+            if (scanned(U, j))
+                bad |= sees_bad(units::tile_row<kBN>(U, j), j < U.n_a ? da : ga,
+                                j < U.n_a ? db : gb, c);
+        };
         for (int32_t j = 0; j < n; ++j, ++cnt) {
             if (!__all_sync(kAll, wait_phase(sm, sm.s_full[map], cnt & 1, err))) return;
             ptx::tc_fence_after();
-            const int32_t k0 = units::tile_row(U, j);
+            if (PACK && j > 0) check_bad(j - 1, cnt - 1);
+            const int32_t k0 = units::tile_row<kBN>(U, j);
             const int32_t klo = j < U.n_a ? da : ga, khi = j < U.n_a ? db : gb;
             const bool masked = k0 < klo || k0 + kBN > khi;
             uint32_t sr[kBN];
@@ -416,22 +453,6 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 l_run *= alpha;
                 if (j > 0) rescale_o(need, alpha);
                 sum = exp_store(std::false_type{}, sr, m_run == kNegInf ? 0.f : m_run, mx, [] {});
-                // V rows that no row of the unit may see: zeroed once, by map
-                // 0's threads (its product is issued first). V(j) is load
-                // 2 cnt + 1 of the ring, and stays until both products ran.
-                const int32_t seen = units::tile_rows(U, j);
-                if (map == 0 && seen < kBN) {
-                    const uint32_t it = 2 * cnt + 1, slot = it % kSlots;
-                    if (!__all_sync(kAll, wait_phase(sm, sm.kv_full[slot], (it / kSlots) & 1, err)))
-                        return;
-                    if (static_cast<int32_t>(r) >= seen && static_cast<int32_t>(r) < tile_cols(U, j)) {
-#pragma unroll
-                        for (int i = 0; i < HD / 64 * 8; ++i)
-                            ptx::st_shared_v4(sm.kv[slot] + (i / 8) * kBN * 128 + r * 128 +
-                                                  (i % 8) * 16, 0, 0, 0, 0);
-                    }
-                    ptx::fence_proxy_async_smem();
-                }
             } else {
                 // Exponentials against the running reference right away, the
                 // tile's maximum in the same pass; the (rare) rows whose
@@ -445,6 +466,37 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                     l_run *= alpha;
                     rescale_o(need, alpha);
                     sum = exp_store(std::false_type{}, sr, m_run, mx, [] {});
+                }
+            }
+            // V rows to zero, once for both maps, by map 0's threads (its product
+            // is issued first; thread = V row). V(j) is load 2 cnt + 1 of the
+            // ring, and stays until both products ran.
+            const int32_t seen = units::tile_rows<kBN>(U, j);
+            if (map == 0 && (seen < kBN || scanned(U, j))) {
+                const uint32_t it = 2 * cnt + 1, slot = it % kSlots;
+                if (!__all_sync(kAll, wait_phase(sm, sm.kv_full[slot], (it / kSlots) & 1, err)))
+                    return;
+                constexpr int kVecs = HD / 64 * 8;
+                auto vec = [&](int i) {   // rotated by row: no bank conflicts
+                    return sm.kv[slot] + (i / 8) * kBN * 128 + r * 128 + ((i + r) % 8) * 16;
+                };
+                const int32_t vr = static_cast<int32_t>(r);
+                bool zero = vr >= seen && vr < tile_cols(U, j);
+                if (scanned(U, j)) {
+                    bool b = false;
+                    if (vr < seen) {
+#pragma unroll
+                        for (int i = 0; i < kVecs; ++i)
+                            b |= not_finite(*reinterpret_cast<const uint4 *>(vec(i)));
+                    }
+                    const uint32_t marks = __ballot_sync(kAll, b);
+                    if ((r & 31) == 0) sm.bad[cnt & 3][r / 32] = marks;
+                    zero |= b;
+                }
+                if (zero) {
+#pragma unroll
+                    for (int i = 0; i < kVecs; ++i) ptx::st_shared_v4(vec(i), 0, 0, 0, 0);
+                    ptx::fence_proxy_async_smem();
                 }
             }
             l_run += sum;
@@ -466,7 +518,9 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                                   wait_phase(sm, sm.o_final, par, err)))
             return;
         ptx::tc_fence_after();
-        const float f1 = sm.inv_l[par][0][r], f2 = sm.inv_l[par][1][r];
+        if (PACK) check_bad(n - 1, cnt - 1);
+        const float nan = __uint_as_float(0x7fffffffu);
+        const float f1 = bad ? nan : sm.inv_l[par][0][r], f2 = bad ? nan : sm.inv_l[par][1][r];
         constexpr int kHalf = HD / 2;
         uint32_t o1[kHalf], o2[kHalf];
         const uint32_t t_o1 = tmem + kMaps * kBN + lane_sel + map * kHalf, t_o2 = t_o1 + HD;
@@ -512,7 +566,7 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
     }
 }
 
-template <int HD>
+template <int HD, bool PACK>
 __global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     Smem<HD> &sm = *reinterpret_cast<Smem<HD> *>(
@@ -562,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_const
     if (!tmem_ok && threadIdx.x == 0) atomicOr(p.err_word, kErrTmemAlloc);
     if (warp < 8) {
         ptx::setmaxnreg_inc<kRegsSoftmax>();
-        if (tmem_ok) softmax_epilogue<HD>(p, S, sm, tmem, warp / 4);
+        if (tmem_ok) softmax_epilogue<HD, PACK>(p, S, sm, tmem, warp / 4);
     } else {
         ptx::setmaxnreg_dec<kRegsOther>();
         if (tmem_ok && lane == 0) {
@@ -608,17 +662,19 @@ atlas_status launch_hd(const DiffArgs &d, const DeviceInfo &dev, cudaStream_t st
     if (!p.err_word) return ATLAS_ERR_CUDA;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.stall_unit = take_stall_request() ? 0 : -1;
+    // Packed units may occur: windows below 128 rows, or unknown ones.
+    const bool pack = p.shape.upw < 0 || (p.shape.upw == 0 && p.shape.N > 0);
     const size_t smem = sizeof(Smem<HD>) + 1024;
-    if (!set_smem_limit(reinterpret_cast<const void *>(diff_tc_kernel<HD>),
-                        static_cast<int>(smem)))
+    auto kernel = pack ? diff_tc_kernel<HD, true> : diff_tc_kernel<HD, false>;
+    if (!set_smem_limit(reinterpret_cast<const void *>(kernel), static_cast<int>(smem)))
         return ATLAS_ERR_CUDA;
     const int grid = static_cast<int>(n_units < dev.sm_count ? n_units : dev.sm_count);
     if (log_enabled())
-        log_launch("diff_tc_kernel", grid, kThreads, smem,
+        log_launch(pack ? "diff_tc_kernel<PACK>" : "diff_tc_kernel", grid, kThreads, smem,
                    "head_dim %d units %lld batch %d heads %d n_detail %d window %d n_global %d", HD,
                    static_cast<long long>(n_units), p.shape.batch, p.shape.heads, p.shape.N,
                    p.shape.L, p.shape.G);
-    diff_tc_kernel<HD><<<grid, kThreads, smem, stream>>>(p);
+    kernel<<<grid, kThreads, smem, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 
