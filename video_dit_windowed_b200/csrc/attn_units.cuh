@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include "atlas_internal.cuh"
+#include "sm100_ptx.cuh"
 
 namespace atlas {
 namespace units {
@@ -258,6 +259,17 @@ __device__ __forceinline__ void key_ranges(const Shape &p, const Unit &U, int32_
         da = db = 0;
         if (w >= 0) window_rows(p, w, da, db);
     }
+}
+
+// The fields that the tile functions above read, as uniform values of a
+// converged warp.
+__device__ __forceinline__ void make_uniform(Unit &U) {
+    U.a0 = ptx::uniform(U.a0);
+    U.a_end = ptx::uniform(U.a_end);
+    U.n_a = ptx::uniform(U.n_a);
+    U.b0 = ptx::uniform(U.b0);
+    U.b_end = ptx::uniform(U.b_end);
+    U.n_b = ptx::uniform(U.n_b);
 }
 
 // The longest window of the offsets (clamped), into *out (0 before), by all

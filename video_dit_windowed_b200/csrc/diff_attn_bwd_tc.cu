@@ -24,7 +24,7 @@
 // those compute; the products that read P and dS follow when they are stored.
 //
 // Warps (320 threads): 0-7 compute (thread = resident row = lane; warpgroup g
-// takes half of a tile's columns), 8 TMA producer, 9 MMA issuer (one thread).
+// takes half of a tile's columns), 8 TMA producer, 9 MMA issuer.
 // Pairs outside the mask: P and dS are set to 0 whatever S and dP hold. 0 * NaN
 // would still reach a row through the accumulating products' streamed operand, so
 // streamed rows that not every resident row meets are zeroed in shared memory
@@ -242,11 +242,13 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD, FORM> &sm) {
 }
 
 // ---------------------------------------------------------------------------
-// MMA issuer (one thread). Tile t: wait until tile t-1 was loaded from S, issue
+// MMA issuer: one converged warp (sm100_ptx.cuh, mma_ss_elect). Tensor memory
+// starts at column 0, so its addresses are constants. Tile t: wait until tile t-1 was loaded from S, issue
 // S and dP of t; then the products of t-1's P and dS.
 // ---------------------------------------------------------------------------
 template <int HD, int FORM>
-__device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uint32_t tmem) {
+__device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD, FORM> &sm) {
+    constexpr uint32_t tmem = 0;
     using SM = Smem<HD, FORM>;
     using TM = Tmem<HD, FORM>;
     constexpr int kStages = SM::kStages, kStream = SM::kStream;
@@ -264,8 +266,11 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD, FORM> &sm, 
     // The streamed tiles as MN-major B operands of the accumulations.
     const uint32_t xs_mn = ptx::desc_sw128_lo(ptx::smem_addr(sm.xs[0]), kPanel);
     const uint32_t ys_mn = ptx::desc_sw128_lo(ptx::smem_addr(sm.ys[0]), kPanel);
-    uint32_t it = 0, unit_iter = 0, done = 0;   // stages taken, units, tiles accumulated
+    uint32_t ring = 0, ring_phase = 0, unit_iter = 0, done = 0;   // done: tiles accumulated
     bool ok = true;
+    auto wait = [&](uint64_t &bar, uint32_t parity) -> bool {
+        return __all_sync(kAll, wait_phase(sm, bar, parity, kErrTimeoutMma));
+    };
 
     // D = A B^T over K = 16 steps [k0, k1) of the channels.
     auto product = [&](uint32_t d, uint32_t a_smem, uint32_t a_tmem, uint32_t b_lo, int k0, int k1) {
@@ -276,9 +281,9 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD, FORM> &sm, 
             const uint32_t a_off = ((ks / 4) * (kRows * 128) + (ks % 4) * 32) >> 4;
             const uint32_t b_off = ((ks / 4) * kPanel + (ks % 4) * 32) >> 4;
             if (FORM == kDQ)
-                ptx::mma_ts(d, a_tmem + ks * 8, ptx::desc_join(b_lo + b_off, kHi), kIdS, i > 0);
+                ptx::mma_ts_elect(d, a_tmem + ks * 8, ptx::desc_join(b_lo + b_off, kHi), kIdS, i > 0);
             else
-                ptx::mma_ss(d, ptx::desc_join(a_smem + a_off, kHi),
+                ptx::mma_ss_elect(d, ptx::desc_join(a_smem + a_off, kHi),
                             ptx::desc_join(b_lo + b_off, kHi), kIdS, i > 0);
         }
     };
@@ -287,46 +292,50 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD, FORM> &sm, 
         product(tmem + TM::kS, x_lo, tmem + TM::kResX, xb, 0, kMapSteps);
         product(tmem + TM::kS + 64, x_lo, tmem + TM::kResX, xb, kMapSteps, 2 * kMapSteps);
         product(tmem + TM::kDP, y_lo, tmem + TM::kResY, yb, 0, HD / 16);
-        ptx::mma_commit(ptx::smem_addr(&sm.s_full));
+        ptx::mma_commit_elect(ptx::smem_addr(&sm.s_full));
     };
     // acc += A (packed, tensor memory) B over the tile's rows.
     auto accumulate = [&](uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, bool first) {
 #pragma unroll
         for (int ks = 0; ks < kStream / 16; ++ks)
-            ptx::mma_ts(d, a + ks * 8, ptx::desc_join(b_lo + ((ks * 16 * 128) >> 4), kHi), idesc,
+            ptx::mma_ts_elect(d, a + ks * 8, ptx::desc_join(b_lo + ((ks * 16 * 128) >> 4), kHi), idesc,
                         (first && ks == 0) ? 0u : 1u);
     };
     auto next_stage = [&](uint32_t &s) -> bool {
-        s = it % kStages;
-        const bool r = wait_phase(sm, sm.st_full[s], (it / kStages) & 1, kErrTimeoutMma);
-        ++it;
+        s = ring;
+        const bool r = wait(sm.st_full[s], ring_phase);
+        if (++ring == kStages) {
+            ring = 0;
+            ring_phase ^= 1;
+        }
         return r;
     };
 
     for (int32_t u = blockIdx.x; u < S.n_units && ok; u += gridDim.x) {
-        const Unit U = unit_at<FORM>(p, S, u);
+        Unit U = unit_at<FORM>(p, S, u);
+        units::make_uniform(U);
         const int32_t n = U.n_a + U.n_b;
         if (n == 0) continue;
-        if (!(ok = wait_phase(sm, sm.x_full, unit_iter & 1, kErrTimeoutMma))) break;
+        if (!(ok = wait(sm.x_full, unit_iter & 1))) break;
         uint32_t cur, next = 0;
         if (!(ok = next_stage(cur))) break;
         // S's columns were read by the previous tile (of the previous unit).
-        if (done > 0 && !(ok = wait_phase(sm, sm.s_read, (done - 1) & 1, kErrTimeoutMma))) break;
+        if (done > 0 && !(ok = wait(sm.s_read, (done - 1) & 1))) break;
         ptx::tc_fence_after();
         issue_s(cur);
         // The resident rows are read by S and dP only.
-        if (n == 1) ptx::mma_commit(ptx::smem_addr(&sm.x_empty));
+        if (n == 1) ptx::mma_commit_elect(ptx::smem_addr(&sm.x_empty));
         for (int32_t j = 0; j < n && ok; ++j) {
             if (j + 1 < n) {
                 if (!(ok = next_stage(next))) break;
-                if (!(ok = wait_phase(sm, sm.s_read, done & 1, kErrTimeoutMma))) break;
+                if (!(ok = wait(sm.s_read, done & 1))) break;
                 ptx::tc_fence_after();
                 issue_s(next);
-                if (j + 2 == n) ptx::mma_commit(ptx::smem_addr(&sm.x_empty));
+                if (j + 2 == n) ptx::mma_commit_elect(ptx::smem_addr(&sm.x_empty));
             }
-            if (!(ok = wait_phase(sm, sm.p_full, done & 1, kErrTimeoutMma))) break;
+            if (!(ok = wait(sm.p_full, done & 1))) break;
             if (j == 0 && unit_iter > 0 &&
-                !(ok = wait_phase(sm, sm.acc_empty, (unit_iter - 1) & 1, kErrTimeoutMma)))
+                !(ok = wait(sm.acc_empty, (unit_iter - 1) & 1)))
                 break;
             ptx::tc_fence_after();
             const uint32_t xb = xs_mn + cur * kTile16, yb = ys_mn + cur * kTile16;
@@ -338,17 +347,17 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD, FORM> &sm, 
             for (int m = 0; m < 2; ++m)
                 accumulate(tmem + TM::kGrad + 64 * m, tmem + TM::kDS + m * TM::kPackedStride,
                            xb + (HD == 128 ? m * (kPanel >> 4) : 0), kIdGrad, j == 0);
-            ptx::mma_commit(ptx::smem_addr(&sm.st_empty[cur]));
-            ptx::mma_commit(ptx::smem_addr(&sm.acc_done));
+            ptx::mma_commit_elect(ptx::smem_addr(&sm.st_empty[cur]));
+            ptx::mma_commit_elect(ptx::smem_addr(&sm.acc_done));
             ++done;
             cur = next;
         }
         if (!ok) break;
-        ptx::mma_commit(ptx::smem_addr(&sm.acc_full));
+        ptx::mma_commit_elect(ptx::smem_addr(&sm.acc_full));
         ++unit_iter;
     }
     // Drain: every MMA issued must finish before tensor memory is freed.
-    ptx::mma_commit(ptx::smem_addr(&sm.drain));
+    ptx::mma_commit_elect(ptx::smem_addr(&sm.drain));
     wait_phase(sm, sm.drain, 0, kErrTimeoutTeardown, false);
 }
 
@@ -660,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_bwd_tc_kernel(const __grid_c
     if (tmem_ok) {
         if (warp < 8) compute<HD, FORM>(p, S, sm, tmem);
         else if (warp == kProducerWarp) producer<HD, FORM>(p, S, sm);
-        else if (lane == 0) mma_issuer<HD, FORM>(p, S, sm, tmem);
+        else mma_issuer<HD, FORM>(p, S, sm);
     }
     __syncwarp();
     ptx::tc_fence_before();

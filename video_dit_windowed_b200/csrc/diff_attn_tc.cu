@@ -17,7 +17,7 @@
 // head-major. Warps (384 threads):
 //   0-3 / 4-7  softmax of map 1 / 2 (thread = query row = TMEM lane); in the
 //              epilogue each group joins half of the output's columns,
-//   8          TMA producer, 9  MMA issuer (one thread), 10-11  idle.
+//   8          TMA producer, 9  MMA issuer, 10-11  idle.
 // Tensor memory: S_1 | S_2 (128 columns each) | O_1 | O_2 (D each); P (bf16) goes
 // over the first half of its S. Issue order per key tile j:
 //   O_1 += P_1(j) V(j), S_1(j+1), O_2 += P_2(j) V(j), S_2(j+1);
@@ -198,10 +198,12 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD> &sm) {
 }
 
 // ---------------------------------------------------------------------------
-// MMA issuer (one thread).
+// MMA issuer: one converged warp (sm100_ptx.cuh, mma_ss_elect). Tensor memory
+// starts at column 0, so its addresses are constants.
 // ---------------------------------------------------------------------------
 template <int HD>
-__device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm, uint32_t tmem) {
+__device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm) {
+    constexpr uint32_t tmem = 0;
     constexpr int kSlots = Smem<HD>::kSlots;
     constexpr int kMapSteps = HD / 32;   // K = 16 steps of one map's channels
     constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, kBN, 0);
@@ -213,13 +215,19 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm, uint32
     const uint32_t q_lo = ptx::desc_sw128_lo(ptx::smem_addr(sm.q), 16);
     const uint32_t k_lo0 = ptx::desc_sw128_lo(ptx::smem_addr(sm.kv[0]), 16);
     const uint32_t v_lo0 = ptx::desc_sw128_lo(ptx::smem_addr(sm.kv[0]), kBN * 128);
-    uint32_t it = 0, unit_iter = 0, p_cnt = 0;
+    uint32_t ring = 0, ring_phase = 0, unit_iter = 0, p_cnt = 0;
     bool ok = true;
 
+    auto wait = [&](uint64_t &bar, uint32_t parity) -> bool {
+        return __all_sync(kAll, wait_phase(sm, bar, parity, kErrTimeoutMma));
+    };
     auto next_slot = [&](uint32_t &slot) -> bool {
-        slot = it % kSlots;
-        const bool r = wait_phase(sm, sm.kv_full[slot], (it / kSlots) & 1, kErrTimeoutMma);
-        ++it;
+        slot = ring;
+        const bool r = wait(sm.kv_full[slot], ring_phase);
+        if (++ring == kSlots) {
+            ring = 0;
+            ring_phase ^= 1;
+        }
         ptx::tc_fence_after();
         return r;
     };
@@ -233,49 +241,50 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm, uint32
         for (int i = 0; i < kMapSteps; ++i) {
             const int ks = m * kMapSteps + i;
             const uint32_t off = ((ks / 4) * (kBM * 128) + (ks % 4) * 32) >> 4;
-            ptx::mma_ss(d_s, ptx::desc_join(q_lo + off, kHi), ptx::desc_join(k_lo + off, kHi),
+            ptx::mma_ss_elect(d_s, ptx::desc_join(q_lo + off, kHi), ptx::desc_join(k_lo + off, kHi),
                         idesc, i > 0);
         }
-        ptx::mma_commit(ptx::smem_addr(&sm.s_full[m]));
+        ptx::mma_commit_elect(ptx::smem_addr(&sm.s_full[m]));
     };
     // O_m += P_m V, P_m from tensor memory; the tile's first nc keys.
     auto issue_pv = [&](int m, uint32_t v_slot, bool first, int32_t nc) -> bool {
-        if (!wait_phase(sm, sm.p_full[m], p_cnt & 1, kErrTimeoutMma)) return false;
+        if (!wait(sm.p_full[m], p_cnt & 1)) return false;
         ptx::tc_fence_after();
         const uint32_t v_lo = v_lo0 + v_slot * kTile16;
         const uint32_t d_o = tmem + kMaps * kBN + m * HD, a_p = tmem + m * kBN;
-        ptx::mma_ts(d_o, a_p, ptx::desc_join(v_lo, kHi), kIdescPV, first ? 0u : 1u);
+        ptx::mma_ts_elect(d_o, a_p, ptx::desc_join(v_lo, kHi), kIdescPV, first ? 0u : 1u);
         if (nc == kBN) {
 #pragma unroll
             for (int ks = 1; ks < kBN / 16; ++ks)
-                ptx::mma_ts(d_o, a_p + ks * 8,
+                ptx::mma_ts_elect(d_o, a_p + ks * 8,
                             ptx::desc_join(v_lo + ((ks * 16 * 128) >> 4), kHi), kIdescPV, 1u);
         } else {
 #pragma unroll 1
             for (int ks = 1; ks * 16 < nc; ++ks)
-                ptx::mma_ts(d_o, a_p + ks * 8,
+                ptx::mma_ts_elect(d_o, a_p + ks * 8,
                             ptx::desc_join(v_lo + ((ks * 16 * 128) >> 4), kHi), kIdescPV, 1u);
         }
         return true;
     };
 
     for (int32_t u = blockIdx.x; u < S.n_units && ok; u += gridDim.x) {
-        const Unit U = units::query_unit<kBN>(p.shape, S, u);
+        Unit U = units::query_unit<kBN>(p.shape, S, u);
+        units::make_uniform(U);
         const int32_t n = U.n_a + U.n_b;
         if (n == 0) continue;
-        if (!(ok = wait_phase(sm, sm.q_full, unit_iter & 1, kErrTimeoutMma))) break;
+        if (!(ok = wait(sm.q_full, unit_iter & 1))) break;
         ptx::tc_fence_after();
         uint32_t k_slot, v_slot;
         if (!(ok = next_slot(k_slot))) break;
         int32_t nc = tile_cols(U, 0);
         issue_s(0, k_slot, nc);
         issue_s(1, k_slot, nc);
-        ptx::mma_commit(ptx::smem_addr(&sm.kv_empty[k_slot]));
+        ptx::mma_commit_elect(ptx::smem_addr(&sm.kv_empty[k_slot]));
         // Only the S MMAs read Q: after the unit's last one it is free.
-        if (n == 1) ptx::mma_commit(ptx::smem_addr(&sm.q_empty));
+        if (n == 1) ptx::mma_commit_elect(ptx::smem_addr(&sm.q_empty));
         // The accumulators of the previous unit have been read.
         if (unit_iter > 0 &&
-            !(ok = wait_phase(sm, sm.o_empty, (unit_iter - 1) & 1, kErrTimeoutMma)))
+            !(ok = wait(sm.o_empty, (unit_iter - 1) & 1)))
             break;
         for (int32_t j = 0; j < n && ok; ++j) {
             const bool more = j + 1 < n;
@@ -288,19 +297,19 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm, uint32
             if (!(ok = issue_pv(1, v_slot, j == 0, nc))) break;
             if (more) {
                 issue_s(1, k_slot, nc_next);
-                ptx::mma_commit(ptx::smem_addr(&sm.kv_empty[k_slot]));
-                if (j + 2 == n) ptx::mma_commit(ptx::smem_addr(&sm.q_empty));
+                ptx::mma_commit_elect(ptx::smem_addr(&sm.kv_empty[k_slot]));
+                if (j + 2 == n) ptx::mma_commit_elect(ptx::smem_addr(&sm.q_empty));
             }
             nc = nc_next;
-            ptx::mma_commit(ptx::smem_addr(&sm.kv_empty[v_slot]));
+            ptx::mma_commit_elect(ptx::smem_addr(&sm.kv_empty[v_slot]));
             ++p_cnt;
         }
         if (!ok) break;
-        ptx::mma_commit(ptx::smem_addr(&sm.o_final));
+        ptx::mma_commit_elect(ptx::smem_addr(&sm.o_final));
         ++unit_iter;
     }
     // Drain: every MMA issued must finish before tensor memory is freed.
-    ptx::mma_commit(ptx::smem_addr(&sm.drain));
+    ptx::mma_commit_elect(ptx::smem_addr(&sm.drain));
     wait_phase(sm, sm.drain, 0, kErrTimeoutTeardown, false);
 }
 
@@ -619,10 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_const
         if (tmem_ok) softmax_epilogue<HD, PACK>(p, S, sm, tmem, warp / 4);
     } else {
         ptx::setmaxnreg_dec<kRegsOther>();
-        if (tmem_ok && lane == 0) {
-            if (warp == kProducerWarp) producer<HD>(p, S, sm);
-            if (warp == kMmaWarp) mma_issuer<HD>(p, S, sm, tmem);
-        }
+        if (tmem_ok && warp == kProducerWarp && lane == 0) producer<HD>(p, S, sm);
+        if (tmem_ok && warp == kMmaWarp) mma_issuer<HD>(p, S, sm);
     }
     __syncwarp();
     ptx::tc_fence_before();

@@ -130,6 +130,38 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         :: "r"(bar) : "memory");
 }
 
+// The same, issued by one elected lane of a converged warp. A warp that runs the
+// issue loop together keeps descriptors and addresses in uniform registers, the
+// operands these instructions take; a single thread's loop moves each of them
+// there, and beside busy warps that takes longer than the MMA: measured with eight
+// warps of arithmetic on the SM, 78 clk per MMA from a single thread for any N up
+// to 128, 38 (N = 64, A in tensor memory), 48 (N = 64) and 65 (N = 128) from a
+// converged warp (32, 32 and 64 ideal).
+__device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_commit_elect(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        :: "r"(bar) : "memory");
+}
+// A value that every lane holds, as one the compiler knows to be uniform.
+__device__ __forceinline__ int32_t uniform(int32_t x) {
+    return __reduce_max_sync(0xffffffffu, x);
+}
+
 // ---- tcgen05: tensor memory <-> registers --------------------------------------
 // 32 lanes x 32 consecutive 32-bit columns; thread i of the warp gets lane
 // (base lane + i), columns col .. col+31. The wait is in the same asm
