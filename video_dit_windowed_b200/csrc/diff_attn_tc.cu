@@ -18,11 +18,17 @@
 //   0-3 / 4-7  softmax of map 1 / 2 (thread = query row = TMEM lane); in the
 //              epilogue each group joins half of the output's columns,
 //   8          TMA producer, 9  MMA issuer, 10-11  idle.
-// Tensor memory: S_1 | S_2 (128 columns each) | O_1 | O_2 (D each); P (bf16) goes
-// over the first half of its S. Issue order per key tile j:
-//   O_1 += P_1(j) V(j), S_1(j+1), O_2 += P_2(j) V(j), S_2(j+1);
-// one thread's MMAs run in order, so S_m(j+1) overwrites P_m(j) only after it
-// was read. Masked keys: their logits are set to -inf whatever they hold; 0 * NaN
+// Tensor memory: two 64-column regions per map, then O_1 | O_2 (D each). A tile's
+// logits come in two halves: keys 0-63 in one region, keys 64-127 in the other;
+// P (bf16, 64 columns) overwrites the first half's region. Once the second half has
+// been loaded its region is free, so the next tile's first half is computed there
+// while this tile's exponentials still run, and its second half follows P V into
+// the region of P; regions swap roles every tile. A softmax therefore finds its
+// next 64 keys waiting and never sits out its own P V. (With one 128-column S per
+// map, whose next tile can only follow P V, a tile took 4020 clk; the exponentials
+// are 2048.) Issue order per key tile j, for each map:
+//   S(j+1) first half, O += P(j) V(j), S(j+1) second half.
+// Masked keys: their logits are set to -inf whatever they hold; 0 * NaN
 // would still reach a row through P V, so the V rows past the unit's range are
 // zeroed in shared memory before the product. In packed units (PACK), whose rows
 // see different windows, so are V rows with a non-finite value, and the rows that
@@ -69,7 +75,9 @@ struct Smem {
     uint32_t bad[4][4];          // PACK: non-finite V rows of the last four tiles
     uint64_t q_full, q_empty;
     uint64_t kv_full[kSlots], kv_empty[kSlots];
-    uint64_t s_full[kMaps];      // S_m(j) in TMEM, O_m += P_m(j-1) V done  (commit)
+    uint64_t s_lo[kMaps];        // first half of S_m(j) in TMEM            (commit)
+    uint64_t s_hi[kMaps];        // second half, and O_m += P_m(j-1) V done (commit)
+    uint64_t s_read[kMaps];      // second half loaded                      (128 arrivals)
     uint64_t p_full[kMaps];      // P_m(j) in TMEM, O_m rescaled            (128 arrivals)
     uint64_t o_final;            // every MMA of the unit done              (commit)
     uint64_t joined;             // both maps' inv_l written                (256 arrivals)
@@ -123,12 +131,14 @@ __device__ __forceinline__ bool not_finite(const uint4 &v) {
     return bad;
 }
 
-// Columns of key tile j that can hold an allowed key: its MMAs take 32, 64 or
-// all kBN of them; the S columns beyond are stale and never used.
-__device__ __forceinline__ int32_t tile_cols(const Unit &U, int32_t j) {
-    const int32_t n = units::tile_rows<kBN>(U, j);
-    return n <= 32 ? 32 : (n <= 64 ? 64 : kBN);
+// K = 16 steps of P V that hold an allowed key of tile j. A tile of at most 64
+// keys also skips the second half of S (stale columns, masked).
+__device__ __forceinline__ int32_t tile_steps(const Unit &U, int32_t j) {
+    return (min(units::tile_rows<kBN>(U, j), kBN) + 15) / 16;
 }
+// First column of the region of tile c's first half (and of its P); the second
+// half has the other region.
+__device__ __forceinline__ uint32_t lo_region(uint32_t c) { return (c & 1) * 64; }
 
 // ---------------------------------------------------------------------------
 // Producer: Q once per unit, then K(0), V(0), K(1), V(1), ...
@@ -203,23 +213,22 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD> &sm) {
 // ---------------------------------------------------------------------------
 template <int HD>
 __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm) {
-    constexpr uint32_t tmem = 0;
     constexpr int kSlots = Smem<HD>::kSlots;
     constexpr int kMapSteps = HD / 32;   // K = 16 steps of one map's channels
-    constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, kBN, 0);
-    constexpr uint32_t kIdescQK64 = ptx::idesc_bf16_f32(kBM, 64, 0);
-    constexpr uint32_t kIdescQK32 = ptx::idesc_bf16_f32(kBM, 32, 0);
+    constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, 64, 0);
     constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, HD, 1);
     constexpr uint32_t kHi = ptx::desc_sw128_hi(1024);
     constexpr uint32_t kTile16 = Smem<HD>::kTileBytes >> 4;
     const uint32_t q_lo = ptx::desc_sw128_lo(ptx::smem_addr(sm.q), 16);
     const uint32_t k_lo0 = ptx::desc_sw128_lo(ptx::smem_addr(sm.kv[0]), 16);
     const uint32_t v_lo0 = ptx::desc_sw128_lo(ptx::smem_addr(sm.kv[0]), kBN * 128);
-    uint32_t ring = 0, ring_phase = 0, unit_iter = 0, p_cnt = 0;
+    uint32_t ring = 0, ring_phase = 0, unit_iter = 0, c = 0;   // c: key tiles
     bool ok = true;
 
     auto wait = [&](uint64_t &bar, uint32_t parity) -> bool {
-        return __all_sync(kAll, wait_phase(sm, bar, parity, kErrTimeoutMma));
+        const bool r = __all_sync(kAll, wait_phase(sm, bar, parity, kErrTimeoutMma));
+        ptx::tc_fence_after();
+        return r;
     };
     auto next_slot = [&](uint32_t &slot) -> bool {
         slot = ring;
@@ -228,43 +237,39 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm) {
             ring = 0;
             ring_phase ^= 1;
         }
-        ptx::tc_fence_after();
         return r;
     };
-    // S_m = Q_m K_m^T for the tile's first nc keys: map m's channels are the
-    // K = 16 steps m * kMapSteps .. of the tile (64-channel panels of 128-byte
-    // rows, four steps each).
-    auto issue_s = [&](int m, uint32_t k_slot, int32_t nc) {
-        const uint32_t k_lo = k_lo0 + k_slot * kTile16, d_s = tmem + m * kBN;
-        const uint32_t idesc = nc == kBN ? kIdescQK : (nc == 64 ? kIdescQK64 : kIdescQK32);
+    // Half `hi` of S_m = Q_m K_m^T for tile t: map m's channels are the K = 16
+    // steps m * kMapSteps .. of the tile (64-channel panels of 128-byte rows,
+    // four steps each), its keys rows 64 hi .. of K.
+    auto issue_s = [&](int m, int hi, uint32_t t, uint32_t k_slot) {
+        const uint32_t k_lo = k_lo0 + k_slot * kTile16 + ((hi * 64 * 128) >> 4);
+        const uint32_t d_s = m * kBN + (hi ? 64 - lo_region(t) : lo_region(t));
 #pragma unroll
         for (int i = 0; i < kMapSteps; ++i) {
             const int ks = m * kMapSteps + i;
             const uint32_t off = ((ks / 4) * (kBM * 128) + (ks % 4) * 32) >> 4;
-            ptx::mma_ss_elect(d_s, ptx::desc_join(q_lo + off, kHi), ptx::desc_join(k_lo + off, kHi),
-                        idesc, i > 0);
+            ptx::mma_ss_elect(d_s, ptx::desc_join(q_lo + off, kHi),
+                              ptx::desc_join(k_lo + off, kHi), kIdescQK, i > 0);
         }
-        ptx::mma_commit_elect(ptx::smem_addr(&sm.s_full[m]));
     };
-    // O_m += P_m V, P_m from tensor memory; the tile's first nc keys.
-    auto issue_pv = [&](int m, uint32_t v_slot, bool first, int32_t nc) -> bool {
-        if (!wait(sm.p_full[m], p_cnt & 1)) return false;
-        ptx::tc_fence_after();
+    // O_m += P_m V, P_m from tensor memory, over `steps` K = 16 steps.
+    auto issue_pv = [&](int m, uint32_t v_slot, bool first, int32_t steps) {
         const uint32_t v_lo = v_lo0 + v_slot * kTile16;
-        const uint32_t d_o = tmem + kMaps * kBN + m * HD, a_p = tmem + m * kBN;
-        ptx::mma_ts_elect(d_o, a_p, ptx::desc_join(v_lo, kHi), kIdescPV, first ? 0u : 1u);
-        if (nc == kBN) {
+        const uint32_t d_o = kMaps * kBN + m * HD, a_p = m * kBN + lo_region(c);
+        if (steps == kBN / 16) {
 #pragma unroll
-            for (int ks = 1; ks < kBN / 16; ++ks)
+            for (int ks = 0; ks < kBN / 16; ++ks)
                 ptx::mma_ts_elect(d_o, a_p + ks * 8,
-                            ptx::desc_join(v_lo + ((ks * 16 * 128) >> 4), kHi), kIdescPV, 1u);
+                                  ptx::desc_join(v_lo + ((ks * 16 * 128) >> 4), kHi), kIdescPV,
+                                  (first && ks == 0) ? 0u : 1u);
         } else {
 #pragma unroll 1
-            for (int ks = 1; ks * 16 < nc; ++ks)
+            for (int ks = 0; ks < steps; ++ks)
                 ptx::mma_ts_elect(d_o, a_p + ks * 8,
-                            ptx::desc_join(v_lo + ((ks * 16 * 128) >> 4), kHi), kIdescPV, 1u);
+                                  ptx::desc_join(v_lo + ((ks * 16 * 128) >> 4), kHi), kIdescPV,
+                                  (first && ks == 0) ? 0u : 1u);
         }
-        return true;
     };
 
     for (int32_t u = blockIdx.x; u < S.n_units && ok; u += gridDim.x) {
@@ -272,37 +277,51 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm) {
         units::make_uniform(U);
         const int32_t n = U.n_a + U.n_b;
         if (n == 0) continue;
-        if (!(ok = wait(sm.q_full, unit_iter & 1))) break;
-        ptx::tc_fence_after();
         uint32_t k_slot, v_slot;
-        if (!(ok = next_slot(k_slot))) break;
-        int32_t nc = tile_cols(U, 0);
-        issue_s(0, k_slot, nc);
-        issue_s(1, k_slot, nc);
+        if (!(ok = wait(sm.q_full, unit_iter & 1)) || !(ok = next_slot(k_slot))) break;
+        int32_t steps = tile_steps(U, 0);
+        for (int m = 0; m < kMaps && ok; ++m) {
+            // Both regions: the previous unit's last S was loaded, and its P V
+            // is ahead in the queue.
+            if (c > 0 && !(ok = wait(sm.s_read[m], (c - 1) & 1))) break;
+            issue_s(m, 0, c, k_slot);
+            ptx::mma_commit_elect(ptx::smem_addr(&sm.s_lo[m]));
+            if (steps > 4) issue_s(m, 1, c, k_slot);
+            ptx::mma_commit_elect(ptx::smem_addr(&sm.s_hi[m]));
+        }
+        if (!ok) break;
         ptx::mma_commit_elect(ptx::smem_addr(&sm.kv_empty[k_slot]));
         // Only the S MMAs read Q: after the unit's last one it is free.
         if (n == 1) ptx::mma_commit_elect(ptx::smem_addr(&sm.q_empty));
         // The accumulators of the previous unit have been read.
-        if (unit_iter > 0 &&
-            !(ok = wait(sm.o_empty, (unit_iter - 1) & 1)))
-            break;
+        if (unit_iter > 0 && !(ok = wait(sm.o_empty, (unit_iter - 1) & 1))) break;
         for (int32_t j = 0; j < n && ok; ++j) {
             const bool more = j + 1 < n;
-            const int32_t nc_next = more ? tile_cols(U, j + 1) : 0;
-            if (!(ok = next_slot(v_slot)) || !(ok = issue_pv(0, v_slot, j == 0, nc))) break;
-            if (more) {
-                if (!(ok = next_slot(k_slot))) break;
-                issue_s(0, k_slot, nc_next);
+            const int32_t next_steps = more ? tile_steps(U, j + 1) : 0;
+            // ring order: V(j) was loaded before K(j+1)
+            if (!(ok = next_slot(v_slot))) break;
+            if (more && !(ok = next_slot(k_slot))) break;
+            for (int m = 0; m < kMaps && ok; ++m) {
+                if (more) {
+                    if (!(ok = wait(sm.s_read[m], c & 1))) break;
+                    issue_s(m, 0, c + 1, k_slot);
+                    ptx::mma_commit_elect(ptx::smem_addr(&sm.s_lo[m]));
+                }
+                if (!(ok = wait(sm.p_full[m], c & 1))) break;
+                issue_pv(m, v_slot, j == 0, steps);
+                if (more) {
+                    if (next_steps > 4) issue_s(m, 1, c + 1, k_slot);
+                    ptx::mma_commit_elect(ptx::smem_addr(&sm.s_hi[m]));
+                }
             }
-            if (!(ok = issue_pv(1, v_slot, j == 0, nc))) break;
+            if (!ok) break;
+            ptx::mma_commit_elect(ptx::smem_addr(&sm.kv_empty[v_slot]));
             if (more) {
-                issue_s(1, k_slot, nc_next);
                 ptx::mma_commit_elect(ptx::smem_addr(&sm.kv_empty[k_slot]));
                 if (j + 2 == n) ptx::mma_commit_elect(ptx::smem_addr(&sm.q_empty));
             }
-            nc = nc_next;
-            ptx::mma_commit_elect(ptx::smem_addr(&sm.kv_empty[v_slot]));
-            ++p_cnt;
+            steps = next_steps;
+            ++c;
         }
         if (!ok) break;
         ptx::mma_commit_elect(ptx::smem_addr(&sm.o_final));
@@ -322,67 +341,45 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
     constexpr int kSlots = Smem<HD>::kSlots;
     const uint32_t r = threadIdx.x & 127;
     const uint32_t lane_sel = ((threadIdx.x / 32) & 3) * (32u << 16);
-    const uint32_t t_s = tmem + map * kBN + lane_sel;      // S, then P over its first half
+    const uint32_t t_s = tmem + map * kBN + lane_sel;
     const uint32_t t_o = tmem + kMaps * kBN + map * HD + lane_sel;
     const uint32_t err = kErrTimeoutSoftmax;
     const float sc = p.scale_log2;
 
-    // P = exp2(S*scale*log2e - m) as bf16 pairs into tensor memory; returns the
-    // row sum of the fp32 P (rounding P to bf16 halves the product's operand
-    // and is 2^-8 of each weight; the sum keeps fp32). with_max: the row maximum
-    // of the raw S, taken in the same pass, into mx.
-    auto exp_store = [&](auto with_max, const uint32_t (&sr)[kBN], float m, float &mx,
-                         auto &&between) -> float {
+    // 64 keys: P = exp2(S*scale*log2e - m) as bf16 pairs into 32 columns of
+    // tensor memory (rounding P halves the product's operand and is 2^-8 of each
+    // weight; the row sum adds the fp32 P). with_max: the maximum of the raw S
+    // joins mx4.
+    auto exp_store = [&](auto with_max, const uint32_t (&sr)[64], float m, uint32_t dst,
+                         float (&sum4)[4], float (&mx4)[4]) {
         constexpr bool kWithMax = decltype(with_max)::value;
-        float sum8[8], m8[8];
+        uint32_t pk[32];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            sum8[k] = 0.f;
-            m8[k] = kNegInf;
+        for (int e = 0; e < 32; ++e) {
+            const float s0 = __uint_as_float(sr[2 * e]), s1 = __uint_as_float(sr[2 * e + 1]);
+            if constexpr (kWithMax) mx4[e & 3] = ptx::max3(mx4[e & 3], s0, s1);
+            const float p0 = ptx::ex2(fmaf(s0, sc, -m));
+            const float p1 = ptx::ex2(fmaf(s1, sc, -m));
+            sum4[e & 3] += p0 + p1;
+            pk[e] = ptx::pack_bf16x2(p0, p1);
         }
-#pragma unroll
-        for (int g = 0; g < kBN / 64; ++g) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int c = g * 64 + 2 * e;
-                const float s0 = __uint_as_float(sr[c]), s1 = __uint_as_float(sr[c + 1]);
-                if constexpr (kWithMax) m8[e & 7] = ptx::max3(m8[e & 7], s0, s1);
-                const float p0 = ptx::ex2(fmaf(s0, sc, -m));
-                const float p1 = ptx::ex2(fmaf(s1, sc, -m));
-                sum8[e & 7] += p0 + p1;
-                pk[e] = ptx::pack_bf16x2(p0, p1);
-            }
-            ptx::tmem_st32_nowait(t_s + g * 32, pk);
-            if (g == 0) between();
-        }
-        ptx::tmem_wait_st();
-#pragma unroll
-        for (int w = 4; w >= 1; w >>= 1)
-#pragma unroll
-            for (int k = 0; k < w; ++k) {
-                sum8[k] += sum8[k + w];
-                if constexpr (kWithMax) m8[k] = fmaxf(m8[k], m8[k + w]);
-            }
-        if constexpr (kWithMax) mx = m8[0];
-        return sum8[0];
+        ptx::tmem_st32_nowait(dst, pk);
     };
-    auto row_max = [&](const uint32_t (&sr)[kBN]) -> float {
-        float m8[8];
+    auto row_max = [&](const uint32_t (&sr)[64]) -> float {
+        float m4[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) m8[k] = __uint_as_float(sr[k]);
+        for (int k = 0; k < 4; ++k) m4[k] = __uint_as_float(sr[k]);
 #pragma unroll
-        for (int c = 8; c + 16 <= kBN; c += 16)
+        for (int c = 4; c < 60; c += 8)
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                m8[k] = ptx::max3(m8[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
+            for (int k = 0; k < 4; ++k)
+                m4[k] = ptx::max3(m4[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 4 + k]));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) m8[k] = fmaxf(m8[k], __uint_as_float(sr[kBN - 8 + k]));
-        return ptx::max3(ptx::max3(m8[0], m8[1], m8[2]), ptx::max3(m8[3], m8[4], m8[5]),
-                         fmaxf(m8[6], m8[7]));
+        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], __uint_as_float(sr[60 + k]));
+        return fmaxf(ptx::max3(m4[0], m4[1], m4[2]), m4[3]);
     };
-    // O *= alpha, in warps where some row moved its reference. The P*V of the
-    // previous tile is done: the commit that signalled this S covers it.
+    // O *= alpha, in warps where some row moved its reference. The P V of the
+    // previous tile is done: the commit that signalled s_hi covers it.
     auto rescale_o = [&](bool need, float alpha) {
         if (!__any_sync(kAll, need)) return;
 #pragma unroll 1
@@ -423,60 +420,69 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
         float m_run = kNegInf, l_run = 0.f;
         bool bad = false;
         // The marks of tile j (tile count c): map 0's threads wrote them before
-        // its product was issued, which S of the next tile and o_final follow.
+        // its product was issued, which s_hi of the next tile and o_final follow.
         auto check_bad = [&](int32_t j, uint32_t c) {
             if (scanned(U, j))
                 bad |= sees_bad(units::tile_row<kBN>(U, j), j < U.n_a ? da : ga,
                                 j < U.n_a ? db : gb, c);
         };
         for (int32_t j = 0; j < n; ++j, ++cnt) {
-            if (!__all_sync(kAll, wait_phase(sm, sm.s_full[map], cnt & 1, err))) return;
+            if (!__all_sync(kAll, wait_phase(sm, sm.s_lo[map], cnt & 1, err))) return;
             ptx::tc_fence_after();
-            if (PACK && j > 0) check_bad(j - 1, cnt - 1);
             const int32_t k0 = units::tile_row<kBN>(U, j);
             const int32_t klo = j < U.n_a ? da : ga, khi = j < U.n_a ? db : gb;
             const bool masked = k0 < klo || k0 + kBN > khi;
-            uint32_t sr[kBN];
-            ptx::tmem_ld64(t_s, *reinterpret_cast<uint32_t(*)[64]>(&sr[0]));
-            ptx::tmem_ld64_nowait(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&sr[64]));
-            auto wait_hi = [&] { ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[64]>(&sr[64])); };
-            float sum, mx;
-            if (__any_sync(kAll, m_run == kNegInf || masked)) {
-                wait_hi();
+            const uint32_t t_lo = t_s + lo_region(cnt), t_hi = t_s + 64 - lo_region(cnt);
+            uint32_t lo[64], hi[64];
+            float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+            float mx4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+            ptx::tmem_ld64(t_lo, lo);
+            const bool slow = __any_sync(kAll, m_run == kNegInf || masked);
+            // Exponentials of the first half against the running reference right
+            // away, the maximum in the same pass.
+            if (!slow) exp_store(std::true_type{}, lo, m_run, t_lo, sum4, mx4);
+            if (!__all_sync(kAll, wait_phase(sm, sm.s_hi[map], cnt & 1, err))) return;
+            ptx::tc_fence_after();
+            ptx::tmem_ld64(t_hi, hi);
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(ptx::smem_addr(&sm.s_read[map]));
+            if (PACK && j > 0) check_bad(j - 1, cnt - 1);
+            float mx2;   // the tile's maximum
+            if (!slow) {
+                exp_store(std::true_type{}, hi, m_run, t_lo + 32, sum4, mx4);
+                mx2 = fmaxf(ptx::max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * sc;
+            } else {
                 if (masked) {
 #pragma unroll
-                    for (int c = 0; c < kBN; ++c)
-                        if (k0 + c < klo || k0 + c >= khi) sr[c] = __float_as_uint(kNegInf);
+                    for (int e = 0; e < 64; ++e) {
+                        if (k0 + e < klo || k0 + e >= khi) lo[e] = __float_as_uint(kNegInf);
+                        if (k0 + 64 + e < klo || k0 + 64 + e >= khi)
+                            hi[e] = __float_as_uint(kNegInf);
+                    }
                 }
-                // The reference moves only when the tile's maximum exceeds it
-                // by more than the threshold (exact either way: O and l share
-                // it).
-                const float mx2 = row_max(sr) * sc;
-                const bool need = m_run == kNegInf ? mx2 != kNegInf
-                                                   : mx2 > m_run + kRescaleThreshold;
+                mx2 = fmaxf(row_max(lo), row_max(hi)) * sc;
+            }
+            // The reference moves only when the tile's maximum exceeds it by more
+            // than the threshold (exact either way: O and l share it); then, and
+            // on the slow path, the tile's exponentials are taken (again).
+            const bool need = m_run == kNegInf ? mx2 != kNegInf : mx2 > m_run + kRescaleThreshold;
+            if (slow || __any_sync(kAll, need)) {
                 float alpha = 1.f;
                 if (need) {
                     alpha = m_run == kNegInf ? 0.f : ptx::ex2(m_run - mx2);
                     m_run = mx2;
                 }
                 l_run *= alpha;
+                ptx::tmem_wait_st();   // the stores that the next ones replace
                 if (j > 0) rescale_o(need, alpha);
-                sum = exp_store(std::false_type{}, sr, m_run == kNegInf ? 0.f : m_run, mx, [] {});
-            } else {
-                // Exponentials against the running reference right away, the
-                // tile's maximum in the same pass; the (rare) rows whose
-                // maximum moved past the threshold are redone.
-                sum = exp_store(std::true_type{}, sr, m_run, mx, wait_hi);
-                const float mx2 = mx * sc;
-                const bool need = mx2 > m_run + kRescaleThreshold;
-                if (__any_sync(kAll, need)) {
-                    const float alpha = need ? ptx::ex2(m_run - mx2) : 1.f;
-                    if (need) m_run = mx2;
-                    l_run *= alpha;
-                    rescale_o(need, alpha);
-                    sum = exp_store(std::false_type{}, sr, m_run, mx, [] {});
-                }
+                const float m = m_run == kNegInf ? 0.f : m_run;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum4[k] = 0.f;
+                exp_store(std::false_type{}, lo, m, t_lo, sum4, mx4);
+                exp_store(std::false_type{}, hi, m, t_lo + 32, sum4, mx4);
             }
+            ptx::tmem_wait_st();
+            const float sum = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
             // V rows to zero, once for both maps, by map 0's threads (its product
             // is issued first; thread = V row). V(j) is load 2 cnt + 1 of the
             // ring, and stays until both products ran.
@@ -490,7 +496,7 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                     return sm.kv[slot] + (i / 8) * kBN * 128 + r * 128 + ((i + r) % 8) * 16;
                 };
                 const int32_t vr = static_cast<int32_t>(r);
-                bool zero = vr >= seen && vr < tile_cols(U, j);
+                bool zero = vr >= seen && vr < 16 * tile_steps(U, j);
                 if (scanned(U, j)) {
                     bool b = false;
                     if (vr < seen) {
@@ -589,7 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_const
             ptx::mbar_init(ptx::smem_addr(&sm.kv_empty[s]), 1);
         }
         for (int m = 0; m < kMaps; ++m) {
-            ptx::mbar_init(ptx::smem_addr(&sm.s_full[m]), 1);
+            ptx::mbar_init(ptx::smem_addr(&sm.s_lo[m]), 1);
+            ptx::mbar_init(ptx::smem_addr(&sm.s_hi[m]), 1);
+            ptx::mbar_init(ptx::smem_addr(&sm.s_read[m]), kBM);
             ptx::mbar_init(ptx::smem_addr(&sm.p_full[m]), kBM);
         }
         ptx::mbar_init(ptx::smem_addr(&sm.o_final), 1);
