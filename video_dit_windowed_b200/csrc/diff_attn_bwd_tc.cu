@@ -23,8 +23,9 @@
 // issued as soon as the compute threads have loaded this tile's, and run while
 // those compute; the products that read P and dS follow when they are stored.
 //
-// Warps (320 threads): 0-7 compute (thread = resident row = lane; warpgroup g
-// takes half of a tile's columns), 8 TMA producer, 9 MMA issuer.
+// Warps (352 threads): 0-7 compute (thread = resident row = lane; warpgroup g
+// takes half of a tile's columns), 8 TMA producer, 9 / 10 MMA issuers (S and dP;
+// the accumulating products).
 // Pairs outside the mask: P and dS are set to 0 whatever S and dP hold. 0 * NaN
 // would still reach a row through the accumulating products' streamed operand, so
 // streamed rows that not every resident row meets are zeroed in shared memory
@@ -50,7 +51,7 @@ constexpr int kRows = units::kRows;
 constexpr int kCompute = 256;
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -97,7 +98,7 @@ struct Smem {
     uint64_t p_full;     // packed P / dS in TMEM                    (256 arrivals)
     uint64_t acc_done;   // the products that read them are done     (commit)
     uint64_t acc_full, acc_empty;
-    uint64_t drain;
+    uint64_t drain[2];
     uint32_t tmem_base;
     int32_t max_len;
     volatile int abort;
@@ -242,13 +243,14 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD, FORM> &sm) {
 }
 
 // ---------------------------------------------------------------------------
-// MMA issuer: one converged warp (sm100_ptx.cuh, mma_ss_elect). Tensor memory
-// starts at column 0, so its addresses are constants. Tile t: wait until tile t-1 was loaded from S, issue
-// S and dP of t; then the products of t-1's P and dS.
+// MMA issuers, each one converged warp (sm100_ptx.cuh, mma_ss_elect): S and dP of
+// tile t as soon as tile t-1 was loaded; the products of P and dS when they are
+// stored. They share no accumulator, and each one's waits and issues take the
+// time of the other's MMAs. Tensor memory starts at column 0, so its addresses
+// are constants.
 // ---------------------------------------------------------------------------
 template <int HD, int FORM>
-__device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD, FORM> &sm) {
-    constexpr uint32_t tmem = 0;
+__device__ void score_issuer(const Params &p, const Sched &S, Smem<HD, FORM> &sm) {
     using SM = Smem<HD, FORM>;
     using TM = Tmem<HD, FORM>;
     constexpr int kStages = SM::kStages, kStream = SM::kStream;
@@ -256,22 +258,16 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD, FORM> &sm) 
     constexpr uint32_t kTile16 = SM::kTileBytes >> 4;
     constexpr uint32_t kPanel = kStream * 128;              // bytes of a streamed 64-channel panel
     constexpr uint32_t kIdS = ptx::idesc_bf16_f32(kRows, kStream, 0);
-    constexpr uint32_t kIdGrad = ptx::idesc_bf16_f32(kRows, 64, 1);
-    constexpr uint32_t kIdV = ptx::idesc_bf16_f32(kRows, HD, 1);
     constexpr uint32_t kHi = ptx::desc_sw128_hi(1024);
     const uint32_t x_lo = ptx::desc_sw128_lo(ptx::smem_addr(sm.x), 16);
     const uint32_t y_lo = ptx::desc_sw128_lo(ptx::smem_addr(sm.y), 16);
     const uint32_t xs_lo = ptx::desc_sw128_lo(ptx::smem_addr(sm.xs[0]), 16);
     const uint32_t ys_lo = ptx::desc_sw128_lo(ptx::smem_addr(sm.ys[0]), 16);
-    // The streamed tiles as MN-major B operands of the accumulations.
-    const uint32_t xs_mn = ptx::desc_sw128_lo(ptx::smem_addr(sm.xs[0]), kPanel);
-    const uint32_t ys_mn = ptx::desc_sw128_lo(ptx::smem_addr(sm.ys[0]), kPanel);
-    uint32_t ring = 0, ring_phase = 0, unit_iter = 0, done = 0;   // done: tiles accumulated
+    uint32_t ring = 0, ring_phase = 0, unit_iter = 0, c = 0;   // c: tiles
     bool ok = true;
     auto wait = [&](uint64_t &bar, uint32_t parity) -> bool {
         return __all_sync(kAll, wait_phase(sm, bar, parity, kErrTimeoutMma));
     };
-
     // D = A B^T over K = 16 steps [k0, k1) of the channels.
     auto product = [&](uint32_t d, uint32_t a_smem, uint32_t a_tmem, uint32_t b_lo, int k0, int k1) {
 #pragma unroll
@@ -284,81 +280,91 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD, FORM> &sm) 
                 ptx::mma_ts_elect(d, a_tmem + ks * 8, ptx::desc_join(b_lo + b_off, kHi), kIdS, i > 0);
             else
                 ptx::mma_ss_elect(d, ptx::desc_join(a_smem + a_off, kHi),
-                            ptx::desc_join(b_lo + b_off, kHi), kIdS, i > 0);
+                                  ptx::desc_join(b_lo + b_off, kHi), kIdS, i > 0);
         }
     };
-    auto issue_s = [&](uint32_t s) {
-        const uint32_t xb = xs_lo + s * kTile16, yb = ys_lo + s * kTile16;
-        product(tmem + TM::kS, x_lo, tmem + TM::kResX, xb, 0, kMapSteps);
-        product(tmem + TM::kS + 64, x_lo, tmem + TM::kResX, xb, kMapSteps, 2 * kMapSteps);
-        product(tmem + TM::kDP, y_lo, tmem + TM::kResY, yb, 0, HD / 16);
-        ptx::mma_commit_elect(ptx::smem_addr(&sm.s_full));
+    for (int32_t u = blockIdx.x; u < S.n_units && ok; u += gridDim.x) {
+        const Unit U = unit_at<FORM>(p, S, u);
+        const int32_t n = ptx::uniform(U.n_a + U.n_b);
+        if (n == 0) continue;
+        if (!(ok = wait(sm.x_full, unit_iter & 1))) break;
+        for (int32_t j = 0; j < n; ++j, ++c) {
+            if (!(ok = wait(sm.st_full[ring], ring_phase))) break;
+            // S's columns were read by the previous tile.
+            if (c > 0 && !(ok = wait(sm.s_read, (c - 1) & 1))) break;
+            ptx::tc_fence_after();
+            const uint32_t xb = xs_lo + ring * kTile16, yb = ys_lo + ring * kTile16;
+            product(TM::kS, x_lo, TM::kResX, xb, 0, kMapSteps);
+            product(TM::kS + 64, x_lo, TM::kResX, xb, kMapSteps, 2 * kMapSteps);
+            product(TM::kDP, y_lo, TM::kResY, yb, 0, HD / 16);
+            ptx::mma_commit_elect(ptx::smem_addr(&sm.s_full));
+            if (++ring == kStages) {
+                ring = 0;
+                ring_phase ^= 1;
+            }
+        }
+        if (!ok) break;
+        // The resident rows are read by S and dP only.
+        ptx::mma_commit_elect(ptx::smem_addr(&sm.x_empty));
+        ++unit_iter;
+    }
+    // Drain: every MMA issued must finish before tensor memory is freed.
+    ptx::mma_commit_elect(ptx::smem_addr(&sm.drain[0]));
+    wait_phase(sm, sm.drain[0], 0, kErrTimeoutTeardown, false);
+}
+
+template <int HD, int FORM>
+__device__ void grad_issuer(const Params &p, const Sched &S, Smem<HD, FORM> &sm) {
+    using SM = Smem<HD, FORM>;
+    using TM = Tmem<HD, FORM>;
+    constexpr int kStages = SM::kStages, kStream = SM::kStream;
+    constexpr uint32_t kTile16 = SM::kTileBytes >> 4;
+    constexpr uint32_t kPanel = kStream * 128;
+    constexpr uint32_t kIdGrad = ptx::idesc_bf16_f32(kRows, 64, 1);
+    constexpr uint32_t kIdV = ptx::idesc_bf16_f32(kRows, HD, 1);
+    constexpr uint32_t kHi = ptx::desc_sw128_hi(1024);
+    // The streamed tiles as MN-major B operands.
+    const uint32_t xs_mn = ptx::desc_sw128_lo(ptx::smem_addr(sm.xs[0]), kPanel);
+    const uint32_t ys_mn = ptx::desc_sw128_lo(ptx::smem_addr(sm.ys[0]), kPanel);
+    uint32_t ring = 0, unit_iter = 0, c = 0;   // c: tiles
+    bool ok = true;
+    auto wait = [&](uint64_t &bar, uint32_t parity) -> bool {
+        return __all_sync(kAll, wait_phase(sm, bar, parity, kErrTimeoutMma));
     };
     // acc += A (packed, tensor memory) B over the tile's rows.
     auto accumulate = [&](uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, bool first) {
 #pragma unroll
         for (int ks = 0; ks < kStream / 16; ++ks)
-            ptx::mma_ts_elect(d, a + ks * 8, ptx::desc_join(b_lo + ((ks * 16 * 128) >> 4), kHi), idesc,
-                        (first && ks == 0) ? 0u : 1u);
+            ptx::mma_ts_elect(d, a + ks * 8, ptx::desc_join(b_lo + ((ks * 16 * 128) >> 4), kHi),
+                              idesc, (first && ks == 0) ? 0u : 1u);
     };
-    auto next_stage = [&](uint32_t &s) -> bool {
-        s = ring;
-        const bool r = wait(sm.st_full[s], ring_phase);
-        if (++ring == kStages) {
-            ring = 0;
-            ring_phase ^= 1;
-        }
-        return r;
-    };
-
     for (int32_t u = blockIdx.x; u < S.n_units && ok; u += gridDim.x) {
-        Unit U = unit_at<FORM>(p, S, u);
-        units::make_uniform(U);
-        const int32_t n = U.n_a + U.n_b;
+        const Unit U = unit_at<FORM>(p, S, u);
+        const int32_t n = ptx::uniform(U.n_a + U.n_b);
         if (n == 0) continue;
-        if (!(ok = wait(sm.x_full, unit_iter & 1))) break;
-        uint32_t cur, next = 0;
-        if (!(ok = next_stage(cur))) break;
-        // S's columns were read by the previous tile (of the previous unit).
-        if (done > 0 && !(ok = wait(sm.s_read, (done - 1) & 1))) break;
-        ptx::tc_fence_after();
-        issue_s(cur);
-        // The resident rows are read by S and dP only.
-        if (n == 1) ptx::mma_commit_elect(ptx::smem_addr(&sm.x_empty));
-        for (int32_t j = 0; j < n && ok; ++j) {
-            if (j + 1 < n) {
-                if (!(ok = next_stage(next))) break;
-                if (!(ok = wait(sm.s_read, done & 1))) break;
-                ptx::tc_fence_after();
-                issue_s(next);
-                if (j + 2 == n) ptx::mma_commit_elect(ptx::smem_addr(&sm.x_empty));
-            }
-            if (!(ok = wait(sm.p_full, done & 1))) break;
-            if (j == 0 && unit_iter > 0 &&
-                !(ok = wait(sm.acc_empty, (unit_iter - 1) & 1)))
-                break;
+        for (int32_t j = 0; j < n; ++j, ++c) {
+            // (p_full follows s_full, which follows the tile's loads)
+            if (!(ok = wait(sm.p_full, c & 1))) break;
+            if (j == 0 && unit_iter > 0 && !(ok = wait(sm.acc_empty, (unit_iter - 1) & 1))) break;
             ptx::tc_fence_after();
-            const uint32_t xb = xs_mn + cur * kTile16, yb = ys_mn + cur * kTile16;
-            if (FORM == kDKDV)
-                accumulate(tmem + TM::kDV, tmem + TM::kPacked, yb, kIdV, j == 0);
+            const uint32_t xb = xs_mn + ring * kTile16, yb = ys_mn + ring * kTile16;
+            if (FORM == kDKDV) accumulate(TM::kDV, TM::kPacked, yb, kIdV, j == 0);
             // Map m's channels: panel m, or (D = 64) both maps' one panel, of
             // which the epilogue takes map m's half.
 #pragma unroll
             for (int m = 0; m < 2; ++m)
-                accumulate(tmem + TM::kGrad + 64 * m, tmem + TM::kDS + m * TM::kPackedStride,
+                accumulate(TM::kGrad + 64 * m, TM::kDS + m * TM::kPackedStride,
                            xb + (HD == 128 ? m * (kPanel >> 4) : 0), kIdGrad, j == 0);
-            ptx::mma_commit_elect(ptx::smem_addr(&sm.st_empty[cur]));
+            ptx::mma_commit_elect(ptx::smem_addr(&sm.st_empty[ring]));
             ptx::mma_commit_elect(ptx::smem_addr(&sm.acc_done));
-            ++done;
-            cur = next;
+            if (++ring == kStages) ring = 0;
         }
         if (!ok) break;
         ptx::mma_commit_elect(ptx::smem_addr(&sm.acc_full));
         ++unit_iter;
     }
-    // Drain: every MMA issued must finish before tensor memory is freed.
-    ptx::mma_commit_elect(ptx::smem_addr(&sm.drain));
-    wait_phase(sm, sm.drain, 0, kErrTimeoutTeardown, false);
+    ptx::mma_commit_elect(ptx::smem_addr(&sm.drain[1]));
+    wait_phase(sm, sm.drain[1], 0, kErrTimeoutTeardown, false);
 }
 
 // ---------------------------------------------------------------------------
@@ -635,7 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1) diff_bwd_tc_kernel(const __grid_c
         ptx::mbar_init(ptx::smem_addr(&sm.acc_done), 1);
         ptx::mbar_init(ptx::smem_addr(&sm.acc_full), 1);
         ptx::mbar_init(ptx::smem_addr(&sm.acc_empty), kCompute);
-        ptx::mbar_init(ptx::smem_addr(&sm.drain), 1);
+        ptx::mbar_init(ptx::smem_addr(&sm.drain[0]), 1);
+        ptx::mbar_init(ptx::smem_addr(&sm.drain[1]), 1);
         sm.abort = 0;
         sm.max_len = 0;
         sm.err_word = p.err_word;
@@ -669,7 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) diff_bwd_tc_kernel(const __grid_c
     if (tmem_ok) {
         if (warp < 8) compute<HD, FORM>(p, S, sm, tmem);
         else if (warp == kProducerWarp) producer<HD, FORM>(p, S, sm);
-        else mma_issuer<HD, FORM>(p, S, sm);
+        else if (warp == kMmaWarp) score_issuer<HD, FORM>(p, S, sm);
+        else grad_issuer<HD, FORM>(p, S, sm);
     }
     __syncwarp();
     ptx::tc_fence_before();

@@ -17,7 +17,7 @@
 // head-major. Warps (384 threads):
 //   0-3 / 4-7  softmax of map 1 / 2 (thread = query row = TMEM lane); in the
 //              epilogue each group joins half of the output's columns,
-//   8          TMA producer, 9  MMA issuer, 10-11  idle.
+//   8          TMA producer, 9 / 10  MMA issuer of map 1 / 2, 11  idle.
 // Tensor memory: two 64-column regions per map, then O_1 | O_2 (D each). A tile's
 // logits come in two halves: keys 0-63 in one region, keys 64-127 in the other;
 // P (bf16, 64 columns) overwrites the first half's region. Once the second half has
@@ -26,7 +26,8 @@
 // the region of P; regions swap roles every tile. A softmax therefore finds its
 // next 64 keys waiting and never sits out its own P V. (With one 128-column S per
 // map, whose next tile can only follow P V, a tile took 4020 clk; the exponentials
-// are 2048.) Issue order per key tile j, for each map:
+// are 2048.) Issue order per key tile j, for each map (one
+// thread's MMAs run in order):
 //   S(j+1) first half, O += P(j) V(j), S(j+1) second half.
 // Masked keys: their logits are set to -inf whatever they hold; 0 * NaN
 // would still reach a row through P V, so the V rows past the unit's range are
@@ -72,9 +73,11 @@ struct Smem {
     alignas(1024) uint8_t q[kTileBytes];
     alignas(1024) uint8_t kv[kSlots][kTileBytes];
     float inv_l[2][kMaps][kBM];  // by unit parity
-    uint32_t bad[4][4];          // PACK: non-finite V rows of the last four tiles
+    uint32_t bad[kMaps][4][4];   // PACK: non-finite V rows of the last four tiles,
+    uint32_t mark[4][kBM];       // and the tile count of those that map 0 zeroed
     uint64_t q_full, q_empty;
-    uint64_t kv_full[kSlots], kv_empty[kSlots];
+    uint64_t kv_full[kSlots];
+    uint64_t kv_empty[kSlots];   // (and q_empty, o_final: a commit by each map's issuer)
     uint64_t s_lo[kMaps];        // first half of S_m(j) in TMEM            (commit)
     uint64_t s_hi[kMaps];        // second half, and O_m += P_m(j-1) V done (commit)
     uint64_t s_read[kMaps];      // second half loaded                      (128 arrivals)
@@ -82,7 +85,7 @@ struct Smem {
     uint64_t o_final;            // every MMA of the unit done              (commit)
     uint64_t joined;             // both maps' inv_l written                (256 arrivals)
     uint64_t o_empty;            // both accumulators read                  (256 arrivals)
-    uint64_t drain;
+    uint64_t drain[kMaps];
     uint32_t tmem_base;
     int32_t max_len;
     volatile int abort;
@@ -208,11 +211,13 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD> &sm) {
 }
 
 // ---------------------------------------------------------------------------
-// MMA issuer: one converged warp (sm100_ptx.cuh, mma_ss_elect). Tensor memory
-// starts at column 0, so its addresses are constants.
+// MMA issuer of map m: one converged warp (sm100_ptx.cuh, mma_ss_elect). Each
+// map's products depend only on its own, so each map has a warp to issue them; one
+// warp for both took 3550 clk of waits and issues per tile (D = 128). Tensor
+// memory starts at column 0, so its addresses are constants.
 // ---------------------------------------------------------------------------
 template <int HD>
-__device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm) {
+__device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm, int m) {
     constexpr int kSlots = Smem<HD>::kSlots;
     constexpr int kMapSteps = HD / 32;   // K = 16 steps of one map's channels
     constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, 64, 0);
@@ -242,7 +247,7 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm) {
     // Half `hi` of S_m = Q_m K_m^T for tile t: map m's channels are the K = 16
     // steps m * kMapSteps .. of the tile (64-channel panels of 128-byte rows,
     // four steps each), its keys rows 64 hi .. of K.
-    auto issue_s = [&](int m, int hi, uint32_t t, uint32_t k_slot) {
+    auto issue_s = [&](int hi, uint32_t t, uint32_t k_slot) {
         const uint32_t k_lo = k_lo0 + k_slot * kTile16 + ((hi * 64 * 128) >> 4);
         const uint32_t d_s = m * kBN + (hi ? 64 - lo_region(t) : lo_region(t));
 #pragma unroll
@@ -254,7 +259,7 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm) {
         }
     };
     // O_m += P_m V, P_m from tensor memory, over `steps` K = 16 steps.
-    auto issue_pv = [&](int m, uint32_t v_slot, bool first, int32_t steps) {
+    auto issue_pv = [&](uint32_t v_slot, bool first, int32_t steps) {
         const uint32_t v_lo = v_lo0 + v_slot * kTile16;
         const uint32_t d_o = kMaps * kBN + m * HD, a_p = m * kBN + lo_region(c);
         if (steps == kBN / 16) {
@@ -280,16 +285,13 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm) {
         uint32_t k_slot, v_slot;
         if (!(ok = wait(sm.q_full, unit_iter & 1)) || !(ok = next_slot(k_slot))) break;
         int32_t steps = tile_steps(U, 0);
-        for (int m = 0; m < kMaps && ok; ++m) {
-            // Both regions: the previous unit's last S was loaded, and its P V
-            // is ahead in the queue.
-            if (c > 0 && !(ok = wait(sm.s_read[m], (c - 1) & 1))) break;
-            issue_s(m, 0, c, k_slot);
-            ptx::mma_commit_elect(ptx::smem_addr(&sm.s_lo[m]));
-            if (steps > 4) issue_s(m, 1, c, k_slot);
-            ptx::mma_commit_elect(ptx::smem_addr(&sm.s_hi[m]));
-        }
-        if (!ok) break;
+        // Both regions: the previous unit's last S was loaded, and its P V is
+        // ahead in the queue.
+        if (c > 0 && !(ok = wait(sm.s_read[m], (c - 1) & 1))) break;
+        issue_s(0, c, k_slot);
+        ptx::mma_commit_elect(ptx::smem_addr(&sm.s_lo[m]));
+        if (steps > 4) issue_s(1, c, k_slot);
+        ptx::mma_commit_elect(ptx::smem_addr(&sm.s_hi[m]));
         ptx::mma_commit_elect(ptx::smem_addr(&sm.kv_empty[k_slot]));
         // Only the S MMAs read Q: after the unit's last one it is free.
         if (n == 1) ptx::mma_commit_elect(ptx::smem_addr(&sm.q_empty));
@@ -300,21 +302,17 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm) {
             const int32_t next_steps = more ? tile_steps(U, j + 1) : 0;
             // ring order: V(j) was loaded before K(j+1)
             if (!(ok = next_slot(v_slot))) break;
-            if (more && !(ok = next_slot(k_slot))) break;
-            for (int m = 0; m < kMaps && ok; ++m) {
-                if (more) {
-                    if (!(ok = wait(sm.s_read[m], c & 1))) break;
-                    issue_s(m, 0, c + 1, k_slot);
-                    ptx::mma_commit_elect(ptx::smem_addr(&sm.s_lo[m]));
-                }
-                if (!(ok = wait(sm.p_full[m], c & 1))) break;
-                issue_pv(m, v_slot, j == 0, steps);
-                if (more) {
-                    if (next_steps > 4) issue_s(m, 1, c + 1, k_slot);
-                    ptx::mma_commit_elect(ptx::smem_addr(&sm.s_hi[m]));
-                }
+            if (more) {
+                if (!(ok = next_slot(k_slot)) || !(ok = wait(sm.s_read[m], c & 1))) break;
+                issue_s(0, c + 1, k_slot);
+                ptx::mma_commit_elect(ptx::smem_addr(&sm.s_lo[m]));
             }
-            if (!ok) break;
+            if (!(ok = wait(sm.p_full[m], c & 1))) break;
+            issue_pv(v_slot, j == 0, steps);
+            if (more) {
+                if (next_steps > 4) issue_s(1, c + 1, k_slot);
+                ptx::mma_commit_elect(ptx::smem_addr(&sm.s_hi[m]));
+            }
             ptx::mma_commit_elect(ptx::smem_addr(&sm.kv_empty[v_slot]));
             if (more) {
                 ptx::mma_commit_elect(ptx::smem_addr(&sm.kv_empty[k_slot]));
@@ -328,8 +326,8 @@ __device__ void mma_issuer(const Params &p, const Sched &S, Smem<HD> &sm) {
         ++unit_iter;
     }
     // Drain: every MMA issued must finish before tensor memory is freed.
-    ptx::mma_commit_elect(ptx::smem_addr(&sm.drain));
-    wait_phase(sm, sm.drain, 0, kErrTimeoutTeardown, false);
+    ptx::mma_commit_elect(ptx::smem_addr(&sm.drain[m]));
+    wait_phase(sm, sm.drain[m], 0, kErrTimeoutTeardown, false);
 }
 
 // ---------------------------------------------------------------------------
@@ -402,7 +400,7 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const int32_t a = max(klo - k0 - 32 * w, 0), b = min(khi - k0 - 32 * w, 32);
-            if (a < b) hit |= sm.bad[c & 3][w] & (kAll >> (32 - b)) & (kAll << a);
+            if (a < b) hit |= sm.bad[map][c & 3][w] & (kAll >> (32 - b)) & (kAll << a);
         }
         return hit != 0;
     };
@@ -419,8 +417,8 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
         const float lam = __ldg(p.lambda + (p.n_lambda == 1 ? 0 : U.head));
         float m_run = kNegInf, l_run = 0.f;
         bool bad = false;
-        // The marks of tile j (tile count c): map 0's threads wrote them before
-        // its product was issued, which s_hi of the next tile and o_final follow.
+        // The bad rows of tile j (tile count c), which this map's threads wrote
+        // before its product was issued; s_hi of the next tile and o_final follow.
         auto check_bad = [&](int32_t j, uint32_t c) {
             if (scanned(U, j))
                 bad |= sees_bad(units::tile_row<kBN>(U, j), j < U.n_a ? da : ga,
@@ -483,11 +481,12 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
             }
             ptx::tmem_wait_st();
             const float sum = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
-            // V rows to zero, once for both maps, by map 0's threads (its product
-            // is issued first; thread = V row). V(j) is load 2 cnt + 1 of the
-            // ring, and stays until both products ran.
+            // V rows to zero, by both maps' threads (thread = V row), each before
+            // its own product. V(j) is load 2 cnt + 1 of the ring, and stays until
+            // both products ran. Of a non-finite row (PACK), map 1's thread may
+            // find the zeros that map 0's wrote: that one leaves its mark first.
             const int32_t seen = units::tile_rows<kBN>(U, j);
-            if (map == 0 && (seen < kBN || scanned(U, j))) {
+            if (seen < kBN || scanned(U, j)) {
                 const uint32_t it = 2 * cnt + 1, slot = it % kSlots;
                 if (!__all_sync(kAll, wait_phase(sm, sm.kv_full[slot], (it / kSlots) & 1, err)))
                     return;
@@ -502,10 +501,15 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                     if (vr < seen) {
 #pragma unroll
                         for (int i = 0; i < kVecs; ++i)
-                            b |= not_finite(*reinterpret_cast<const uint4 *>(vec(i)));
+                            b |= not_finite(ptx::ld_shared_v4(vec(i)));
+                        __threadfence_block();
+                        volatile uint32_t &mark = sm.mark[cnt & 3][r];
+                        if (map == 0 && b) mark = cnt + 1;
+                        if (map == 1) b |= mark == cnt + 1;
+                        __threadfence_block();
                     }
-                    const uint32_t marks = __ballot_sync(kAll, b);
-                    if ((r & 31) == 0) sm.bad[cnt & 3][r / 32] = marks;
+                    const uint32_t rows = __ballot_sync(kAll, b);
+                    if ((r & 31) == 0) sm.bad[map][cnt & 3][r / 32] = rows;
                     zero |= b;
                 }
                 if (zero) {
@@ -589,21 +593,22 @@ __global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_const
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         ptx::mbar_init(ptx::smem_addr(&sm.q_full), 1);
-        ptx::mbar_init(ptx::smem_addr(&sm.q_empty), 1);
+        ptx::mbar_init(ptx::smem_addr(&sm.q_empty), kMaps);
         for (int s = 0; s < Smem<HD>::kSlots; ++s) {
             ptx::mbar_init(ptx::smem_addr(&sm.kv_full[s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&sm.kv_empty[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&sm.kv_empty[s]), kMaps);
         }
         for (int m = 0; m < kMaps; ++m) {
             ptx::mbar_init(ptx::smem_addr(&sm.s_lo[m]), 1);
             ptx::mbar_init(ptx::smem_addr(&sm.s_hi[m]), 1);
             ptx::mbar_init(ptx::smem_addr(&sm.s_read[m]), kBM);
             ptx::mbar_init(ptx::smem_addr(&sm.p_full[m]), kBM);
+            ptx::mbar_init(ptx::smem_addr(&sm.drain[m]), 1);
         }
-        ptx::mbar_init(ptx::smem_addr(&sm.o_final), 1);
+        ptx::mbar_init(ptx::smem_addr(&sm.o_final), kMaps);
+        for (int i = 0; i < 4 * kBM; ++i) sm.mark[i / kBM][i % kBM] = 0;
         ptx::mbar_init(ptx::smem_addr(&sm.joined), kMaps * kBM);
         ptx::mbar_init(ptx::smem_addr(&sm.o_empty), kMaps * kBM);
-        ptx::mbar_init(ptx::smem_addr(&sm.drain), 1);
         sm.abort = 0;
         sm.max_len = 0;
         sm.err_word = p.err_word;
@@ -637,7 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_const
     } else {
         ptx::setmaxnreg_dec<kRegsOther>();
         if (tmem_ok && warp == kProducerWarp && lane == 0) producer<HD>(p, S, sm);
-        if (tmem_ok && warp == kMmaWarp) mma_issuer<HD>(p, S, sm);
+        if (tmem_ok && (warp == kMmaWarp || warp == kMmaWarp + 1))
+            mma_issuer<HD>(p, S, sm, static_cast<int>(warp) - kMmaWarp);
     }
     __syncwarp();
     ptx::tc_fence_before();
