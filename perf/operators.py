@@ -449,7 +449,7 @@ def own_diff(state):
     atlas.diff_attn(*ins, t["lam"], t["o_d"], t["o_g"], t["s_d"], t["s_g"], t["lse"], **layout)
     atlas.diff_attn_bwd(t["q_d"], t["k_d"], t["v_d"], t["o_d"], t["s_d"], t["do_d"], t["q_g"], t["k_g"],
                         t["v_g"], t["o_g"], t["s_g"], t["do_g"], t["lam"], t["lse"], t["dq_d"], t["dk_d"],
-                        t["dv_d"], t["dq_g"], t["dk_g"], t["dv_g"], t["dlam"], t["work"], **layout)
+                        t["dv_d"], t["dq_g"], t["dk_g"], t["dv_g"], t["dlam"], **layout)
     atlas.diff_lambda_bwd(*t["vectors"], t["dlam"], *t["dvectors"])
     out = {n + "_" + p: t[n + "_" + p] for p in parts for n in ("o", "dq", "dk", "dv")}
     out["dvectors"] = t["dvectors"]
