@@ -650,7 +650,7 @@ atlas_status atlas_diff_attn_bwd(
 
 /* Bytes of atlas_diff_attn_bwd's workspace (host; 0 for invalid sizes). */
 int64_t atlas_diff_attn_bwd_workspace(int64_t batch, int64_t n_detail, int64_t n_global,
-                                      int32_t heads);
+                                      int32_t heads, int32_t head_dim, atlas_dtype dtype);
 
 /* ------------------------------------------------------------------------
  * Group norm, channels last, with an activation.

@@ -91,6 +91,7 @@ FIXED = [
     (1, 127 * 3, 127, 63, 1), # one row short of a tile
     (1, 1000, 500, 515, 2),
     (2, 96, 24, 640, 1),
+    (1, 2304, 768, 260, 1),   # few long units over global keys: cut into parts
 ]
 
 
@@ -116,6 +117,8 @@ OFFSETS = [
     ([0, 300], [0, 257], 257),
     ([0, 128, 256, 384], [0, 128, 131, 260], 260),
     ([0, 7], None, 0),
+    # parts of units whose queries run out: some see no window
+    ([0, 700, 1400, 2100], [0, 140, 140, 300], 300),
 ]
 
 

@@ -176,7 +176,7 @@ def _declare(lib):
         [_vp] * 6 + [_i64] + [_vp] * 6 + [_i64, ctypes.POINTER(AttnLayout), _i32, _i32,
                                          ctypes.c_float, ctypes.c_int, _vp, _i32] + [_vp] * 10)
     lib.atlas_diff_attn_bwd_workspace.restype = _i64
-    lib.atlas_diff_attn_bwd_workspace.argtypes = [_i64, _i64, _i64, _i32]
+    lib.atlas_diff_attn_bwd_workspace.argtypes = [_i64, _i64, _i64, _i32, _i32, ctypes.c_int]
     lib.atlas_group_norm.restype = ctypes.c_int
     lib.atlas_group_norm.argtypes = [_vp] * 4 + [_i64, _i64, _i64, _i32, ctypes.c_double,
                                                  ctypes.c_int, ctypes.c_int, _vp, _vp, _vp]
@@ -737,7 +737,9 @@ def diff_attn_bwd(q_d, k_d, v_d, o_d, s_d, do_d, q_g, k_g, v_g, o_g, s_g, do_g, 
     _same_device(ref, lse, dlam)
     _fp32(2 * int(batch) * heads * (n_d + n_g), "diff_attn_bwd lse", lse)
     _fp32(lam.numel(), "diff_attn_bwd dlam", dlam)
-    work = _work(workspace, ref, stream, diff_attn_bwd_workspace(batch, n_d, n_g, heads))
+    work = _work(workspace, ref, stream,
+                 int(lib().atlas_diff_attn_bwd_workspace(int(batch), n_d, n_g, heads, hd,
+                                                         _dtype_code(ref))))
     nz = lambda t, n: _ptr(t) if n > 0 else None
     _run("atlas_diff_attn_bwd", ref, stream, lambda s: lib().atlas_diff_attn_bwd(
         nz(q_d, n_d), nz(k_d, n_d), nz(v_d, n_d), nz(o_d, n_d), nz(s_d, n_d), nz(do_d, n_d), n_d,
@@ -748,10 +750,11 @@ def diff_attn_bwd(q_d, k_d, v_d, o_d, s_d, do_d, q_g, k_g, v_g, o_g, s_g, do_g, 
     return dq_d, dk_d, dv_d, dq_g, dk_g, dv_g, dlam
 
 
-def diff_attn_bwd_workspace(batch, n_detail, n_global, heads) -> int:
-    """Bytes of ``diff_attn_bwd``'s workspace (rows of one problem)."""
+def diff_attn_bwd_workspace(batch, n_detail, n_global, heads, head_dim, dtype) -> int:
+    """Bytes of ``diff_attn_bwd``'s workspace (rows of one problem; dtype BF16
+    or FP32)."""
     return int(lib().atlas_diff_attn_bwd_workspace(int(batch), int(n_detail), int(n_global),
-                                                   int(heads)))
+                                                   int(heads), int(head_dim), int(dtype)))
 
 
 def _norm_sizes(x, rows, groups, tensors, vectors, stats):

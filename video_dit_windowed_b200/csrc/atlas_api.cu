@@ -902,12 +902,16 @@ ATLAS_API atlas_status atlas_diff_attn(const void *q_d, const void *k_d, const v
 }
 
 ATLAS_API int64_t atlas_diff_attn_bwd_workspace(int64_t batch, int64_t n_detail,
-                                                int64_t n_global, int32_t heads) {
+                                                int64_t n_global, int32_t heads,
+                                                int32_t head_dim, atlas_dtype dtype) {
     if (batch < 1 || batch > kMaxRows || n_detail < 0 || n_global < 0 ||
-        n_detail > kMaxRows / batch || n_global > kMaxRows / batch || heads < 1 || heads > 65535)
+        n_detail > kMaxRows / batch || n_global > kMaxRows / batch || heads < 1 ||
+        heads > 65535 || (head_dim != 64 && head_dim != 128) || elem_bytes(dtype) == 0)
         return 0;
+    const int parts = dtype == ATLAS_BF16 ? diff_split_plan(batch, n_detail, n_global, heads) : 1;
     return 4 * (2 * batch * heads * (n_detail + n_global) +
-                static_cast<int64_t>(heads) * kDiffLambdaParts);
+                static_cast<int64_t>(heads) * kDiffLambdaParts +
+                (parts > 1 ? parts * batch * heads * n_global * 2 * head_dim : 0));
 }
 
 ATLAS_API atlas_status atlas_diff_attn_bwd(
@@ -934,8 +938,8 @@ ATLAS_API atlas_status atlas_diff_attn_bwd(
     }
     if (!aligned16(workspace) || !aligned_to(lse, 4) || !aligned_to(dlambda, 4))
         return ATLAS_ERR_ALIGN;
-    const size_t bw = static_cast<size_t>(
-        atlas_diff_attn_bwd_workspace(layout->batch, n_detail, n_global, heads));
+    const size_t bw = static_cast<size_t>(atlas_diff_attn_bwd_workspace(
+        layout->batch, n_detail, n_global, heads, head_dim, dtype));
     Span all[24] = {{dq_d, bd}, {dk_d, bd}, {dv_d, bd}, {dq_g, bg}, {dk_g, bg}, {dv_g, bg},
                     {workspace, bw}, {dlambda, sizeof(float) * static_cast<size_t>(n_lambda)},
                     {lse, diff_lse_bytes(d.attn)},
@@ -951,9 +955,11 @@ ATLAS_API atlas_status atlas_diff_attn_bwd(
     d.attn.lse = const_cast<float *>(lse);
     d.s_d = const_cast<void *>(s_d);
     d.s_g = const_cast<void *>(s_g);
-    float *delta = static_cast<float *>(workspace);
+    // The parts' sums, read and written 16 bytes at a time, first.
     const int64_t rows = layout->batch * (n_detail + n_global);
-    DiffBwdArgs b{d, do_d, do_g, delta, delta + 2 * rows * heads, dq_d, dk_d, dv_d,
+    float *split = static_cast<float *>(workspace);
+    float *delta = split + (bw / 4 - 2 * rows * heads - static_cast<int64_t>(heads) * kDiffLambdaParts);
+    DiffBwdArgs b{d, do_d, do_g, delta, delta + 2 * rows * heads, split, dq_d, dk_d, dv_d,
                   dq_g, dk_g, dv_g, dlambda};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (rows > 0) {

@@ -27,6 +27,7 @@ struct Shape {
     int32_t tiles_d, tiles_g;        // 128-row tiles of one problem's rows
     int32_t upw;                     // slots per window; 0: packed; -1: from the offsets
     int32_t n_long;                  // dK/dV: units over global keys, scheduled first
+    int32_t n_split;                 // and the parts that each one's queries are cut into
 };
 
 // The unit form and counts, the same in every thread of every CTA.
@@ -50,7 +51,7 @@ __device__ __forceinline__ Sched make_sched(const Shape &p, int32_t max_len) {
     const int32_t n_win = p.win_off != nullptr ? p.n_win : (p.L > 0 ? p.N / p.L : 0);
     S.n_dunits = S.upw > 0 ? n_win * S.upw : p.tiles_d;
     S.per_prob = S.n_dunits + p.tiles_g;
-    S.n_units = S.per_prob * p.batch * p.heads;
+    S.n_units = S.per_prob * p.batch * p.heads + (p.n_split - 1) * p.n_long;
     return S;
 }
 
@@ -105,6 +106,7 @@ __device__ __forceinline__ int32_t window_of_global(const Shape &p, int32_t g) {
 // n_a + n_b == 0: an empty slot.
 struct Unit {
     int32_t head, b, detail, r0, rend, a0, n_a, a_end, b0, n_b, b_end, win;
+    int32_t part;   // of a split unit
 };
 
 template <int TILE>
@@ -137,6 +139,7 @@ template <int TILE>
 __device__ __forceinline__ Unit query_unit(const Shape &p, const Sched &S, int32_t u) {
     Unit U;
     U.win = -1;
+    U.part = 0;
     U.head = u / (S.per_prob * p.batch);
     int32_t lu = u - U.head * S.per_prob * p.batch;
     U.b = lu / S.per_prob;
@@ -169,14 +172,15 @@ __device__ __forceinline__ Unit query_unit(const Shape &p, const Sched &S, int32
 }
 
 // Key rows and the queries that see them (dK/dV). Units over global keys come
-// first: they stream every query that sees them.
+// first: they stream every query that sees them, in n_split parts.
 template <int TILE>
 __device__ __forceinline__ Unit key_unit(const Shape &p, const Sched &S, int32_t u) {
     Unit U;
     U.win = -1;
-    const bool global_keys_unit = u < p.n_long;
+    const bool global_keys_unit = u < p.n_long * p.n_split;
     const int32_t span = global_keys_unit ? p.tiles_g : S.n_dunits;
-    const int32_t v = global_keys_unit ? u : u - p.n_long;
+    const int32_t v = global_keys_unit ? u / p.n_split : u - p.n_long * p.n_split;
+    U.part = global_keys_unit ? u - v * p.n_split : 0;
     U.head = v / (span * p.batch);
     int32_t lv = v - U.head * span * p.batch;
     U.b = lv / span;
@@ -216,6 +220,17 @@ __device__ __forceinline__ Unit key_unit(const Shape &p, const Sched &S, int32_t
         U.n_b = tiles<TILE>(p.G);
     }
     U.n_a = tiles<TILE>(U.a_end - U.a0);
+    if (!U.detail && p.n_split > 1) {
+        // tiles [t0, t1) of the n_a + n_b
+        const int32_t n = U.n_a + U.n_b;
+        const int32_t t0 = static_cast<int32_t>(static_cast<int64_t>(n) * U.part / p.n_split);
+        const int32_t t1 = static_cast<int32_t>(static_cast<int64_t>(n) * (U.part + 1) / p.n_split);
+        const int32_t a = max(min(t1, U.n_a) - min(t0, U.n_a), 0);
+        U.a0 += min(t0, U.n_a) * TILE;
+        U.b0 += max(t0 - U.n_a, 0) * TILE;
+        U.n_a = a;
+        U.n_b = t1 - t0 - a;
+    }
     return U;
 }
 
@@ -314,6 +329,7 @@ inline bool make_shape(const AttnArgs &a, int sm_count, Shape *out, int64_t *n_u
         if (n > INT32_MAX) return false;
     }
     p.n_long = static_cast<int32_t>(p.tiles_g * cells);
+    p.n_split = 1;
     *out = p;
     *n_units = n;
     return true;

@@ -13,7 +13,10 @@
 //   DQ    resident: 128 rows of Q and dO, in tensor memory (A operands of S and
 //         dP); streamed: 64-row tiles of K and V; accumulates dQ.
 //   DKDV  resident: 128 rows of K and V in shared memory; streamed: 48-row tiles
-//         of Q and dO with their lse and D; accumulates dV and dK.
+//         of Q and dO with their lse and D; accumulates dV and dK. With few heads
+//         the units over global keys are few and long (each streams every query):
+//         their queries are cut into parts, whose fp32 sums a second kernel joins
+//         in order (diff_split_plan).
 // Tensor memory holds S_1 | S_2 | dP of one tile, the packed bf16 dS_1 | dS_2 (and
 // W) in columns of their own, and the accumulators:
 //   DQ    3 x 64 + 64 + 128 (dQ) + 128 (resident Q, dO) = 512,
@@ -115,6 +118,7 @@ struct Params {
     uint32_t *err_word;
     float scale_log2, scale;
     int32_t o_v8;
+    float *split;   // DKDV: [n_split][batch * heads][G][dV | dK: D each] (n_split > 1)
     Shape shape;
 };
 
@@ -418,9 +422,19 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
     for (int32_t u = blockIdx.x; u < S.n_units; u += gridDim.x) {
         const Unit U = unit_at<FORM>(p, S, u);
         const int32_t n = U.n_a + U.n_b;
-        if (n == 0) continue;
         const int32_t row = U.r0 + static_cast<int32_t>(r);   // resident row (in problem)
         const bool valid = row < U.rend;
+        // A part's sums of this row (warpgroup 0: dV, 1: dK).
+        float *sums = nullptr;
+        if (FORM == kDKDV && !U.detail && p.shape.n_split > 1 && valid)
+            sums = p.split + (((static_cast<int64_t>(U.part) * p.shape.batch + U.b) * p.shape.heads +
+                               U.head) * G + row) * (2 * HD) + part * HD;
+        if (n == 0) {
+            if (sums != nullptr)
+                for (int c = 0; c < HD; c += 4)
+                    *reinterpret_cast<float4 *>(sums + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+            continue;
+        }
         const float nlam = -__ldg(p.lambda + (p.n_lambda == 1 ? 0 : U.head));
         int32_t da = 0, db = 0, ga = 0, gb = 0;   // streamed rows this row meets
         float own_l[2] = {__builtin_huge_valf(), __builtin_huge_valf()}, own_d[2] = {0.f, 0.f};
@@ -582,7 +596,12 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
             for (int c = 0; c < ncol / 32; ++c) {
                 uint32_t o[32];
                 ptx::tmem_ld32(t + col + c * 32, o);
-                if (valid) {
+                if (sums != nullptr) {
+                    uint4 *at = reinterpret_cast<uint4 *>(sums + ch0 + c * 32);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        at[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                } else if (valid) {
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
                         uint32_t w[8];
@@ -686,6 +705,39 @@ __global__ void __launch_bounds__(kThreads, 1) diff_bwd_tc_kernel(const __grid_c
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
+// Global rows' dV and dK from the parts' sums: one thread per four channels of a
+// (row, head), parts added in order.
+template <int HD>
+__global__ void __launch_bounds__(256) diff_split_join_kernel(const Params p) {
+    constexpr int kVecs = 2 * HD / 4;
+    const int64_t cells = static_cast<int64_t>(p.shape.batch) * p.shape.heads;
+    const int64_t total = cells * p.shape.G * kVecs;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= total) return;
+    const int64_t at = i / kVecs;   // (cell, row)
+    const int c = static_cast<int>(i - at * kVecs) * 4;
+    const int64_t cell = at / p.shape.G, row = at - cell * p.shape.G;
+    const int64_t b = cell / p.shape.heads, head = cell - b * p.shape.heads;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int part = 0; part < p.shape.n_split; ++part) {
+        const float4 x = __ldcs(reinterpret_cast<const float4 *>(
+            p.split + (part * cells * p.shape.G + at) * (2 * HD) + c));
+        s.x += x.x;
+        s.y += x.y;
+        s.z += x.z;
+        s.w += x.w;
+    }
+    const bool dv = c < HD;
+    const int ch = dv ? c : c - HD;
+    const float f = dv ? 1.f
+                       : (ch < HD / 2 ? p.scale
+                                      : -p.scale * __ldg(p.lambda + (p.n_lambda == 1 ? 0 : head)));
+    __nv_bfloat16 *out = (dv ? p.dv[1] : p.grad[1]) +
+                         ((b * p.shape.G + row) * p.shape.heads + head) * HD + ch;
+    *reinterpret_cast<uint2 *>(out) =
+        make_uint2(ptx::pack_bf16x2(s.x * f, s.y * f), ptx::pack_bf16x2(s.z * f, s.w * f));
+}
+
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
@@ -728,6 +780,11 @@ atlas_status launch_form(const DiffBwdArgs &b, const DeviceInfo &dev, cudaStream
     if (!p.err_word) return ATLAS_ERR_CUDA;
     p.scale = a.scale;
     p.scale_log2 = a.scale * kLog2e;
+    if (!dq) {
+        p.shape.n_split = diff_split_plan(a.batch, a.n_detail, a.n_global, a.heads);
+        n_units += static_cast<int64_t>(p.shape.n_split - 1) * p.shape.n_long;
+        p.split = b.split;
+    }
     const size_t smem = sizeof(SM) + 1024;
     if (!set_smem_limit(reinterpret_cast<const void *>(diff_bwd_tc_kernel<HD, FORM>),
                         static_cast<int>(smem)))
@@ -735,14 +792,41 @@ atlas_status launch_form(const DiffBwdArgs &b, const DeviceInfo &dev, cudaStream
     const int grid = static_cast<int>(n_units < dev.sm_count ? n_units : dev.sm_count);
     if (log_enabled())
         log_launch(dq ? "diff_bwd_tc_kernel<dQ>" : "diff_bwd_tc_kernel<dK/dV>", grid, kThreads, smem,
-                   "head_dim %d units %lld batch %d heads %d n_detail %d n_global %d", HD,
-                   static_cast<long long>(n_units), p.shape.batch, p.shape.heads, p.shape.N,
-                   p.shape.G);
+                   "head_dim %d units %lld split %d batch %d heads %d n_detail %d n_global %d", HD,
+                   static_cast<long long>(n_units), p.shape.n_split, p.shape.batch, p.shape.heads,
+                   p.shape.N, p.shape.G);
     diff_bwd_tc_kernel<HD, FORM><<<grid, kThreads, smem, stream>>>(p);
+    if (p.shape.n_split > 1) {
+        const int64_t vecs = rows[1] * a.heads * (2 * HD / 4);
+        diff_split_join_kernel<HD><<<static_cast<unsigned>((vecs + 255) / 256), 256, 0, stream>>>(p);
+    }
     return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 
 }  // namespace
+
+// Parts that the units over global keys are cut into (1: none): the count, up to
+// 16, with the fewest tiles on the busiest of a B200's 148 SMs, a unit's start and
+// end taken as four tiles and the joining launch as eight. 720p: with one head 40
+// units of 1,785 tiles kept 40 SMs busy for 2,423 us, cut into 11 parts 440 units
+// take all of them 805 us; from four heads on the uncut units fill the SMs.
+int diff_split_plan(int64_t batch, int64_t n_detail, int64_t n_global, int32_t heads) {
+    constexpr int64_t kSms = 148;
+    const int64_t units = (n_global + kRows - 1) / kRows * batch * heads;
+    const int64_t len = (n_detail + n_global + Tile<kDKDV>::kStream - 1) / Tile<kDKDV>::kStream;
+    if (units == 0 || units > 16 * kSms) return 1;
+    const int64_t whole = (units + kSms - 1) / kSms * (len + 4);
+    int best = 1;
+    int64_t least = whole;
+    for (int s = 2; s <= 16; ++s) {
+        const int64_t load = (units * s + kSms - 1) / kSms * ((len + s - 1) / s + 4) + 8;
+        if (load < least) {
+            best = s;
+            least = load;
+        }
+    }
+    return 10 * least < 9 * whole ? best : 1;
+}
 
 atlas_status launch_diff_bwd_tc(const DiffBwdArgs &b, cudaStream_t stream) {
     DeviceInfo dev;

@@ -82,6 +82,7 @@ struct Smem {
     uint64_t s_hi[kMaps];        // second half, and O_m += P_m(j-1) V done (commit)
     uint64_t s_read[kMaps];      // second half loaded                      (128 arrivals)
     uint64_t p_full[kMaps];      // P_m(j) in TMEM, O_m rescaled            (128 arrivals)
+    uint64_t half;               // map 0 is half through the unit's second tile (128 arrivals)
     uint64_t o_final;            // every MMA of the unit done              (commit)
     uint64_t joined;             // both maps' inv_l written                (256 arrivals)
     uint64_t o_empty;            // both accumulators read                  (256 arrivals)
@@ -425,6 +426,12 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                                 j < U.n_a ? db : gb, c);
         };
         for (int32_t j = 0; j < n; ++j, ++cnt) {
+            // Map 1 runs half a tile behind map 0, so that one's exponentials
+            // fill the other's waits and tensor-memory accesses: started once
+            // per unit, the distance holds.
+            if (map == 1 && j == 1 &&
+                !__all_sync(kAll, wait_phase(sm, sm.half, unit_iter & 1, err)))
+                return;
             if (!__all_sync(kAll, wait_phase(sm, sm.s_lo[map], cnt & 1, err))) return;
             ptx::tc_fence_after();
             const int32_t k0 = units::tile_row<kBN>(U, j);
@@ -444,6 +451,7 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
             ptx::tmem_ld64(t_hi, hi);
             ptx::tc_fence_before();
             ptx::mbar_arrive(ptx::smem_addr(&sm.s_read[map]));
+            if (map == 0 && j == min(1, n - 1)) ptx::mbar_arrive(ptx::smem_addr(&sm.half));
             if (PACK && j > 0) check_bad(j - 1, cnt - 1);
             float mx2;   // the tile's maximum
             if (!slow) {
@@ -605,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_const
             ptx::mbar_init(ptx::smem_addr(&sm.p_full[m]), kBM);
             ptx::mbar_init(ptx::smem_addr(&sm.drain[m]), 1);
         }
+        ptx::mbar_init(ptx::smem_addr(&sm.half), kBM);
         ptx::mbar_init(ptx::smem_addr(&sm.o_final), kMaps);
         for (int i = 0; i < 4 * kBM; ++i) sm.mark[i / kBM][i % kBM] = 0;
         ptx::mbar_init(ptx::smem_addr(&sm.joined), kMaps * kBM);
