@@ -142,13 +142,16 @@ template <typename SM>
 __device__ __forceinline__ bool wait_phase(SM &sm, uint64_t &bar, uint32_t parity, uint32_t err,
                                            bool honor_abort = true) {
     const uint32_t a = ptx::smem_addr(&bar);
-    if (ptx::mbar_try_wait(a, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
+    // The timer is read only once a wait has failed many times: reading it takes
+    // about as long as a tile's exponentials.
+    uint64_t t0 = 0;
     for (uint32_t spin = 1;; ++spin) {
         if (ptx::mbar_try_wait(a, parity)) return true;
         if ((spin & 63u) == 0) {
             if (honor_abort && sm.abort) return false;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
                 atomicOr(sm.err_word, err);
                 sm.abort = 1;
                 return false;
