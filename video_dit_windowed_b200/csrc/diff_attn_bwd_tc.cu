@@ -138,7 +138,10 @@ __device__ __forceinline__ Unit unit_at(const Params &p, const Sched &S, int32_t
     else return units::key_unit<Tile<FORM>::kStream>(p.shape, S, u);
 }
 
-template <typename SM>
+// Bounded wait. SLEEP: nanoseconds to sleep between tries, for the producer, which
+// runs ahead: its tries otherwise take issue slots from the compute warps of its
+// sub-partition.
+template <int SLEEP = 0, typename SM>
 __device__ __forceinline__ bool wait_phase(SM &sm, uint64_t &bar, uint32_t parity, uint32_t err,
                                            bool honor_abort = true) {
     const uint32_t a = ptx::smem_addr(&bar);
@@ -147,6 +150,7 @@ __device__ __forceinline__ bool wait_phase(SM &sm, uint64_t &bar, uint32_t parit
     uint64_t t0 = 0;
     for (uint32_t spin = 1;; ++spin) {
         if (ptx::mbar_try_wait(a, parity)) return true;
+        if (SLEEP > 0) __nanosleep(SLEEP);
         if ((spin & 63u) == 0) {
             if (honor_abort && sm.abort) return false;
             const uint64_t now = global_timer_ns();
@@ -188,7 +192,7 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD, FORM> &sm) {
         // around the warp-wide steps below.
         if (FORM == kDKDV) {
             if (unit_iter > 0 &&
-                !(ok = __all_sync(kAll, wait_phase(sm, sm.x_empty, (unit_iter - 1) & 1,
+                !(ok = __all_sync(kAll, wait_phase<200>(sm, sm.x_empty, (unit_iter - 1) & 1,
                                                    kErrTimeoutProducer))))
                 break;
             if (lane == 0) {
@@ -204,7 +208,7 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD, FORM> &sm) {
         for (int32_t j = 0; j < n && ok; ++j, ++it) {
             const uint32_t s = it % kStages, round = it / kStages;
             if (round > 0 &&
-                !(ok = __all_sync(kAll, wait_phase(sm, sm.st_empty[s], (round - 1) & 1,
+                !(ok = __all_sync(kAll, wait_phase<200>(sm, sm.st_empty[s], (round - 1) & 1,
                                                    kErrTimeoutProducer))))
                 break;
             const bool det = j < U.n_a;

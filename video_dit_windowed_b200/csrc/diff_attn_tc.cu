@@ -106,7 +106,10 @@ struct Params {
     Shape shape;
 };
 
-template <int HD>
+// Bounded wait. SLEEP: nanoseconds to sleep between tries, for the producer, which
+// runs ahead: its tries otherwise take issue slots from the two softmax warps of
+// its sub-partition, whose tiles then took 600 clk longer than the others'.
+template <int SLEEP = 0, int HD>
 __device__ __forceinline__ bool wait_phase(Smem<HD> &sm, uint64_t &bar, uint32_t parity,
                                            uint32_t err, bool honor_abort = true) {
     const uint32_t a = ptx::smem_addr(&bar);
@@ -115,6 +118,7 @@ __device__ __forceinline__ bool wait_phase(Smem<HD> &sm, uint64_t &bar, uint32_t
     uint64_t t0 = 0;
     for (uint32_t spin = 1;; ++spin) {
         if (ptx::mbar_try_wait(a, parity)) return true;
+        if (SLEEP > 0) __nanosleep(SLEEP);
         if ((spin & 63u) == 0) {
             if (honor_abort && sm.abort) return false;
             const uint64_t now = global_timer_ns();
@@ -162,7 +166,7 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD> &sm) {
     auto load = [&](const CUtensorMap *map, int32_t head, int32_t row) -> bool {
         const uint32_t slot = it % kSlots, round = it / kSlots;
         if (round > 0 &&
-            !wait_phase(sm, sm.kv_empty[slot], (round - 1) & 1, kErrTimeoutProducer))
+            !wait_phase<200>(sm, sm.kv_empty[slot], (round - 1) & 1, kErrTimeoutProducer))
             return false;
         const uint32_t bar = ptx::smem_addr(&sm.kv_full[slot]);
         ptx::mbar_arrive_expect_tx(bar, kBytes);
@@ -180,7 +184,7 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD> &sm) {
         const Unit U = units::query_unit<kBN>(p.shape, S, u);
         const int32_t n = U.n_a + U.n_b;
         if (n == 0) continue;
-        if (unit_iter > 0 && !(ok = wait_phase(sm, sm.q_empty, (unit_iter - 1) & 1,
+        if (unit_iter > 0 && !(ok = wait_phase<200>(sm, sm.q_empty, (unit_iter - 1) & 1,
                                                kErrTimeoutProducer)))
             break;
         const int32_t base[2] = {U.b * p.shape.N, U.b * p.shape.G};
