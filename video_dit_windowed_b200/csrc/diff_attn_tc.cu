@@ -82,7 +82,6 @@ struct Smem {
     uint64_t s_hi[kMaps];        // second half, and O_m += P_m(j-1) V done (commit)
     uint64_t s_read[kMaps];      // second half loaded                      (128 arrivals)
     uint64_t p_full[kMaps];      // P_m(j) in TMEM, O_m rescaled            (128 arrivals)
-    uint64_t half;               // map 0 is half through the unit's second tile (128 arrivals)
     uint64_t o_final;            // every MMA of the unit done              (commit)
     uint64_t joined;             // both maps' inv_l written                (256 arrivals)
     uint64_t o_empty;            // both accumulators read                  (256 arrivals)
@@ -352,24 +351,46 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
     const uint32_t err = kErrTimeoutSoftmax;
     const float sc = p.scale_log2;
 
-    // 64 keys: P = exp2(S*scale*log2e - m) as bf16 pairs into 32 columns of
-    // tensor memory (rounding P halves the product's operand and is 2^-8 of each
-    // weight; the row sum adds the fp32 P). with_max: the maximum of the raw S
-    // joins mx4.
-    auto exp_store = [&](auto with_max, const uint32_t (&sr)[64], float m, uint32_t dst,
-                         float (&sum4)[4], float (&mx4)[4]) {
-        constexpr bool kWithMax = decltype(with_max)::value;
-        uint32_t pk[32];
+    // Columns [B, B + N) of 64 keys' S: P = exp2(S*scale*log2e - m) as bf16 pairs
+    // into pk (rounding P halves the product's operand and is 2^-8 of each weight;
+    // the row sum adds the fp32 P). FAST: the maximum of the raw S joins mx, NaN
+    // kept, and one pair of eight takes its exponentials on the FMA pipe (720p, D =
+    // 128 / 32,760 global tokens, D = 64: none 1628 / 906-975 us, one 1612 / 889, two
+    // 1597 / 920, three 1640 / 970, four 1703 / 1015: beyond one the issue slots cost
+    // what the MUFU saves).
+    auto exps = [&](auto fast, auto from, auto count, const uint32_t (&sr)[64], float m,
+                    ptx::F2 &sum, float (&mx)[2], uint32_t (&pk)[16]) {
+        constexpr bool kFast = decltype(fast)::value;
+        constexpr int B = decltype(from)::value, N = decltype(count)::value;
+        const ptx::F2 scale2 = ptx::f2(sc, sc), negm2 = ptx::f2(-m, -m);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            const float s0 = __uint_as_float(sr[2 * e]), s1 = __uint_as_float(sr[2 * e + 1]);
-            if constexpr (kWithMax) mx4[e & 3] = ptx::max3(mx4[e & 3], s0, s1);
-            const float p0 = ptx::ex2(fmaf(s0, sc, -m));
-            const float p1 = ptx::ex2(fmaf(s1, sc, -m));
-            sum4[e & 3] += p0 + p1;
-            pk[e] = ptx::pack_bf16x2(p0, p1);
+        for (int e = 0; e < N / 2; ++e) {
+            const int c = B + 2 * e;
+            const float s0 = __uint_as_float(sr[c]), s1 = __uint_as_float(sr[c + 1]);
+            if constexpr (kFast) mx[e & 1] = ptx::max3_nan(mx[e & 1], s0, s1);
+            const ptx::F2 x = ptx::fma2(ptx::f2(s0, s1), scale2, negm2);
+            float p0, p1;
+            if (kFast && e % 8 == 3) {
+                ptx::exp2_pair(x, p0, p1);
+            } else {
+                ptx::unpack(x, p0, p1);
+                p0 = ptx::ex2(p0);
+                p1 = ptx::ex2(p1);
+            }
+            sum = ptx::add2(sum, ptx::f2(p0, p1));
+            pk[(c % 32) / 2] = ptx::pack_bf16x2(p0, p1);
         }
-        ptx::tmem_st32_nowait(dst, pk);
+    };
+    constexpr std::integral_constant<int, 0> c0{};
+    constexpr std::integral_constant<int, 32> c32{};
+    // All 64 with ex2, stored (masked tiles, and rows whose reference moves).
+    auto exps_all = [&](const uint32_t (&sr)[64], float m, uint32_t dst, ptx::F2 &sum) {
+        float unused[2];
+        uint32_t pk[16];
+        exps(std::false_type{}, c0, c32, sr, m, sum, unused, pk);
+        ptx::tmem_st16_nowait(dst, pk);
+        exps(std::false_type{}, c32, c32, sr, m, sum, unused, pk);
+        ptx::tmem_st16_nowait(dst + 16, pk);
     };
     auto row_max = [&](const uint32_t (&sr)[64]) -> float {
         float m4[4];
@@ -423,6 +444,8 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
         int32_t da, db, ga, gb;   // keys of this row
         units::query_ranges(p.shape, U, row, da, db, ga, gb);
         const float lam = __ldg(p.lambda + (p.n_lambda == 1 ? 0 : U.head));
+        // The reference m_run (log2 units) is whole, so that moving it scales by a
+        // power of two, exactly.
         float m_run = kNegInf, l_run = 0.f;
         bool bad = false;
         // The bad rows of tile j (tile count c), which this map's threads wrote
@@ -432,39 +455,38 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 bad |= sees_bad(units::tile_row<kBN>(U, j), j < U.n_a ? da : ga,
                                 j < U.n_a ? db : gb, c);
         };
+        uint32_t lo[64], hi[64];
+        // Move the reference of rows whose maximum mx2 exceeds it by more than the
+        // threshold; returns the factor of everything summed so far. O: the P V of
+        // the previous tile is done once s_hi is.
+        auto move = [&](float mx2, bool o_empty) -> float {
+            const bool need = m_run == kNegInf ? mx2 != kNegInf : mx2 > m_run + kRescaleThreshold;
+            float alpha = 1.f;
+            if (need) {
+                const float m_new = ceilf(mx2);
+                alpha = m_run == kNegInf ? 0.f : ptx::ex2(m_run - m_new);
+                m_run = m_new;
+            }
+            l_run *= alpha;
+            if (!o_empty) rescale_o(need, alpha);
+            return alpha;
+        };
         for (int32_t j = 0; j < n; ++j, ++cnt) {
-            // Map 1 runs half a tile behind map 0, so that one's exponentials
-            // fill the other's waits and tensor-memory accesses: started once
-            // per unit, the distance holds.
-            if (map == 1 && j == 1 &&
-                !__all_sync(kAll, wait_phase(sm, sm.half, unit_iter & 1, err)))
-                return;
-            if (!__all_sync(kAll, wait_phase(sm, sm.s_lo[map], cnt & 1, err))) return;
-            ptx::tc_fence_after();
             const int32_t k0 = units::tile_row<kBN>(U, j);
             const int32_t klo = j < U.n_a ? da : ga, khi = j < U.n_a ? db : gb;
             const bool masked = k0 < klo || k0 + kBN > khi;
             const uint32_t t_lo = t_s + lo_region(cnt), t_hi = t_s + 64 - lo_region(cnt);
-            uint32_t lo[64], hi[64];
-            float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-            float mx4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-            ptx::tmem_ld64(t_lo, lo);
-            const bool slow = __any_sync(kAll, m_run == kNegInf || masked);
-            // Exponentials of the first half against the running reference right
-            // away, the maximum in the same pass.
-            if (!slow) exp_store(std::true_type{}, lo, m_run, t_lo, sum4, mx4);
-            if (!__all_sync(kAll, wait_phase(sm, sm.s_hi[map], cnt & 1, err))) return;
+            if (!__all_sync(kAll, wait_phase(sm, sm.s_lo[map], cnt & 1, err))) return;
             ptx::tc_fence_after();
-            ptx::tmem_ld64(t_hi, hi);
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(ptx::smem_addr(&sm.s_read[map]));
-            if (map == 0 && j == min(1, n - 1)) ptx::mbar_arrive(ptx::smem_addr(&sm.half));
-            if (PACK && j > 0) check_bad(j - 1, cnt - 1);
-            float mx2;   // the tile's maximum
-            if (!slow) {
-                exp_store(std::true_type{}, hi, m_run, t_lo + 32, sum4, mx4);
-                mx2 = fmaxf(ptx::max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * sc;
-            } else {
+            ptx::tmem_ld64(t_lo, lo);
+            ptx::F2 sum = ptx::f2(0.f, 0.f);
+            if (__any_sync(kAll, m_run == kNegInf || masked)) {
+                if (!__all_sync(kAll, wait_phase(sm, sm.s_hi[map], cnt & 1, err))) return;
+                ptx::tc_fence_after();
+                ptx::tmem_ld64(t_hi, hi);
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(ptx::smem_addr(&sm.s_read[map]));
+                if (PACK && j > 0) check_bad(j - 1, cnt - 1);
                 if (masked) {
 #pragma unroll
                     for (int e = 0; e < 64; ++e) {
@@ -473,29 +495,60 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                             hi[e] = __float_as_uint(kNegInf);
                     }
                 }
-                mx2 = fmaxf(row_max(lo), row_max(hi)) * sc;
-            }
-            // The reference moves only when the tile's maximum exceeds it by more
-            // than the threshold (exact either way: O and l share it); then, and
-            // on the slow path, the tile's exponentials are taken (again).
-            const bool need = m_run == kNegInf ? mx2 != kNegInf : mx2 > m_run + kRescaleThreshold;
-            if (slow || __any_sync(kAll, need)) {
-                float alpha = 1.f;
-                if (need) {
-                    alpha = m_run == kNegInf ? 0.f : ptx::ex2(m_run - mx2);
-                    m_run = mx2;
-                }
-                l_run *= alpha;
-                ptx::tmem_wait_st();   // the stores that the next ones replace
-                if (j > 0) rescale_o(need, alpha);
+                move(fmaxf(row_max(lo), row_max(hi)) * sc, j == 0);
                 const float m = m_run == kNegInf ? 0.f : m_run;
+                exps_all(lo, m, t_lo, sum);
+                exps_all(hi, m, t_lo + 32, sum);
+            } else {
+                // Exponentials against the running reference right away; a half
+                // whose maximum turns out past the threshold (or NaN) is redone.
+                float mx[2] = {kNegInf, kNegInf};
+                uint32_t pk[16];
+                exps(std::true_type{}, c0, c32, lo, m_run, sum, mx, pk);
+                ptx::tmem_st16_nowait(t_lo, pk);
+                exps(std::true_type{}, c32, c32, lo, m_run, sum, mx, pk);
+                ptx::tmem_st16_nowait(t_lo + 16, pk);
+                if (!__all_sync(kAll, wait_phase(sm, sm.s_hi[map], cnt & 1, err))) return;
+                ptx::tc_fence_after();
+                float mx2 = ptx::max_nan(mx[0], mx[1]) * sc;
+                if (__any_sync(kAll, !(mx2 <= m_run + kRescaleThreshold))) {
+                    ptx::tmem_wait_st();
+                    move(mx2, false);
+                    sum = ptx::f2(0.f, 0.f);
+                    exps_all(lo, m_run, t_lo, sum);
+                }
+                ptx::tmem_ld64(t_hi, hi);
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(ptx::smem_addr(&sm.s_read[map]));
+                if (PACK && j > 0) check_bad(j - 1, cnt - 1);
+                const ptx::F2 sum_lo = sum;
+                mx[0] = mx[1] = kNegInf;
+                sum = ptx::f2(0.f, 0.f);
+                exps(std::true_type{}, c0, c32, hi, m_run, sum, mx, pk);
+                ptx::tmem_st16_nowait(t_lo + 32, pk);
+                exps(std::true_type{}, c32, c32, hi, m_run, sum, mx, pk);
+                ptx::tmem_st16_nowait(t_lo + 48, pk);
+                mx2 = ptx::max_nan(mx[0], mx[1]) * sc;
+                float f = 1.f;
+                if (__any_sync(kAll, !(mx2 <= m_run + kRescaleThreshold))) {
+                    ptx::tmem_wait_st();
+                    f = move(mx2, false);
+                    uint32_t plo[32];
+                    ptx::tmem_ld32(t_lo, plo);
+                    const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) sum4[k] = 0.f;
-                exp_store(std::false_type{}, lo, m, t_lo, sum4, mx4);
-                exp_store(std::false_type{}, hi, m, t_lo + 32, sum4, mx4);
+                    for (int e = 0; e < 32; ++e) {
+                        const __nv_bfloat162 v =
+                            __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&plo[e]), f2);
+                        plo[e] = *reinterpret_cast<const uint32_t *>(&v);
+                    }
+                    ptx::tmem_st32_nowait(t_lo, plo);
+                    sum = ptx::f2(0.f, 0.f);
+                    exps_all(hi, m_run, t_lo + 32, sum);
+                }
+                sum = ptx::fma2(sum_lo, ptx::f2(f, f), sum);
             }
             ptx::tmem_wait_st();
-            const float sum = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
             // V rows to zero, by both maps' threads (thread = V row), each before
             // its own product. V(j) is load 2 cnt + 1 of the ring, and stays until
             // both products ran. Of a non-finite row (PACK), map 1's thread may
@@ -533,7 +586,9 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                     ptx::fence_proxy_async_smem();
                 }
             }
-            l_run += sum;
+            float sum0, sum1;
+            ptx::unpack(sum, sum0, sum1);
+            l_run += sum0 + sum1;
             ptx::tc_fence_before();
             ptx::mbar_arrive(ptx::smem_addr(&sm.p_full[map]));
         }
@@ -620,7 +675,6 @@ __global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_const
             ptx::mbar_init(ptx::smem_addr(&sm.p_full[m]), kBM);
             ptx::mbar_init(ptx::smem_addr(&sm.drain[m]), 1);
         }
-        ptx::mbar_init(ptx::smem_addr(&sm.half), kBM);
         ptx::mbar_init(ptx::smem_addr(&sm.o_final), kMaps);
         for (int i = 0; i < 4 * kBM; ++i) sm.mark[i / kBM][i % kBM] = 0;
         ptx::mbar_init(ptx::smem_addr(&sm.joined), kMaps * kBM);

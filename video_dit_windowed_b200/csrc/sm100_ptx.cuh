@@ -376,6 +376,64 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// max with NaN kept (the plain forms drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Two floats in one 64-bit register, one instruction for both.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack(F2 a, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+// 2^x of a pair on the FMA pipe, for x in [-125, 127] (below: about 2^-125; NaN and
+// larger: unspecified): x = n + f with f in [-1/2, 1/2], 2^f by a polynomial of
+// degree 4 (least maximum relative error, 2.7e-6, fitted for this use) and n added
+// to its exponent.
+__device__ __forceinline__ void exp2_pair(F2 x, float &lo, float &hi) {
+    constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: x + kMagic rounds x to whole
+    float a, b;
+    unpack(x, a, b);
+    x = f2(fmaxf(a, -125.f), fmaxf(b, -125.f));
+    const F2 t = add2(x, f2(kMagic, kMagic));
+    const F2 n = add2(t, f2(-kMagic, -kMagic));
+    const F2 f = fma2(n, f2(-1.f, -1.f), x);
+    F2 p = fma2(f2(0x1.3997d6p-7f, 0x1.3997d6p-7f), f, f2(0x1.ca1440p-5f, 0x1.ca1440p-5f));
+    p = fma2(p, f, f2(0x1.ec06dap-3f, 0x1.ec06dap-3f));
+    p = fma2(p, f, f2(0x1.62e0dcp-1f, 0x1.62e0dcp-1f));
+    p = fma2(p, f, f2(0x1.ffffe8p-1f, 0x1.ffffe8p-1f));
+    float ta, tb, pa, pb;
+    unpack(t, ta, tb);
+    unpack(p, pa, pb);
+    lo = __uint_as_float(__float_as_uint(pa) + (__float_as_uint(ta) << 23));
+    hi = __uint_as_float(__float_as_uint(pb) + (__float_as_uint(tb) << 23));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     uint32_t r;
     // cvt.rn.bf16x2.f32 d, a, b puts a in the upper half, b in the lower.
