@@ -6,49 +6,91 @@
 // Backward, with dz = dy act'(z), dh = dz gamma:
 //   dx = rstd (dh - mean(dh) - xhat mean(dh xhat)),
 //   dgamma = sum dz xhat,  dbeta = sum dz.
+// HBM-bound throughout. Three forms, by what one sample's group needs:
+//   heads     one row per sample and a group of 1, 2, 4, .. 32 16-byte vectors:
+//             a group is that many lanes of a warp, its sums are shuffles, and
+//             every element is read once;
+//   resident  a sample's rows of some whole groups fit in shared memory: a block
+//             reads them once and keeps them there between the sums and the
+//             result;
+//   split     anything longer: the sums' pass is cut into chunks of rows over the
+//             whole GPU, partial sums per channel are joined by a second kernel,
+//             and a third writes the result, walking the rows backwards so that
+//             it starts with the rows that are still in L2.
+// Variances are sums of squared deviations: from the mean where the values are
+// held (heads, resident), else from a value of the same channel, joined in fp64, so
+// a large mean costs no digits of the deviations.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "atlas_internal.cuh"
+#include "cube_geom.cuh"
 
 namespace atlas {
 namespace {
 
-constexpr int kThreads = 256;
+using geom::FastDiv;
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ float from_f<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
-    return __float2bfloat16_rn(v);
-}
+constexpr int kThreads = 256;
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kSms = 148;                    // of a B200: grids and workspaces are sized by it
+constexpr int64_t kResidentBytes = 96 * 1024;
+constexpr int64_t kSplitBlocks = 8 * kSms;   // blocks of a split pass
+constexpr int64_t kPartBlocks = 4 * kSms;    // blocks of a backward pass that keep dgamma sums
 
 struct Params {
     const void *x, *dy;
     void *out;                      // y or dx
     const float *gamma, *beta;
-    float *stats;                   // (mean, rstd) of every (sample, group)
+    float2 *stats;                  // (mean, rstd) of every (sample, group); may be NULL forward
     float *dgamma, *dbeta;
     int64_t samples, rows, channels;
-    int32_t groups, silu;
+    int32_t groups, cg, silu;
     float eps;
+    // resident: groups and channels of a slice, slices; threads per group
+    int32_t slice_groups, slices, team;
+    FastDiv by_cgv;
+    // split: rows of a chunk, chunks of a sample
+    int64_t chunk_rows;
+    int32_t chunks;
+    float2 *part;                   // partial sums (see each kernel)
+    float2 *coef;                   // split: (mean, rstd), or the backward's two means
+    int32_t n_parts;                // partial sums of dgamma and dbeta
 };
 
-__device__ __forceinline__ float block_sum(float v) {
-    __shared__ float part[kThreads / 32];
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
-    __syncthreads();
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) s += part[i];
-    return s;
-}
+template <typename T>
+struct Io;
+template <>
+struct Io<float> {
+    static constexpr int kVec = 4;
+    static __device__ __forceinline__ float get(const float &v) { return v; }
+    static __device__ __forceinline__ float put(float v) { return v; }
+};
+template <>
+struct Io<__nv_bfloat16> {
+    static constexpr int kVec = 8;
+    static __device__ __forceinline__ float get(const __nv_bfloat16 &v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+
+// V consecutive values (16 bytes, or one).
+template <typename T, int V>
+struct Pack {
+    T v[V];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (V > 1) *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(p);
+        else v[0] = *p;
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (V > 1) *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(v);
+        else *p = v[0];
+    }
+    __device__ __forceinline__ float operator[](int i) const { return Io<T>::get(v[i]); }
+    __device__ __forceinline__ void set(int i, float f) { v[i] = Io<T>::put(f); }
+};
+template <typename T, int V>
+struct alignas(V > 1 ? 16 : sizeof(T)) Vec : Pack<T, V> {};
 
 __device__ __forceinline__ float gamma_of(const Params &p, int64_t c) {
     return p.gamma ? __ldg(p.gamma + c) : 1.f;
@@ -56,156 +98,710 @@ __device__ __forceinline__ float gamma_of(const Params &p, int64_t c) {
 __device__ __forceinline__ float beta_of(const Params &p, int64_t c) {
     return p.beta ? __ldg(p.beta + c) : 0.f;
 }
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 // act(z), and dy act'(z).
-__device__ __forceinline__ float act(float z, int silu) {
-    return silu ? z / (1.f + __expf(-z)) : z;
-}
+__device__ __forceinline__ float act(float z, int silu) { return silu ? z * sigmoid(z) : z; }
 __device__ __forceinline__ float act_grad(float dy, float z, int silu) {
     if (!silu) return dy;
-    const float s = 1.f / (1.f + __expf(-z));
-    return dy * (s * (1.f + z * (1.f - s)));
+    const float s = sigmoid(z);
+    return dy * (s * fmaf(z, 1.f - s, 1.f));
+}
+// xhat and dz of one element.
+struct Grad {
+    float hat, dz;
+};
+__device__ __forceinline__ Grad grad_of(float x, float dy, float2 st, float ga, float be, int silu) {
+    Grad g;
+    g.hat = (x - st.x) * st.y;
+    g.dz = act_grad(dy, fmaf(g.hat, ga, be), silu);
+    return g;
+}
+// dh: its own rounding, so that a group of one value gives exactly 0.
+__device__ __forceinline__ float dh_of(float dz, float ga) { return __fmul_rn(dz, ga); }
+
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+    for (int off = lanes / 2; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+    return v;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const Params p) {
-    const int64_t cg = p.channels / p.groups, n = p.rows * cg;
-    const int64_t s = blockIdx.x / p.groups, g = blockIdx.x - s * p.groups;
-    const int64_t base = s * p.rows * p.channels + g * cg;
-    const T *x = static_cast<const T *>(p.x) + base;
-    T *y = static_cast<T *>(p.out) + base;
-    auto at = [&](int64_t i) { return i / cg * p.channels + i % cg; };
-    float sum = 0.f;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) sum += to_f(x[at(i)]);
-    const float mean = block_sum(sum) / static_cast<float>(n);
-    sum = 0.f;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-        const float d = to_f(x[at(i)]) - mean;
-        sum = fmaf(d, d, sum);
+// ---------------------------------------------------------------------------
+// Heads: rows == 1. Thread = one 16-byte column of a token; block = a slice of up
+// to 256 columns (blockIdx.y), or several tokens when the rows are shorter; a
+// thread keeps its column for all its tokens, so gamma, beta and its sums of
+// dgamma and dbeta stay in registers.
+// ---------------------------------------------------------------------------
+template <typename T, int LANES, bool BWD>
+__global__ void __launch_bounds__(kThreads) norm_heads_kernel(const Params p) {
+    constexpr int V = Io<T>::kVec, kFlight = BWD ? 2 : 4;
+    const int nv = static_cast<int>(p.channels / V);
+    const int width = min(nv, kThreads), per_block = kThreads / width;   // tokens at a time
+    const int sub = threadIdx.x / width;
+    const int col = blockIdx.y * kThreads + threadIdx.x - sub * width;
+    const bool active = sub < per_block && col < nv;
+    const int64_t ch = static_cast<int64_t>(col) * V, group = col / LANES;
+    float ga[V], be[V], dga[V], dbe[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        ga[e] = active ? gamma_of(p, ch + e) : 0.f;
+        be[e] = active ? beta_of(p, ch + e) : 0.f;
+        dga[e] = dbe[e] = 0.f;
     }
-    const float rstd = rsqrtf(block_sum(sum) / static_cast<float>(n) + p.eps);
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-        const int64_t c = g * cg + i % cg;
-        const float hat = (to_f(x[at(i)]) - mean) * rstd;
-        y[at(i)] = from_f<T>(act(fmaf(hat, gamma_of(p, c), beta_of(p, c)), p.silu));
-    }
-    if (p.stats != nullptr && threadIdx.x == 0) {
-        p.stats[2 * static_cast<int64_t>(blockIdx.x)] = mean;
-        p.stats[2 * static_cast<int64_t>(blockIdx.x) + 1] = rstd;
-    }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_dx_kernel(const Params p) {
-    const int64_t cg = p.channels / p.groups, n = p.rows * cg;
-    const int64_t s = blockIdx.x / p.groups, g = blockIdx.x - s * p.groups;
-    const int64_t base = s * p.rows * p.channels + g * cg;
-    const T *x = static_cast<const T *>(p.x) + base, *dy = static_cast<const T *>(p.dy) + base;
-    T *dx = static_cast<T *>(p.out) + base;
-    const float mean = p.stats[2 * static_cast<int64_t>(blockIdx.x)];
-    const float rstd = p.stats[2 * static_cast<int64_t>(blockIdx.x) + 1];
-    auto at = [&](int64_t i) { return i / cg * p.channels + i % cg; };
-    auto grads = [&](int64_t i, float &hat) -> float {
-        const int64_t c = g * cg + i % cg;
-        hat = (to_f(x[at(i)]) - mean) * rstd;
-        const float z = fmaf(hat, gamma_of(p, c), beta_of(p, c));
-        return __fmul_rn(act_grad(to_f(dy[at(i)]), z, p.silu), gamma_of(p, c));
-    };
-    float s1 = 0.f, s2 = 0.f, hat;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-        const float dh = grads(i, hat);
-        s1 += dh;
-        s2 = fmaf(dh, hat, s2);
-    }
-    const float m1 = block_sum(s1) / static_cast<float>(n);
-    const float m2 = block_sum(s2) / static_cast<float>(n);
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-        const float dh = grads(i, hat);
-        dx[at(i)] = from_f<T>(rstd * (dh - m1 - hat * m2));
-    }
-}
-
-// dgamma, dbeta: a block takes 32 channels, eight rows at a time.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_dgamma_kernel(const Params p) {
-    __shared__ float part[2][8][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane, cg = p.channels / p.groups;
-    float a = 0.f, b = 0.f;
-    if (c < p.channels) {
-        const int64_t g = c / cg;
-        for (int64_t r = warp; r < p.samples * p.rows; r += 8) {
-            const float *st = p.stats + 2 * (r / p.rows * p.groups + g);
-            const float hat = (to_f(static_cast<const T *>(p.x)[r * p.channels + c]) - st[0]) * st[1];
-            const float z = fmaf(hat, gamma_of(p, c), beta_of(p, c));
-            const float dz = act_grad(to_f(static_cast<const T *>(p.dy)[r * p.channels + c]), z, p.silu);
-            a = fmaf(dz, hat, a);
-            b += dz;
+    const float inv_n = 1.f / (LANES * V);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+    const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy);
+    for (int64_t s0 = static_cast<int64_t>(blockIdx.x) * per_block; s0 < p.samples;
+         s0 += step * kFlight) {
+        Vec<T, V> xv[kFlight], gv[kFlight];
+        float2 st[kFlight];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int64_t s = s0 + f * step + sub;
+            const bool on = active && s < p.samples;
+            const int64_t at = (on ? s : 0) * p.channels + (on ? ch : 0);
+            xv[f].load(x + at);
+            if (BWD) {
+                gv[f].load(dy + at);
+                st[f] = __ldg(p.stats + (on ? s * p.groups + group : 0));
+            }
+        }
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int64_t s = s0 + f * step + sub;
+            const bool on = active && s < p.samples;
+            Vec<T, V> o;
+            if (!BWD) {
+                float sum = 0.f, sq = 0.f;
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum += xv[f][e];
+                const float mean = lanes_sum(sum, LANES) * inv_n;
+#pragma unroll
+                for (int e = 0; e < V; ++e) sq = fmaf(xv[f][e] - mean, xv[f][e] - mean, sq);
+                const float rstd = rsqrtf(fmaf(lanes_sum(sq, LANES), inv_n, p.eps));
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    o.set(e, act(fmaf((xv[f][e] - mean) * rstd, ga[e], be[e]), p.silu));
+                if (on && p.stats != nullptr && col % LANES == 0)
+                    p.stats[s * p.groups + group] = make_float2(mean, rstd);
+            } else {
+                float hat[V], dh[V], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const Grad g = grad_of(xv[f][e], gv[f][e], st[f], ga[e], be[e], p.silu);
+                    hat[e] = g.hat;
+                    dh[e] = dh_of(g.dz, ga[e]);
+                    s1 += dh[e];
+                    s2 = fmaf(dh[e], g.hat, s2);
+                    if (on) {
+                        dga[e] = fmaf(g.dz, g.hat, dga[e]);
+                        dbe[e] += g.dz;
+                    }
+                }
+                const float m1 = lanes_sum(s1, LANES) * inv_n, m2 = lanes_sum(s2, LANES) * inv_n;
+#pragma unroll
+                for (int e = 0; e < V; ++e) o.set(e, st[f].y * (dh[e] - m1 - hat[e] * m2));
+            }
+            if (on) o.store(static_cast<T *>(p.out) + s * p.channels + ch);
         }
     }
-    part[0][warp][lane] = a;
-    part[1][warp][lane] = b;
-    __syncthreads();
-    if (warp < 2 && c < p.channels) {
-        float s = 0.f;
-        for (int i = 0; i < 8; ++i) s += part[warp][i][lane];
-        float *out = warp == 0 ? p.dgamma : p.dbeta;
-        if (out != nullptr) out[c] = s;
+    if (BWD && p.n_parts > 0) {
+        // part [block][channel] of (dgamma, dbeta): the block's tokens in order
+        __shared__ float2 sums[kThreads][V + 1];
+#pragma unroll
+        for (int e = 0; e < V; ++e) sums[threadIdx.x][e] = make_float2(dga[e], dbe[e]);
+        __syncthreads();
+        if (sub == 0 && col < nv) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                float2 a = sums[threadIdx.x][e];
+                for (int k = 1; k < per_block; ++k) {
+                    a.x += sums[k * width + threadIdx.x][e].x;
+                    a.y += sums[k * width + threadIdx.x][e].y;
+                }
+                p.part[blockIdx.x * p.channels + ch + e] = a;
+            }
+        }
     }
 }
 
-Params params_of(const NormArgs &a) {
-    Params p;
+// ---------------------------------------------------------------------------
+// Resident: block = a slice of whole groups (blockIdx.y) of one sample after
+// another. A group's `team` threads (a power of two) hold its V-wide items
+// (row, column) in turn, in shared memory of their own.
+// ---------------------------------------------------------------------------
+template <typename T, int V, bool BWD>
+__global__ void __launch_bounds__(kThreads) norm_resident_kernel(const Params p) {
+    extern __shared__ uint8_t smem[];
+    __shared__ float warp_sums[2][kThreads / 32];
+    const int cgv = p.cg / V, team = p.team, g = threadIdx.x / team, lane = threadIdx.x % team;
+    const int g0 = blockIdx.y * p.slice_groups, ng = min(p.slice_groups, p.groups - g0);
+    const bool on = g < ng;
+    const int64_t n_items = on ? p.rows * cgv : 0;
+    const float n = static_cast<float>(p.rows * p.cg);   // (a division: exact for a constant)
+    const int width = p.slice_groups * p.cg;   // channels of a slice
+    T *xs = reinterpret_cast<T *>(smem);
+    T *gs = xs + p.rows * width;               // BWD: dy
+    float2 *acc = reinterpret_cast<float2 *>(
+        smem + (2 * p.rows * width * sizeof(T) + 15) / 16 * 16);   // BWD: (dgamma, dbeta) [width]
+    const int64_t ch0 = static_cast<int64_t>(g0) * p.cg;
+    if (BWD)
+        for (int c = threadIdx.x; c < width; c += kThreads) acc[c] = make_float2(0.f, 0.f);
+    // Sum over a team, the same in all its threads (every thread calls).
+    int which = 0;
+    auto team_sum = [&](float v) -> float {
+        v = lanes_sum(v, min(team, 32));
+        if (team <= 32) return v;
+        which ^= 1;   // the other buffer: one barrier a sum
+        if ((threadIdx.x & 31) == 0) warp_sums[which][threadIdx.x / 32] = v;
+        __syncthreads();
+        float s = 0.f;
+        const int first = threadIdx.x / team * (team / 32);
+        for (int i = 0; i < team / 32; ++i) s += warp_sums[which][first + i];
+        return s;
+    };
+    for (int64_t s = blockIdx.x; s < p.samples; s += gridDim.x) {
+        const int64_t base = s * p.rows * p.channels + ch0;
+        const T *x = static_cast<const T *>(p.x) + base, *dy = static_cast<const T *>(p.dy) + base;
+        T *out = static_cast<T *>(p.out) + base;
+        // item i of the group: row, then column; in the tensor and in the slice
+        auto place = [&](int64_t i, int64_t &at, int &in, int &c) {
+            const uint32_t r = p.by_cgv.div(static_cast<uint32_t>(i));
+            c = g * p.cg + static_cast<int>(i - static_cast<int64_t>(r) * cgv) * V;
+            at = r * p.channels + c;
+            in = static_cast<int>(r) * width + c;
+        };
+        int64_t at;
+        int in, c;
+        const int64_t stat = s * p.groups + g0 + g;
+        if (!BWD) {
+            float sum = 0.f;
+            for (int64_t i = lane; i < n_items; i += team) {
+                place(i, at, in, c);
+                Vec<T, V> v;
+                v.load(x + at);
+                v.store(xs + in);
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum += v[e];
+            }
+            const float mean = team_sum(sum) / n;
+            float sq = 0.f;
+            for (int64_t i = lane; i < n_items; i += team) {
+                place(i, at, in, c);
+                Vec<T, V> v;
+                v.load(xs + in);
+#pragma unroll
+                for (int e = 0; e < V; ++e) sq = fmaf(v[e] - mean, v[e] - mean, sq);
+            }
+            const float rstd = rsqrtf(team_sum(sq) / n + p.eps);
+            for (int64_t i = lane; i < n_items; i += team) {
+                place(i, at, in, c);
+                Vec<T, V> v, o;
+                v.load(xs + in);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    o.set(e, act(fmaf((v[e] - mean) * rstd, gamma_of(p, ch0 + c + e),
+                                      beta_of(p, ch0 + c + e)), p.silu));
+                o.store(out + at);
+            }
+            if (on && lane == 0 && p.stats != nullptr) p.stats[stat] = make_float2(mean, rstd);
+        } else {
+            const float2 st = on ? __ldg(p.stats + stat) : make_float2(0.f, 0.f);
+            float s1 = 0.f, s2 = 0.f;
+            for (int64_t i = lane; i < n_items; i += team) {
+                place(i, at, in, c);
+                Vec<T, V> v, w;
+                v.load(x + at);
+                w.load(dy + at);
+                v.store(xs + in);
+                w.store(gs + in);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float ga = gamma_of(p, ch0 + c + e);
+                    const Grad d = grad_of(v[e], w[e], st, ga, beta_of(p, ch0 + c + e), p.silu);
+                    s1 += dh_of(d.dz, ga);
+                    s2 = fmaf(dh_of(d.dz, ga), d.hat, s2);
+                }
+            }
+            const float m1 = team_sum(s1) / n, m2 = team_sum(s2) / n;
+            for (int64_t i = lane; i < n_items; i += team) {
+                place(i, at, in, c);
+                Vec<T, V> v, w, o;
+                v.load(xs + in);
+                w.load(gs + in);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float ga = gamma_of(p, ch0 + c + e);
+                    const Grad d = grad_of(v[e], w[e], st, ga, beta_of(p, ch0 + c + e), p.silu);
+                    o.set(e, st.y * (dh_of(d.dz, ga) - m1 - d.hat * m2));
+                }
+                o.store(out + at);
+            }
+            if (p.n_parts > 0) {
+                // dgamma, dbeta: thread = channel, rows in order
+                __syncthreads();
+                for (int k = threadIdx.x; k < ng * p.cg; k += kThreads) {
+                    const float2 sk = __ldg(p.stats + s * p.groups + g0 + k / p.cg);
+                    const float ga = gamma_of(p, ch0 + k), be = beta_of(p, ch0 + k);
+                    float2 a = acc[k];
+                    for (int64_t r = 0; r < p.rows; ++r) {
+                        const Grad d = grad_of(Io<T>::get(xs[r * width + k]),
+                                               Io<T>::get(gs[r * width + k]), sk, ga, be, p.silu);
+                        a.x = fmaf(d.dz, d.hat, a.x);
+                        a.y += d.dz;
+                    }
+                    acc[k] = a;
+                }
+                __syncthreads();
+            }
+        }
+    }
+    if (BWD && p.n_parts > 0) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < ng * p.cg; c += kThreads)
+            p.part[blockIdx.x * p.channels + ch0 + c] = acc[c];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Split: thread = one column of V channels for all rows of a chunk; block = a
+// slice of up to 256 columns (blockIdx.y) of one chunk of a sample (blockIdx.x),
+// several rows at a time when the rows are shorter.
+// ---------------------------------------------------------------------------
+struct Slot {
+    int width, per_block, sub, col;
+    bool active;
+};
+__device__ __forceinline__ Slot slot_of(int64_t nv) {
+    Slot t;
+    t.width = static_cast<int>(nv < kThreads ? nv : kThreads);
+    t.per_block = kThreads / t.width;
+    t.sub = threadIdx.x / t.width;
+    t.col = blockIdx.y * kThreads + threadIdx.x - t.sub * t.width;
+    t.active = t.sub < t.per_block && t.col < nv;
+    return t;
+}
+
+// Joins (n, mean, M2) of two sets of values.
+struct Moments {
+    double n = 0, mean = 0, m2 = 0;
+    __device__ __forceinline__ void join(double bn, double bmean, double bm2) {
+        if (bn == 0) return;
+        const double t = n + bn, d = bmean - mean;
+        mean += d * (bn / t);
+        m2 += bm2 + d * d * (n * (bn / t));
+        n = t;
+    }
+};
+
+// Forward: part [sample][chunk][channel] = (mean, M2) of the chunk's rows.
+// Backward: (sum dz xhat, sum dz).
+template <typename T, int V, bool BWD>
+__global__ void __launch_bounds__(kThreads) norm_split_sums_kernel(const Params p) {
+    constexpr int kFlight = BWD ? 4 : 8;
+    __shared__ float2 sums[kThreads][V + 1];
+    const Slot t = slot_of(p.channels / V);
+    const int64_t ch = static_cast<int64_t>(t.col) * V;
+    const int64_t s = blockIdx.x / p.chunks, chunk = blockIdx.x - s * p.chunks;
+    const int64_t r0 = chunk * p.chunk_rows, r1 = min(r0 + p.chunk_rows, p.rows);
+    const T *x = static_cast<const T *>(p.x) + s * p.rows * p.channels + ch;
+    const T *dy = static_cast<const T *>(p.dy) + s * p.rows * p.channels + ch;
+    float ga[V], be[V], a[V], b[V], pivot[V];
+    float2 st[V];
+    const bool any = t.active && r0 + t.sub < r1;
+    Vec<T, V> first;
+    if (any) first.load(x + (r0 + t.sub) * p.channels);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        a[e] = b[e] = 0.f;
+        pivot[e] = any ? first[e] : 0.f;
+        if (BWD) {
+            ga[e] = any ? gamma_of(p, ch + e) : 0.f;
+            be[e] = any ? beta_of(p, ch + e) : 0.f;
+            st[e] = any ? __ldg(p.stats + s * p.groups + (ch + e) / p.cg) : make_float2(0.f, 0.f);
+        }
+    }
+    int64_t n = 0;
+    if (any) {
+        for (int64_t r = r0 + t.sub; r < r1; r += kFlight * t.per_block) {
+            Vec<T, V> v[kFlight], w[kFlight];
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                const int64_t rr = r + f * t.per_block;
+                if (rr >= r1) continue;
+                v[f].load(x + rr * p.channels);
+                if (BWD) w[f].load(dy + rr * p.channels);
+            }
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                if (r + f * t.per_block >= r1) continue;
+                ++n;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    if (BWD) {
+                        const Grad d = grad_of(v[f][e], w[f][e], st[e], ga[e], be[e], p.silu);
+                        a[e] = fmaf(d.dz, d.hat, a[e]);
+                        b[e] += d.dz;
+                    } else {
+                        const float d = v[f][e] - pivot[e];
+                        a[e] += d;
+                        b[e] = fmaf(d, d, b[e]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if (!BWD && n > 0) {
+            // deviations from the pivot -> mean and squared deviations from it
+            const float d = a[e] / static_cast<float>(n);
+            b[e] = fmaxf(fmaf(-d, a[e], b[e]), 0.f);
+            a[e] = pivot[e] + d;
+        }
+        sums[threadIdx.x][e] = make_float2(a[e], b[e]);
+    }
+    __syncthreads();
+    if (t.sub != 0 || !t.active) return;
+    for (int e = 0; e < V; ++e) {
+        float2 out = sums[threadIdx.x][e];
+        if (BWD) {
+            for (int k = 1; k < t.per_block; ++k) {
+                out.x += sums[k * t.width + threadIdx.x][e].x;
+                out.y += sums[k * t.width + threadIdx.x][e].y;
+            }
+        } else {
+            Moments m;
+            for (int k = 0; k < t.per_block; ++k) {
+                const int64_t left = r1 - r0 - k;   // rows r0 + k, + per_block, ..
+                const float2 q = sums[k * t.width + threadIdx.x][e];
+                m.join(left > 0 ? static_cast<double>((left + t.per_block - 1) / t.per_block) : 0.0,
+                       q.x, q.y);
+            }
+            out = make_float2(static_cast<float>(m.mean), static_cast<float>(m.m2));
+        }
+        p.part[blockIdx.x * p.channels + ch + e] = out;
+    }
+}
+
+// One warp per (sample, group): the parts of its channels and chunks, in order.
+// Forward: coef = (mean, rstd), also into stats. Backward: the two means of dh.
+template <bool BWD>
+__global__ void __launch_bounds__(kThreads) norm_split_join_kernel(const Params p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+    if (w >= p.samples * p.groups) return;
+    const int64_t s = w / p.groups, c0 = (w - s * p.groups) * p.cg;
+    const int64_t items = static_cast<int64_t>(p.chunks) * p.cg;
+    Moments m;
+    double s1 = 0, s2 = 0;
+    for (int64_t i = lane; i < items; i += 32) {
+        const int64_t chunk = i / p.cg, c = c0 + (i - chunk * p.cg);
+        const float2 q = p.part[(s * p.chunks + chunk) * p.channels + c];
+        if (BWD) {
+            const double ga = gamma_of(p, c);
+            s1 += ga * q.y;
+            s2 += ga * q.x;
+        } else {
+            m.join(static_cast<double>(min(p.chunk_rows, p.rows - chunk * p.chunk_rows)), q.x, q.y);
+        }
+    }
+    for (int off = 16; off > 0; off >>= 1) {
+        if (BWD) {
+            s1 += __shfl_xor_sync(kAll, s1, off);
+            s2 += __shfl_xor_sync(kAll, s2, off);
+        } else {
+            // every lane joins in the same order: the lower lane's values first
+            const double n = __shfl_xor_sync(kAll, m.n, off), mean = __shfl_xor_sync(kAll, m.mean, off),
+                         m2 = __shfl_xor_sync(kAll, m.m2, off);
+            if (lane & off) {
+                Moments lower;
+                lower.n = n;
+                lower.mean = mean;
+                lower.m2 = m2;
+                lower.join(m.n, m.mean, m.m2);
+                m = lower;
+            } else {
+                m.join(n, mean, m2);
+            }
+        }
+    }
+    if (lane != 0) return;
+    const double n = static_cast<double>(p.rows) * p.cg;
+    if (BWD) {
+        p.coef[w] = make_float2(static_cast<float>(s1 / n), static_cast<float>(s2 / n));
+    } else {
+        const float2 st = make_float2(static_cast<float>(m.mean),
+                                      rsqrtf(static_cast<float>(m.m2 / n) + p.eps));
+        p.coef[w] = st;
+        if (p.stats != nullptr) p.stats[w] = st;
+    }
+}
+
+// The result, rows of all samples last to first.
+template <typename T, int V, bool BWD>
+__global__ void __launch_bounds__(kThreads) norm_split_apply_kernel(const Params p) {
+    constexpr int kFlight = 4;
+    const Slot t = slot_of(p.channels / V);
+    if (!t.active) return;
+    const int64_t ch = static_cast<int64_t>(t.col) * V;
+    const int64_t block = gridDim.x - 1 - blockIdx.x;   // (sample, chunk)
+    const int64_t s = block / p.chunks, chunk = block - s * p.chunks;
+    const int64_t r0 = chunk * p.chunk_rows, r1 = min(r0 + p.chunk_rows, p.rows);
+    const int64_t base = s * p.rows * p.channels + ch;
+    const T *x = static_cast<const T *>(p.x) + base, *dy = static_cast<const T *>(p.dy) + base;
+    T *out = static_cast<T *>(p.out) + base;
+    float ga[V], be[V];
+    float2 st[V], mm[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const int64_t w = s * p.groups + (ch + e) / p.cg;
+        ga[e] = gamma_of(p, ch + e);
+        be[e] = beta_of(p, ch + e);
+        st[e] = BWD ? __ldg(p.stats + w) : p.coef[w];
+        mm[e] = BWD ? p.coef[w] : make_float2(0.f, 0.f);
+    }
+    for (int64_t r = r1 - 1 - t.sub; r >= r0; r -= kFlight * t.per_block) {
+        Vec<T, V> v[kFlight], w[kFlight];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int64_t rr = r - f * t.per_block;
+            if (rr < r0) continue;
+            v[f].load(x + rr * p.channels);
+            if (BWD) w[f].load(dy + rr * p.channels);
+        }
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int64_t rr = r - f * t.per_block;
+            if (rr < r0) continue;
+            Vec<T, V> o;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                if (BWD) {
+                    const Grad d = grad_of(v[f][e], w[f][e], st[e], ga[e], be[e], p.silu);
+                    o.set(e, st[e].y * (dh_of(d.dz, ga[e]) - mm[e].x - d.hat * mm[e].y));
+                } else {
+                    o.set(e, act(fmaf((v[f][e] - st[e].x) * st[e].y, ga[e], be[e]), p.silu));
+                }
+            }
+            o.store(out + rr * p.channels);
+        }
+    }
+}
+
+// dgamma and dbeta from the parts: eight warps add every eighth part each, in
+// order; lane = channel.
+__global__ void __launch_bounds__(kThreads) norm_dgamma_kernel(const Params p) {
+    __shared__ float2 sums[kThreads / 32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    float2 a = make_float2(0.f, 0.f);
+    if (c < p.channels)
+        for (int64_t i = warp; i < p.n_parts; i += kThreads / 32) {
+            const float2 q = p.part[i * p.channels + c];
+            a.x += q.x;
+            a.y += q.y;
+        }
+    sums[warp][lane] = a;
+    __syncthreads();
+    if (warp != 0 || c >= p.channels) return;
+    for (int i = 1; i < kThreads / 32; ++i) {
+        a.x += sums[i][lane].x;
+        a.y += sums[i][lane].y;
+    }
+    if (p.dgamma != nullptr) p.dgamma[c] = a.x;
+    if (p.dbeta != nullptr) p.dbeta[c] = a.y;
+}
+
+// ---------------------------------------------------------------------------
+// Host side: the form of a call, its grids and workspace.
+// ---------------------------------------------------------------------------
+enum Form { kHeads, kResident, kSplit };
+
+struct Plan {
+    Form form;
+    bool vec;                  // 16-byte columns
+    int lanes;                 // heads
+    int32_t slice_groups, slices, team;
+    int64_t smem;              // resident
+    int64_t chunk_rows;
+    int32_t chunks;
+    int64_t grid;              // blockIdx.x of the main passes
+    int32_t parts;             // backward: partial sums of dgamma and dbeta
+    int64_t part_bytes, coef_bytes;
+};
+
+Plan plan_of(const NormArgs &a, bool bwd) {
+    Plan p{};
+    const int64_t eb = a.elem_bytes, cg = a.channels / a.groups;
+    const int vec = static_cast<int>(16 / eb);
+    const bool aligned = a.channels % vec == 0;
+    // Heads: the lanes of a group within a warp.
+    if (a.rows == 1 && cg % vec == 0) {
+        const int64_t lanes = cg / vec;
+        if (lanes <= 32 && (lanes & (lanes - 1)) == 0) {
+            p.form = kHeads;
+            p.vec = true;
+            p.lanes = static_cast<int>(lanes);
+            const int64_t width = std::min<int64_t>(a.channels / vec, kThreads);
+            const int64_t tokens = (a.samples + kThreads / width - 1) / (kThreads / width);
+            p.grid = std::min<int64_t>(tokens, bwd ? kPartBlocks : 16 * kSms);
+            p.parts = static_cast<int32_t>(p.grid);
+            p.part_bytes = bwd ? p.parts * a.channels * 8 : 0;
+            return p;
+        }
+    }
+    // Resident: the fewest groups whose rows are at least two sectors long (64
+    // bytes), 16-byte aligned where the tensor allows it, and fill a block's
+    // threads eight items deep; twice that while it stays within half of the
+    // shared memory and two blocks an SM remain.
+    const bool vec_items = aligned && cg % vec == 0;
+    const int64_t per_group = a.rows * cg * eb * (bwd ? 2 : 1) + (bwd ? cg * 8 : 0);
+    int64_t sg = 1;
+    while (sg < a.groups && sg * cg * eb < 64) sg *= 2;
+    while (sg < a.groups && 2 * sg <= kThreads && 2 * sg * per_group <= kResidentBytes / 2 &&
+           a.samples * ((a.groups + 2 * sg - 1) / (2 * sg)) >= 2 * kSms)
+        sg *= 2;
+    sg = std::min<int64_t>(sg, a.groups);
+    if (sg <= kThreads && sg * per_group + 16 <= kResidentBytes &&
+        a.rows * (cg / (vec_items ? vec : 1)) < (1ll << 31)) {
+        p.form = kResident;
+        p.vec = vec_items;
+        p.slice_groups = static_cast<int32_t>(sg);
+        p.slices = static_cast<int32_t>((a.groups + sg - 1) / sg);
+        p.team = 1;
+        while (2 * p.team * sg <= kThreads) p.team *= 2;
+        p.smem = sg * per_group + 16;
+        const int64_t fill = (bwd ? kPartBlocks : 1 << 20);
+        p.grid = std::min<int64_t>(a.samples, std::max<int64_t>(1, fill / p.slices));
+        p.parts = static_cast<int32_t>(p.grid);
+        p.part_bytes = bwd ? p.parts * a.channels * 8 : 0;
+        if (p.slices <= 65535) return p;
+    }
+    // Split.
+    p.form = kSplit;
+    p.vec = aligned;
+    const int64_t nv = a.channels / (aligned ? vec : 1), slices = (nv + kThreads - 1) / kThreads;
+    const int64_t want = std::max<int64_t>(1, kSplitBlocks / (a.samples * slices));
+    p.chunk_rows = std::max<int64_t>((a.rows + want - 1) / want, 1);
+    p.chunks = static_cast<int32_t>((a.rows + p.chunk_rows - 1) / p.chunk_rows);
+    p.grid = a.samples * p.chunks;
+    p.parts = static_cast<int32_t>(p.grid);
+    p.part_bytes = p.grid * a.channels * 8;
+    p.coef_bytes = a.samples * a.groups * 8;
+    return p;
+}
+
+template <typename T, int LANES>
+void heads(const Params &p, dim3 grid, bool bwd, cudaStream_t s) {
+    if (bwd) norm_heads_kernel<T, LANES, true><<<grid, kThreads, 0, s>>>(p);
+    else norm_heads_kernel<T, LANES, false><<<grid, kThreads, 0, s>>>(p);
+}
+
+template <typename T, int V>
+atlas_status resident(const Params &p, const Plan &plan, bool bwd, cudaStream_t s) {
+    auto kernel = bwd ? norm_resident_kernel<T, V, true> : norm_resident_kernel<T, V, false>;
+    if (!set_smem_limit(reinterpret_cast<const void *>(kernel), static_cast<int>(kResidentBytes)))
+        return ATLAS_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>(plan.grid), static_cast<unsigned>(plan.slices));
+    kernel<<<grid, kThreads, static_cast<size_t>(plan.smem), s>>>(p);
+    return ATLAS_OK;
+}
+
+template <typename T, int V>
+void split(const Params &p, const Plan &plan, bool bwd, cudaStream_t s) {
+    const int64_t nv = p.channels / V;
+    const dim3 grid(static_cast<unsigned>(plan.grid),
+                    static_cast<unsigned>((nv + kThreads - 1) / kThreads));
+    const unsigned join =
+        static_cast<unsigned>((p.samples * p.groups + kThreads / 32 - 1) / (kThreads / 32));
+    if (bwd) {
+        norm_split_sums_kernel<T, V, true><<<grid, kThreads, 0, s>>>(p);
+        norm_split_join_kernel<true><<<join, kThreads, 0, s>>>(p);
+        norm_split_apply_kernel<T, V, true><<<grid, kThreads, 0, s>>>(p);
+    } else {
+        norm_split_sums_kernel<T, V, false><<<grid, kThreads, 0, s>>>(p);
+        norm_split_join_kernel<false><<<join, kThreads, 0, s>>>(p);
+        norm_split_apply_kernel<T, V, false><<<grid, kThreads, 0, s>>>(p);
+    }
+}
+
+template <typename T>
+atlas_status launch(const Params &p, const Plan &plan, bool bwd, cudaStream_t s) {
+    constexpr int V = Io<T>::kVec;
+    if (plan.form == kHeads) {
+        const dim3 grid(static_cast<unsigned>(plan.grid),
+                        static_cast<unsigned>((p.channels / V + kThreads - 1) / kThreads));
+        switch (plan.lanes) {
+            case 1: heads<T, 1>(p, grid, bwd, s); break;
+            case 2: heads<T, 2>(p, grid, bwd, s); break;
+            case 4: heads<T, 4>(p, grid, bwd, s); break;
+            case 8: heads<T, 8>(p, grid, bwd, s); break;
+            case 16: heads<T, 16>(p, grid, bwd, s); break;
+            default: heads<T, 32>(p, grid, bwd, s); break;
+        }
+        return ATLAS_OK;
+    }
+    if (plan.form == kResident)
+        return plan.vec ? resident<T, V>(p, plan, bwd, s) : resident<T, 1>(p, plan, bwd, s);
+    if (plan.vec) split<T, V>(p, plan, bwd, s);
+    else split<T, 1>(p, plan, bwd, s);
+    return ATLAS_OK;
+}
+
+int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
+
+}  // namespace
+
+int64_t group_norm_workspace(const NormArgs &a, bool bwd) {
+    const Plan plan = plan_of(a, bwd);
+    return round16(plan.part_bytes) + round16(plan.coef_bytes);
+}
+
+atlas_status launch_group_norm(const NormArgs &a, bool bwd, cudaStream_t stream) {
+    const Plan plan = plan_of(a, bwd);
+    const int vec = 16 / a.elem_bytes;
+    const int64_t columns = a.channels / (plan.vec ? vec : 1);
+    if (plan.form != kResident && (columns + kThreads - 1) / kThreads > 65535)
+        return ATLAS_ERR_SHAPE;
+    Params p{};
     p.x = a.x;
     p.dy = a.dy;
     p.out = a.out;
     p.gamma = a.gamma;
     p.beta = a.beta;
-    p.stats = a.stats;
+    p.stats = reinterpret_cast<float2 *>(a.stats);
     p.dgamma = a.dgamma;
     p.dbeta = a.dbeta;
     p.samples = a.samples;
     p.rows = a.rows;
     p.channels = a.channels;
     p.groups = a.groups;
+    p.cg = static_cast<int32_t>(a.channels / a.groups);
     p.silu = a.act == ATLAS_ACT_SILU;
     p.eps = static_cast<float>(a.eps);
-    return p;
-}
-
-template <typename T>
-void launch_fwd(const Params &p, cudaStream_t stream) {
-    norm_kernel<T><<<static_cast<unsigned>(p.samples * p.groups), kThreads, 0, stream>>>(p);
-}
-template <typename T>
-void launch_bwd(const Params &p, cudaStream_t stream) {
-    // dgamma first: dx may overwrite x or dy.
-    if (p.dgamma != nullptr || p.dbeta != nullptr)
-        norm_dgamma_kernel<T><<<static_cast<unsigned>((p.channels + 31) / 32), kThreads, 0, stream>>>(p);
-    norm_dx_kernel<T><<<static_cast<unsigned>(p.samples * p.groups), kThreads, 0, stream>>>(p);
-}
-
-}  // namespace
-
-int64_t group_norm_workspace(const NormArgs &a, bool bwd) {
-    (void)a;
-    (void)bwd;
-    return 0;
-}
-
-atlas_status launch_group_norm(const NormArgs &a, bool bwd, cudaStream_t stream) {
-    const Params p = params_of(a);
+    p.slice_groups = plan.slice_groups;
+    p.slices = plan.slices;
+    p.team = plan.team;
+    p.by_cgv = FastDiv(static_cast<uint32_t>(p.cg / (plan.vec ? vec : 1)));
+    p.chunk_rows = plan.chunk_rows;
+    p.chunks = plan.chunks;
+    p.part = static_cast<float2 *>(a.workspace);
+    p.coef = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.workspace) + round16(plan.part_bytes));
+    const bool sums = bwd && (a.dgamma != nullptr || a.dbeta != nullptr);
+    p.n_parts = sums ? plan.parts : 0;
+    static const char *const names[] = {"norm_heads_kernel", "norm_resident_kernel",
+                                        "norm_split_*_kernel"};
     if (log_enabled())
-        log_launch(bwd ? "norm_dx_kernel" : "norm_kernel", static_cast<int>(p.samples * p.groups),
-                   kThreads, 0, "elem_bytes %d samples %lld rows %lld channels %lld groups %d",
-                   a.elem_bytes, static_cast<long long>(p.samples), static_cast<long long>(p.rows),
-                   static_cast<long long>(p.channels), p.groups);
-    if (a.elem_bytes == 2) {
-        if (bwd) launch_bwd<__nv_bfloat16>(p, stream);
-        else launch_fwd<__nv_bfloat16>(p, stream);
-    } else {
-        if (bwd) launch_bwd<float>(p, stream);
-        else launch_fwd<float>(p, stream);
-    }
+        log_launch(names[plan.form], static_cast<int>(plan.grid), kThreads,
+                   static_cast<size_t>(plan.smem),
+                   "%s elem_bytes %d samples %lld rows %lld channels %lld groups %d vec %d",
+                   bwd ? "backward" : "forward", a.elem_bytes, static_cast<long long>(p.samples),
+                   static_cast<long long>(p.rows), static_cast<long long>(p.channels), p.groups,
+                   plan.vec);
+    const atlas_status st = a.elem_bytes == 2 ? launch<__nv_bfloat16>(p, plan, bwd, stream)
+                                              : launch<float>(p, plan, bwd, stream);
+    if (st != ATLAS_OK) return st;
+    if (sums)
+        norm_dgamma_kernel<<<static_cast<unsigned>((a.channels + 31) / 32), kThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 
