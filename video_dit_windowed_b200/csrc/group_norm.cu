@@ -48,6 +48,7 @@ struct Params {
     int64_t samples, rows, channels;
     int32_t groups, cg, silu;
     float eps;
+    int32_t width, per_block;       // heads, split: columns of a slice, rows at a time
     // resident: groups and channels of a slice, slices; threads per group
     int32_t slice_groups, slices, team;
     FastDiv by_cgv;
@@ -84,6 +85,15 @@ struct Pack {
     }
     __device__ __forceinline__ void store(T *p) const {
         if constexpr (V > 1) *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(v);
+        else *p = v[0];
+    }
+    // The same for data that is not read again: first to leave L2.
+    __device__ __forceinline__ void load_last(const T *p) {
+        if constexpr (V > 1) *reinterpret_cast<uint4 *>(v) = __ldcs(reinterpret_cast<const uint4 *>(p));
+        else v[0] = *p;
+    }
+    __device__ __forceinline__ void store_last(T *p) const {
+        if constexpr (V > 1) __stcs(reinterpret_cast<uint4 *>(p), *reinterpret_cast<const uint4 *>(v));
         else *p = v[0];
     }
     __device__ __forceinline__ float operator[](int i) const { return Io<T>::get(v[i]); }
@@ -134,9 +144,9 @@ template <typename T, int LANES, bool BWD>
 __global__ void __launch_bounds__(kThreads) norm_heads_kernel(const Params p) {
     constexpr int V = Io<T>::kVec, kFlight = BWD ? 2 : 4;
     const int nv = static_cast<int>(p.channels / V);
-    const int width = min(nv, kThreads), per_block = kThreads / width;   // tokens at a time
+    const int width = p.width, per_block = p.per_block;   // tokens at a time
     const int sub = threadIdx.x / width;
-    const int col = blockIdx.y * kThreads + threadIdx.x - sub * width;
+    const int col = blockIdx.y * width + threadIdx.x - sub * width;
     const bool active = sub < per_block && col < nv;
     const int64_t ch = static_cast<int64_t>(col) * V, group = col / LANES;
     float ga[V], be[V], dga[V], dbe[V];
@@ -158,9 +168,9 @@ __global__ void __launch_bounds__(kThreads) norm_heads_kernel(const Params p) {
             const int64_t s = s0 + f * step + sub;
             const bool on = active && s < p.samples;
             const int64_t at = (on ? s : 0) * p.channels + (on ? ch : 0);
-            xv[f].load(x + at);
+            xv[f].load_last(x + at);
             if (BWD) {
-                gv[f].load(dy + at);
+                gv[f].load_last(dy + at);
                 st[f] = __ldg(p.stats + (on ? s * p.groups + group : 0));
             }
         }
@@ -200,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) norm_heads_kernel(const Params p) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) o.set(e, st[f].y * (dh[e] - m1 - hat[e] * m2));
             }
-            if (on) o.store(static_cast<T *>(p.out) + s * p.channels + ch);
+            if (on) o.store_last(static_cast<T *>(p.out) + s * p.channels + ch);
         }
     }
     if (BWD && p.n_parts > 0) {
@@ -367,73 +377,59 @@ __global__ void __launch_bounds__(kThreads) norm_resident_kernel(const Params p)
 // several rows at a time when the rows are shorter.
 // ---------------------------------------------------------------------------
 struct Slot {
-    int width, per_block, sub, col;
+    int sub, col;
     bool active;
 };
-__device__ __forceinline__ Slot slot_of(int64_t nv) {
+__device__ __forceinline__ Slot slot_of(const Params &p, int64_t nv) {
     Slot t;
-    t.width = static_cast<int>(nv < kThreads ? nv : kThreads);
-    t.per_block = kThreads / t.width;
-    t.sub = threadIdx.x / t.width;
-    t.col = blockIdx.y * kThreads + threadIdx.x - t.sub * t.width;
-    t.active = t.sub < t.per_block && t.col < nv;
+    t.sub = threadIdx.x / p.width;
+    t.col = blockIdx.y * p.width + threadIdx.x - t.sub * p.width;
+    t.active = t.sub < p.per_block && t.col < nv;
     return t;
 }
 
-// Joins (n, mean, M2) of two sets of values.
-struct Moments {
-    double n = 0, mean = 0, m2 = 0;
-    __device__ __forceinline__ void join(double bn, double bmean, double bm2) {
-        if (bn == 0) return;
-        const double t = n + bn, d = bmean - mean;
-        mean += d * (bn / t);
-        m2 += bm2 + d * d * (n * (bn / t));
-        n = t;
-    }
-};
-
-// Forward: part [sample][chunk][channel] = (mean, M2) of the chunk's rows.
-// Backward: (sum dz xhat, sum dz).
+// Forward: part [sample][chunk][channel] = (mean, M2) of the chunk's rows, from
+// sums of deviations from the chunk's first value of the channel. Backward: (sum
+// dz xhat, sum dz).
 template <typename T, int V, bool BWD>
 __global__ void __launch_bounds__(kThreads) norm_split_sums_kernel(const Params p) {
     constexpr int kFlight = BWD ? 4 : 8;
     __shared__ float2 sums[kThreads][V + 1];
-    const Slot t = slot_of(p.channels / V);
+    const Slot t = slot_of(p, p.channels / V);
     const int64_t ch = static_cast<int64_t>(t.col) * V;
     const int64_t s = blockIdx.x / p.chunks, chunk = blockIdx.x - s * p.chunks;
     const int64_t r0 = chunk * p.chunk_rows, r1 = min(r0 + p.chunk_rows, p.rows);
     const T *x = static_cast<const T *>(p.x) + s * p.rows * p.channels + ch;
     const T *dy = static_cast<const T *>(p.dy) + s * p.rows * p.channels + ch;
-    float ga[V], be[V], a[V], b[V], pivot[V];
-    float2 st[V];
-    const bool any = t.active && r0 + t.sub < r1;
-    Vec<T, V> first;
-    if (any) first.load(x + (r0 + t.sub) * p.channels);
+    float a[V], b[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        a[e] = b[e] = 0.f;
-        pivot[e] = any ? first[e] : 0.f;
-        if (BWD) {
-            ga[e] = any ? gamma_of(p, ch + e) : 0.f;
-            be[e] = any ? beta_of(p, ch + e) : 0.f;
-            st[e] = any ? __ldg(p.stats + s * p.groups + (ch + e) / p.cg) : make_float2(0.f, 0.f);
+    for (int e = 0; e < V; ++e) a[e] = b[e] = 0.f;
+    if (t.active) {
+        float ga[V], be[V];
+        float2 st[V];   // forward: the pivot
+        Vec<T, V> first;
+        first.load(x + r0 * p.channels);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (BWD) {
+                ga[e] = gamma_of(p, ch + e);
+                be[e] = beta_of(p, ch + e);
+                st[e] = __ldg(p.stats + s * p.groups + (ch + e) / p.cg);
+            } else {
+                st[e].x = first[e];
+            }
         }
-    }
-    int64_t n = 0;
-    if (any) {
-        for (int64_t r = r0 + t.sub; r < r1; r += kFlight * t.per_block) {
+        for (int64_t r = r0 + t.sub; r < r1; r += kFlight * p.per_block) {
             Vec<T, V> v[kFlight], w[kFlight];
 #pragma unroll
             for (int f = 0; f < kFlight; ++f) {
-                const int64_t rr = r + f * t.per_block;
-                if (rr >= r1) continue;
+                const int64_t rr = min(r + f * p.per_block, r1 - 1);
                 v[f].load(x + rr * p.channels);
                 if (BWD) w[f].load(dy + rr * p.channels);
             }
 #pragma unroll
             for (int f = 0; f < kFlight; ++f) {
-                if (r + f * t.per_block >= r1) continue;
-                ++n;
+                if (r + f * p.per_block >= r1) continue;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     if (BWD) {
@@ -441,7 +437,7 @@ __global__ void __launch_bounds__(kThreads) norm_split_sums_kernel(const Params 
                         a[e] = fmaf(d.dz, d.hat, a[e]);
                         b[e] += d.dz;
                     } else {
-                        const float d = v[f][e] - pivot[e];
+                        const float d = v[f][e] - st[e].x;
                         a[e] += d;
                         b[e] = fmaf(d, d, b[e]);
                     }
@@ -450,87 +446,111 @@ __global__ void __launch_bounds__(kThreads) norm_split_sums_kernel(const Params 
         }
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        if (!BWD && n > 0) {
-            // deviations from the pivot -> mean and squared deviations from it
-            const float d = a[e] / static_cast<float>(n);
-            b[e] = fmaxf(fmaf(-d, a[e], b[e]), 0.f);
-            a[e] = pivot[e] + d;
-        }
-        sums[threadIdx.x][e] = make_float2(a[e], b[e]);
-    }
+    for (int e = 0; e < V; ++e) sums[threadIdx.x][e] = make_float2(a[e], b[e]);
     __syncthreads();
-    if (t.sub != 0 || !t.active) return;
-    for (int e = 0; e < V; ++e) {
-        float2 out = sums[threadIdx.x][e];
-        if (BWD) {
-            for (int k = 1; k < t.per_block; ++k) {
-                out.x += sums[k * t.width + threadIdx.x][e].x;
-                out.y += sums[k * t.width + threadIdx.x][e].y;
-            }
-        } else {
-            Moments m;
-            for (int k = 0; k < t.per_block; ++k) {
-                const int64_t left = r1 - r0 - k;   // rows r0 + k, + per_block, ..
-                const float2 q = sums[k * t.width + threadIdx.x][e];
-                m.join(left > 0 ? static_cast<double>((left + t.per_block - 1) / t.per_block) : 0.0,
-                       q.x, q.y);
-            }
-            out = make_float2(static_cast<float>(m.mean), static_cast<float>(m.m2));
+    // thread = channel of the slice
+    for (int i = threadIdx.x; i < p.width * V; i += kThreads) {
+        const int64_t c = static_cast<int64_t>(blockIdx.y) * p.width * V + i;
+        if (c >= p.channels) break;
+        float2 q = sums[i / V][i % V];
+        for (int k = 1; k < p.per_block; ++k) {
+            q.x += sums[k * p.width + i / V][i % V].x;
+            q.y += sums[k * p.width + i / V][i % V].y;
         }
-        p.part[blockIdx.x * p.channels + ch + e] = out;
+        if (!BWD) {
+            const float d = q.x / static_cast<float>(r1 - r0);
+            q.y = fmaxf(fmaf(-d, q.x, q.y), 0.f);
+            q.x = Io<T>::get(static_cast<const T *>(p.x)[(s * p.rows + r0) * p.channels + c]) + d;
+        }
+        p.part[blockIdx.x * p.channels + c] = q;
     }
 }
 
-// One warp per (sample, group): the parts of its channels and chunks, in order.
-// Forward: coef = (mean, rstd), also into stats. Backward: the two means of dh.
+// Sum over the block in fp64, in a fixed order, in every thread.
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double part[kThreads / 32];
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    double s = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) s += part[i];
+    return s;
+}
+
+// dgamma and dbeta of 32 channels from the parts: eight warps add every eighth
+// part each, in order; lane = channel.
+__device__ __forceinline__ void dgamma_sums(const Params &p, int64_t block) {
+    __shared__ float2 sums[kThreads / 32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int64_t c = block * 32 + lane;
+    float2 a = make_float2(0.f, 0.f);
+    if (c < p.channels) {
+#pragma unroll 8
+        for (int i = warp; i < p.n_parts; i += kThreads / 32) {
+            const float2 q = p.part[i * p.channels + c];
+            a.x += q.x;
+            a.y += q.y;
+        }
+    }
+    sums[warp][lane] = a;
+    __syncthreads();
+    if (warp != 0 || c >= p.channels) return;
+    for (int i = 1; i < kThreads / 32; ++i) {
+        a.x += sums[i][lane].x;
+        a.y += sums[i][lane].y;
+    }
+    if (p.dgamma != nullptr) p.dgamma[c] = a.x;
+    if (p.dbeta != nullptr) p.dbeta[c] = a.y;
+}
+__global__ void __launch_bounds__(kThreads) norm_dgamma_kernel(const Params p) {
+    dgamma_sums(p, blockIdx.x);
+}
+
+// One block per (sample, group): the parts of its channels and chunks. Forward:
+// coef = (mean, rstd), also into stats. Backward: the two means of dh; the blocks
+// behind those sum dgamma and dbeta.
 template <bool BWD>
 __global__ void __launch_bounds__(kThreads) norm_split_join_kernel(const Params p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
-    if (w >= p.samples * p.groups) return;
+    const int64_t w = blockIdx.x;
+    if (BWD && w >= p.samples * p.groups) {
+        dgamma_sums(p, w - p.samples * p.groups);
+        return;
+    }
     const int64_t s = w / p.groups, c0 = (w - s * p.groups) * p.cg;
     const int64_t items = static_cast<int64_t>(p.chunks) * p.cg;
-    Moments m;
+    const float2 *part = p.part + s * p.chunks * p.channels + c0;
+    const double n = static_cast<double>(p.rows) * p.cg;
     double s1 = 0, s2 = 0;
-    for (int64_t i = lane; i < items; i += 32) {
-        const int64_t chunk = i / p.cg, c = c0 + (i - chunk * p.cg);
-        const float2 q = p.part[(s * p.chunks + chunk) * p.channels + c];
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < items; i += kThreads) {
+        const int64_t chunk = i / p.cg, c = i - chunk * p.cg;
+        const float2 q = part[chunk * p.channels + c];
         if (BWD) {
-            const double ga = gamma_of(p, c);
+            const double ga = gamma_of(p, c0 + c);
             s1 += ga * q.y;
             s2 += ga * q.x;
         } else {
-            m.join(static_cast<double>(min(p.chunk_rows, p.rows - chunk * p.chunk_rows)), q.x, q.y);
+            s1 += static_cast<double>(min(p.chunk_rows, p.rows - chunk * p.chunk_rows)) * q.x;
         }
     }
-    for (int off = 16; off > 0; off >>= 1) {
-        if (BWD) {
-            s1 += __shfl_xor_sync(kAll, s1, off);
-            s2 += __shfl_xor_sync(kAll, s2, off);
-        } else {
-            // every lane joins in the same order: the lower lane's values first
-            const double n = __shfl_xor_sync(kAll, m.n, off), mean = __shfl_xor_sync(kAll, m.mean, off),
-                         m2 = __shfl_xor_sync(kAll, m.m2, off);
-            if (lane & off) {
-                Moments lower;
-                lower.n = n;
-                lower.mean = mean;
-                lower.m2 = m2;
-                lower.join(m.n, m.mean, m.m2);
-                m = lower;
-            } else {
-                m.join(n, mean, m2);
-            }
-        }
-    }
-    if (lane != 0) return;
-    const double n = static_cast<double>(p.rows) * p.cg;
+    s1 = block_sum(s1) / n;
     if (BWD) {
-        p.coef[w] = make_float2(static_cast<float>(s1 / n), static_cast<float>(s2 / n));
-    } else {
-        const float2 st = make_float2(static_cast<float>(m.mean),
-                                      rsqrtf(static_cast<float>(m.m2 / n) + p.eps));
+        s2 = block_sum(s2) / n;
+        if (threadIdx.x == 0) p.coef[w] = make_float2(static_cast<float>(s1), static_cast<float>(s2));
+        return;
+    }
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < items; i += kThreads) {
+        const int64_t chunk = i / p.cg, c = i - chunk * p.cg;
+        const float2 q = part[chunk * p.channels + c];
+        const double d = q.x - s1;
+        s2 += q.y + static_cast<double>(min(p.chunk_rows, p.rows - chunk * p.chunk_rows)) * d * d;
+    }
+    s2 = block_sum(s2) / n;
+    if (threadIdx.x == 0) {
+        const float2 st = make_float2(static_cast<float>(s1), rsqrtf(static_cast<float>(s2) + p.eps));
         p.coef[w] = st;
         if (p.stats != nullptr) p.stats[w] = st;
     }
@@ -540,7 +560,7 @@ __global__ void __launch_bounds__(kThreads) norm_split_join_kernel(const Params 
 template <typename T, int V, bool BWD>
 __global__ void __launch_bounds__(kThreads) norm_split_apply_kernel(const Params p) {
     constexpr int kFlight = 4;
-    const Slot t = slot_of(p.channels / V);
+    const Slot t = slot_of(p, p.channels / V);
     if (!t.active) return;
     const int64_t ch = static_cast<int64_t>(t.col) * V;
     const int64_t block = gridDim.x - 1 - blockIdx.x;   // (sample, chunk)
@@ -559,18 +579,17 @@ __global__ void __launch_bounds__(kThreads) norm_split_apply_kernel(const Params
         st[e] = BWD ? __ldg(p.stats + w) : p.coef[w];
         mm[e] = BWD ? p.coef[w] : make_float2(0.f, 0.f);
     }
-    for (int64_t r = r1 - 1 - t.sub; r >= r0; r -= kFlight * t.per_block) {
+    for (int64_t r = r1 - 1 - t.sub; r >= r0; r -= kFlight * p.per_block) {
         Vec<T, V> v[kFlight], w[kFlight];
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
-            const int64_t rr = r - f * t.per_block;
-            if (rr < r0) continue;
-            v[f].load(x + rr * p.channels);
-            if (BWD) w[f].load(dy + rr * p.channels);
+            const int64_t rr = max(r - f * p.per_block, r0);
+            v[f].load_last(x + rr * p.channels);
+            if (BWD) w[f].load_last(dy + rr * p.channels);
         }
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
-            const int64_t rr = r - f * t.per_block;
+            const int64_t rr = r - f * p.per_block;
             if (rr < r0) continue;
             Vec<T, V> o;
 #pragma unroll
@@ -582,33 +601,9 @@ __global__ void __launch_bounds__(kThreads) norm_split_apply_kernel(const Params
                     o.set(e, act(fmaf((v[f][e] - st[e].x) * st[e].y, ga[e], be[e]), p.silu));
                 }
             }
-            o.store(out + rr * p.channels);
+            o.store_last(out + rr * p.channels);
         }
     }
-}
-
-// dgamma and dbeta from the parts: eight warps add every eighth part each, in
-// order; lane = channel.
-__global__ void __launch_bounds__(kThreads) norm_dgamma_kernel(const Params p) {
-    __shared__ float2 sums[kThreads / 32][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-    float2 a = make_float2(0.f, 0.f);
-    if (c < p.channels)
-        for (int64_t i = warp; i < p.n_parts; i += kThreads / 32) {
-            const float2 q = p.part[i * p.channels + c];
-            a.x += q.x;
-            a.y += q.y;
-        }
-    sums[warp][lane] = a;
-    __syncthreads();
-    if (warp != 0 || c >= p.channels) return;
-    for (int i = 1; i < kThreads / 32; ++i) {
-        a.x += sums[i][lane].x;
-        a.y += sums[i][lane].y;
-    }
-    if (p.dgamma != nullptr) p.dgamma[c] = a.x;
-    if (p.dbeta != nullptr) p.dbeta[c] = a.y;
 }
 
 // ---------------------------------------------------------------------------
@@ -624,10 +619,19 @@ struct Plan {
     int64_t smem;              // resident
     int64_t chunk_rows;
     int32_t chunks;
-    int64_t grid;              // blockIdx.x of the main passes
+    int32_t width, per_block;  // heads, split: columns of a slice, rows at a time
+    int64_t grid, slices_y;    // of the main passes
     int32_t parts;             // backward: partial sums of dgamma and dbeta
     int64_t part_bytes, coef_bytes;
 };
+
+// nv columns in slices of at most a block's threads, as even as whole warps allow.
+void slice_columns(int64_t nv, Plan *p) {
+    p->slices_y = (nv + kThreads - 1) / kThreads;
+    const int64_t even = (nv + p->slices_y - 1) / p->slices_y;
+    p->width = static_cast<int32_t>(p->slices_y == 1 ? nv : (even + 31) / 32 * 32);
+    p->per_block = kThreads / p->width;
+}
 
 Plan plan_of(const NormArgs &a, bool bwd) {
     Plan p{};
@@ -641,8 +645,8 @@ Plan plan_of(const NormArgs &a, bool bwd) {
             p.form = kHeads;
             p.vec = true;
             p.lanes = static_cast<int>(lanes);
-            const int64_t width = std::min<int64_t>(a.channels / vec, kThreads);
-            const int64_t tokens = (a.samples + kThreads / width - 1) / (kThreads / width);
+            slice_columns(a.channels / vec, &p);
+            const int64_t tokens = (a.samples + p.per_block - 1) / p.per_block;
             p.grid = std::min<int64_t>(tokens, bwd ? kPartBlocks : 16 * kSms);
             p.parts = static_cast<int32_t>(p.grid);
             p.part_bytes = bwd ? p.parts * a.channels * 8 : 0;
@@ -674,13 +678,14 @@ Plan plan_of(const NormArgs &a, bool bwd) {
         p.grid = std::min<int64_t>(a.samples, std::max<int64_t>(1, fill / p.slices));
         p.parts = static_cast<int32_t>(p.grid);
         p.part_bytes = bwd ? p.parts * a.channels * 8 : 0;
+        p.slices_y = p.slices;
         if (p.slices <= 65535) return p;
     }
     // Split.
     p.form = kSplit;
     p.vec = aligned;
-    const int64_t nv = a.channels / (aligned ? vec : 1), slices = (nv + kThreads - 1) / kThreads;
-    const int64_t want = std::max<int64_t>(1, kSplitBlocks / (a.samples * slices));
+    slice_columns(a.channels / (aligned ? vec : 1), &p);
+    const int64_t want = std::max<int64_t>(1, kSplitBlocks / (a.samples * p.slices_y));
     p.chunk_rows = std::max<int64_t>((a.rows + want - 1) / want, 1);
     p.chunks = static_cast<int32_t>((a.rows + p.chunk_rows - 1) / p.chunk_rows);
     p.grid = a.samples * p.chunks;
@@ -708,14 +713,12 @@ atlas_status resident(const Params &p, const Plan &plan, bool bwd, cudaStream_t 
 
 template <typename T, int V>
 void split(const Params &p, const Plan &plan, bool bwd, cudaStream_t s) {
-    const int64_t nv = p.channels / V;
-    const dim3 grid(static_cast<unsigned>(plan.grid),
-                    static_cast<unsigned>((nv + kThreads - 1) / kThreads));
-    const unsigned join =
-        static_cast<unsigned>((p.samples * p.groups + kThreads / 32 - 1) / (kThreads / 32));
+    const dim3 grid(static_cast<unsigned>(plan.grid), static_cast<unsigned>(plan.slices_y));
+    const unsigned join = static_cast<unsigned>(p.samples * p.groups);
     if (bwd) {
+        const unsigned more = p.n_parts > 0 ? static_cast<unsigned>((p.channels + 31) / 32) : 0;
         norm_split_sums_kernel<T, V, true><<<grid, kThreads, 0, s>>>(p);
-        norm_split_join_kernel<true><<<join, kThreads, 0, s>>>(p);
+        norm_split_join_kernel<true><<<join + more, kThreads, 0, s>>>(p);
         norm_split_apply_kernel<T, V, true><<<grid, kThreads, 0, s>>>(p);
     } else {
         norm_split_sums_kernel<T, V, false><<<grid, kThreads, 0, s>>>(p);
@@ -728,8 +731,7 @@ template <typename T>
 atlas_status launch(const Params &p, const Plan &plan, bool bwd, cudaStream_t s) {
     constexpr int V = Io<T>::kVec;
     if (plan.form == kHeads) {
-        const dim3 grid(static_cast<unsigned>(plan.grid),
-                        static_cast<unsigned>((p.channels / V + kThreads - 1) / kThreads));
+        const dim3 grid(static_cast<unsigned>(plan.grid), static_cast<unsigned>(plan.slices_y));
         switch (plan.lanes) {
             case 1: heads<T, 1>(p, grid, bwd, s); break;
             case 2: heads<T, 2>(p, grid, bwd, s); break;
@@ -759,9 +761,7 @@ int64_t group_norm_workspace(const NormArgs &a, bool bwd) {
 atlas_status launch_group_norm(const NormArgs &a, bool bwd, cudaStream_t stream) {
     const Plan plan = plan_of(a, bwd);
     const int vec = 16 / a.elem_bytes;
-    const int64_t columns = a.channels / (plan.vec ? vec : 1);
-    if (plan.form != kResident && (columns + kThreads - 1) / kThreads > 65535)
-        return ATLAS_ERR_SHAPE;
+    if (plan.slices_y > 65535) return ATLAS_ERR_SHAPE;
     Params p{};
     p.x = a.x;
     p.dy = a.dy;
@@ -778,6 +778,8 @@ atlas_status launch_group_norm(const NormArgs &a, bool bwd, cudaStream_t stream)
     p.cg = static_cast<int32_t>(a.channels / a.groups);
     p.silu = a.act == ATLAS_ACT_SILU;
     p.eps = static_cast<float>(a.eps);
+    p.width = plan.width;
+    p.per_block = plan.per_block;
     p.slice_groups = plan.slice_groups;
     p.slices = plan.slices;
     p.team = plan.team;
@@ -800,7 +802,7 @@ atlas_status launch_group_norm(const NormArgs &a, bool bwd, cudaStream_t stream)
     const atlas_status st = a.elem_bytes == 2 ? launch<__nv_bfloat16>(p, plan, bwd, stream)
                                               : launch<float>(p, plan, bwd, stream);
     if (st != ATLAS_OK) return st;
-    if (sums)
+    if (sums && plan.form != kSplit)
         norm_dgamma_kernel<<<static_cast<unsigned>((a.channels + 31) / 32), kThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
