@@ -205,6 +205,8 @@ def _declare(lib):
 def lib():
     """The loaded library. Raises if ``libatlas.so`` has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -547,33 +549,51 @@ def _require(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _same_device(ref, *tensors):
-    """Every tensor (None skipped) on ref's CUDA device."""
-    _require(ref.is_cuda, "tensors must live on a CUDA device")
+def _on(dev: int, *tensors):
+    """Every tensor (None skipped) on CUDA device ``dev``."""
     for t in tensors:
-        _require(t is None or t.device == ref.device, "tensors must live on one device")
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise ValueError("tensors must live on one CUDA device")
 
 
 def _fp32(n, what, *tensors):
     import torch
     for t in tensors:
-        _require(t is None or (t.dtype == torch.float32 and t.numel() == n),
-                 f"{what}: fp32 of {n} elements expected")
+        if t is not None and (t.dtype != torch.float32 or t.numel() != n):
+            raise ValueError(f"{what}: fp32 of {n} elements expected")
 
 
-def _run(where, ref, stream, call):
-    """call(stream pointer) with ref's device current; raises on a status."""
+def _at(t):
+    """Device address of a contiguous tensor (None: NULL)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _run(where, dev, stream, fn, *args):
+    """fn(*args, stream) with device ``dev`` current; raises on a status."""
     import torch
-    if ref.device.index == torch.cuda.current_device():
-        _check(call(_stream(ref, stream)), where)
-        return
-    with torch.cuda.device(ref.device):
-        _check(call(_stream(ref, stream)), where)
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _run(where, dev, stream, fn, *args)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    status = fn(*args, stream.cuda_stream)
+    if status != OK:
+        raise AtlasError(status, where)
 
 
-def _scratch(ref, stream, nbytes):
-    """A workspace whose memory goes back to the pool of the stream using it."""
+def _work(workspace, ref, stream, nbytes):
+    """The caller's workspace once checked, or a new one whose memory goes back
+    to the pool of the stream using it."""
     import torch
+    if workspace is not None:
+        _on(ref.get_device(), workspace)
+        _require(workspace.numel() * workspace.element_size() >= nbytes,
+                 "the workspace is smaller than the call needs")
+        return workspace
     if nbytes == 0:
         return None
     if stream is None:
@@ -582,25 +602,14 @@ def _scratch(ref, stream, nbytes):
         return torch.empty(nbytes, dtype=torch.uint8, device=ref.device)
 
 
-def _work(workspace, ref, stream, nbytes):
-    """The caller's workspace once checked, or a new one."""
-    if workspace is None:
-        return _scratch(ref, stream, nbytes)
-    _same_device(ref, workspace)
-    _require(workspace.numel() * workspace.element_size() >= nbytes,
-             f"workspace of {nbytes} bytes expected")
-    return workspace
-
-
 def _rows(t):
-    """(pointer, row stride in elements) of [rows, heads, head_dim] whose rows
+    """(address, row stride in elements) of [rows, heads, head_dim] whose rows
     are contiguous, as a slice of a wider buffer's columns is."""
-    _require(t.is_cuda, "tensors must live on a CUDA device")
-    _require(t.dim() == 3 and (t.shape[2] == 1 or t.stride(2) == 1) and
-             (t.shape[1] == 1 or t.stride(1) == t.shape[2]),
+    n, heads, hd = t.shape
+    s0, s1, s2 = t.stride()
+    _require((hd == 1 or s2 == 1) and (heads == 1 or s1 == hd),
              "tensors must be [rows, heads, head_dim] with contiguous rows")
-    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-    return t.data_ptr(), stride
+    return t.data_ptr(), s0 if n > 1 else heads * hd
 
 
 def rotary(tensors, grid, rot: Rotary, *, cube=None, order="raster", positions=None,
@@ -616,77 +625,86 @@ def rotary(tensors, grid, rot: Rotary, *, cube=None, order="raster", positions=N
     import torch
     _require(len(tensors) > 0, "at least one tensor")
     ref = tensors[0][0]
+    dev, dtype, hd = ref.get_device(), ref.dtype, ref.shape[-1]
     rows = int(batch) * grid[0] * grid[1] * grid[2]
     items = (RotaryTensor * len(tensors))()
     for item, t in zip(items, tensors):
         src, dst = t[0], t[1]
-        _same_device(ref, src, dst)
-        _require(src.shape == dst.shape and src.shape[0] == rows and
-                 src.shape[2] == ref.shape[2], "rotary: src and dst of [batch*T*H*W, heads, "
-                 "head_dim], one head_dim for all")
-        _require(src.dtype == ref.dtype and dst.dtype == ref.dtype, "rotary: one dtype for all")
+        _on(dev, src, dst)
+        _require(src.dim() == 3 and src.shape == dst.shape and src.shape[0] == rows and
+                 src.shape[2] == hd, "rotary: src and dst of [batch*T*H*W, heads, head_dim], one "
+                 "head_dim for all")
+        _require(src.dtype == dtype and dst.dtype == dtype, "rotary: one dtype for all")
         item.src, item.src_stride = _rows(src)
         item.dst, item.dst_stride = _rows(dst)
         item.heads, item.rotate = src.shape[1], int(bool(t[2]) if len(t) > 2 else True)
     axes = 0
     if positions is not None:
-        _same_device(ref, positions)
-        _require(positions.dtype == torch.int32 and positions.shape[0] == rows and
-                 positions.dim() <= 2, "rotary: positions are int32 [batch*T*H*W(, axes)]")
+        _on(dev, positions)
+        _require(positions.dtype == torch.int32 and positions.dim() in (1, 2) and
+                 positions.shape[0] == rows, "rotary: positions are int32 [batch*T*H*W(, axes)]")
         axes = positions.shape[1] if positions.dim() == 2 else 1
     if bool(rot.transpose) != bool(transpose):
         rot = Rotary.from_buffer_copy(rot)
         rot.transpose = int(bool(transpose))
     c = ctypes.byref(Cube3(*cube)) if cube is not None else None
-    _run("atlas_rotary_apply", ref, stream, lambda s: lib().atlas_rotary_apply(
-        items, len(tensors), int(batch), Grid3(*grid), c, ORDERS[order], _ptr(positions), axes,
-        ref.shape[2], _dtype_code(ref), ctypes.byref(rot), s))
+    _run("atlas_rotary_apply", dev, stream, lib().atlas_rotary_apply, items, len(tensors), int(batch),
+         Grid3(*grid), c, ORDERS[order], _at(positions), axes, hd, _dtype_code(ref),
+         ctypes.byref(rot))
     return [t[1] for t in tensors]
+
+
+def _vectors(what, vectors, scalars):
+    """(device, n, d) of lambda's [n, d] vectors, all of one dtype, and its [n]."""
+    q1 = vectors[0]
+    _on(q1.get_device(), *vectors, scalars)
+    for t in vectors:
+        _require(t.dim() == 2 and t.shape == q1.shape and t.dtype == q1.dtype,
+                 "diff_lambda: vectors of [n, d] and one dtype")
+    _fp32(q1.shape[0], what, scalars)
+    return q1.get_device(), q1.shape[0], q1.shape[1]
 
 
 def diff_lambda(q1, k1, q2, k2, lambda_init, lam, stream=None):
     """lam [n] = exp<q1,k1> - exp<q2,k2> + lambda_init from vectors [n, d]."""
-    _same_device(q1, k1, q2, k2, lam)
-    _require(q1.dim() == 2 and all(t.shape == q1.shape and t.dtype == q1.dtype
-                                   for t in (k1, q2, k2)), "diff_lambda: four [n, d] of one dtype")
-    _fp32(q1.shape[0], "diff_lambda lam", lam)
-    _run("atlas_diff_lambda", q1, stream, lambda s: lib().atlas_diff_lambda(
-        _ptr(q1), _ptr(k1), _ptr(q2), _ptr(k2), q1.shape[0], q1.shape[1], float(lambda_init),
-        _dtype_code(q1), _ptr(lam), s))
+    dev, n, d = _vectors("diff_lambda lam", (q1, k1, q2, k2), lam)
+    _run("atlas_diff_lambda", dev, stream, lib().atlas_diff_lambda, _at(q1), _at(k1), _at(q2),
+         _at(k2), n, d, float(lambda_init), _dtype_code(q1), _at(lam))
     return lam
 
 
 def diff_lambda_bwd(q1, k1, q2, k2, dlam, dq1, dk1, dq2, dk2, stream=None):
     """Gradients of ``diff_lambda``'s vectors from dlam [n]."""
-    _same_device(q1, k1, q2, k2, dlam, dq1, dk1, dq2, dk2)
-    _require(q1.dim() == 2 and all(t.shape == q1.shape and t.dtype == q1.dtype
-                                   for t in (k1, q2, k2, dq1, dk1, dq2, dk2)),
-             "diff_lambda_bwd: eight [n, d] of one dtype")
-    _fp32(q1.shape[0], "diff_lambda_bwd dlam", dlam)
-    _run("atlas_diff_lambda_bwd", q1, stream, lambda s: lib().atlas_diff_lambda_bwd(
-        _ptr(q1), _ptr(k1), _ptr(q2), _ptr(k2), q1.shape[0], q1.shape[1], _ptr(dlam),
-        _dtype_code(q1), _ptr(dq1), _ptr(dk1), _ptr(dq2), _ptr(dk2), s))
+    dev, n, d = _vectors("diff_lambda_bwd dlam", (q1, k1, q2, k2, dq1, dk1, dq2, dk2), dlam)
+    _run("atlas_diff_lambda_bwd", dev, stream, lib().atlas_diff_lambda_bwd, _at(q1), _at(k1), _at(q2),
+         _at(k2), n, d, _at(dlam), _dtype_code(q1), _at(dq1), _at(dk1), _at(dq2), _at(dk2))
     return dq1, dk1, dq2, dk2
 
 
 def _diff_sides(batch, detail, glob, window_offsets, global_window_offsets, window_len, lam):
     """Shapes shared by diff_attn and its backward: (reference tensor, detail
-    rows and global rows of one problem, layout). None stands for no rows."""
+    rows and global rows of one problem, addresses of both sides, layout). None
+    stands for no rows."""
     import torch
+    batch = int(batch)
     ref = next((t for t in (*detail, *glob) if t is not None and t.shape[0] > 0), None)
-    _require(ref is not None and ref.dim() == 3 and int(batch) >= 1,
+    _require(ref is not None and ref.dim() == 3 and batch >= 1,
              "diff_attn: [rows, heads, head_dim] tensors and batch >= 1")
-    counts = []
+    dev, dtype, tail = ref.get_device(), ref.dtype, ref.shape[1:]
+    counts, sides = [], []
     for side in (detail, glob):
         n = side[0].shape[0] if side[0] is not None else 0
-        for t in side:
-            _require(n == 0 or t is None or (tuple(t.shape) == (n, *ref.shape[1:]) and
-                                             t.dtype == ref.dtype),
-                     "diff_attn: tensors of one side have one shape and dtype")
-        _require(n % int(batch) == 0, "diff_attn: rows are not a multiple of batch")
-        _same_device(ref, *(t for t in side if n > 0))
-        counts.append(n // int(batch))
-    _same_device(ref, lam, window_offsets, global_window_offsets)
+        _require(n % batch == 0, "diff_attn: rows are not a multiple of batch")
+        if n == 0:
+            sides.append([None] * len(side))
+        else:
+            _on(dev, *side)
+            for t in side:
+                _require(t is None or (t.shape[0] == n and t.shape[1:] == tail and t.dtype == dtype),
+                         "diff_attn: tensors of one side have one shape and dtype")
+            sides.append([_at(t) for t in side])
+        counts.append(n // batch)
+    _on(dev, lam, window_offsets, global_window_offsets)
     _require(lam.numel() in (1, ref.shape[1]), "diff_attn: lam has one entry or one per head")
     _fp32(lam.numel(), "diff_attn lam", lam)
     for off in (window_offsets, global_window_offsets):
@@ -696,10 +714,9 @@ def _diff_sides(batch, detail, glob, window_offsets, global_window_offsets, wind
         _require(window_offsets.numel() == global_window_offsets.numel(),
                  "diff_attn: one global range per window")
     first = window_offsets if window_offsets is not None else global_window_offsets
-    address = lambda t: _ptr(t).value if t is not None else None
-    ly = AttnLayout(int(batch), int(window_len), address(window_offsets),
-                    first.numel() - 1 if first is not None else 0, address(global_window_offsets))
-    return ref, counts[0], counts[1], ly
+    ly = AttnLayout(batch, int(window_len), _at(window_offsets),
+                    first.numel() - 1 if first is not None else 0, _at(global_window_offsets))
+    return ref, counts[0], counts[1], sides[0], sides[1], ly
 
 
 def diff_attn(q_d, k_d, v_d, q_g, k_g, v_g, lam, o_d, o_g, s_d=None, s_g=None, lse=None, *,
@@ -709,16 +726,15 @@ def diff_attn(q_d, k_d, v_d, q_g, k_g, v_g, lam, o_d, o_g, s_d=None, s_g=None, l
     the layouts of ``local_global_attn_ex``; the halves of a head are the two
     maps. lam: fp32, one entry or one per head. For ``diff_attn_bwd`` pass s_d
     and s_g (the second map's output) and lse (fp32 [batch, heads, 2, N+G])."""
-    ref, n_d, n_g, ly = _diff_sides(batch, (q_d, k_d, v_d, o_d, s_d), (q_g, k_g, v_g, o_g, s_g),
-                                    window_offsets, global_window_offsets, window_len, lam)
+    ref, n_d, n_g, d, g, ly = _diff_sides(
+        batch, (q_d, k_d, v_d, o_d, s_d), (q_g, k_g, v_g, o_g, s_g), window_offsets,
+        global_window_offsets, window_len, lam)
     heads, hd = ref.shape[1], ref.shape[2]
-    _same_device(ref, lse)
-    _fp32(2 * int(batch) * heads * (n_d + n_g), "diff_attn lse", lse)
-    nz = lambda t, n: _ptr(t) if n > 0 else None
-    _run("atlas_diff_attn", ref, stream, lambda s: lib().atlas_diff_attn(
-        nz(q_d, n_d), nz(k_d, n_d), nz(v_d, n_d), n_d, nz(q_g, n_g), nz(k_g, n_g), nz(v_g, n_g),
-        n_g, ctypes.byref(ly), heads, hd, float(softmax_scale), _dtype_code(ref), _ptr(lam),
-        lam.numel(), nz(o_d, n_d), nz(o_g, n_g), nz(s_d, n_d), nz(s_g, n_g), _ptr(lse), s))
+    _on(ref.get_device(), lse)
+    _fp32(2 * ly.batch * heads * (n_d + n_g), "diff_attn lse", lse)
+    _run("atlas_diff_attn", ref.get_device(), stream, lib().atlas_diff_attn, d[0], d[1], d[2], n_d,
+         g[0], g[1], g[2], n_g, ctypes.byref(ly), heads, hd, float(softmax_scale), _dtype_code(ref),
+         _at(lam), lam.numel(), d[3], g[3], d[4], g[4], _at(lse))
     return o_d, o_g
 
 
@@ -729,24 +745,20 @@ def diff_attn_bwd(q_d, k_d, v_d, o_d, s_d, do_d, q_g, k_g, v_g, o_g, s_g, do_g, 
     """Gradients of ``diff_attn`` (same layout arguments): dq_*, dk_*, dv_* and
     dlam (as lam). workspace: any dtype, of at least
     ``diff_attn_bwd_workspace`` bytes; allocated here when not given."""
-    ref, n_d, n_g, ly = _diff_sides(
+    ref, n_d, n_g, d, g, ly = _diff_sides(
         batch, (q_d, k_d, v_d, o_d, s_d, do_d, dq_d, dk_d, dv_d),
         (q_g, k_g, v_g, o_g, s_g, do_g, dq_g, dk_g, dv_g), window_offsets, global_window_offsets,
         window_len, lam)
-    heads, hd = ref.shape[1], ref.shape[2]
-    _same_device(ref, lse, dlam)
-    _fp32(2 * int(batch) * heads * (n_d + n_g), "diff_attn_bwd lse", lse)
+    dev, heads, hd = ref.get_device(), ref.shape[1], ref.shape[2]
+    _on(dev, lse, dlam)
+    _fp32(2 * ly.batch * heads * (n_d + n_g), "diff_attn_bwd lse", lse)
     _fp32(lam.numel(), "diff_attn_bwd dlam", dlam)
+    code = _dtype_code(ref)
     work = _work(workspace, ref, stream,
-                 int(lib().atlas_diff_attn_bwd_workspace(int(batch), n_d, n_g, heads, hd,
-                                                         _dtype_code(ref))))
-    nz = lambda t, n: _ptr(t) if n > 0 else None
-    _run("atlas_diff_attn_bwd", ref, stream, lambda s: lib().atlas_diff_attn_bwd(
-        nz(q_d, n_d), nz(k_d, n_d), nz(v_d, n_d), nz(o_d, n_d), nz(s_d, n_d), nz(do_d, n_d), n_d,
-        nz(q_g, n_g), nz(k_g, n_g), nz(v_g, n_g), nz(o_g, n_g), nz(s_g, n_g), nz(do_g, n_g), n_g,
-        ctypes.byref(ly), heads, hd, float(softmax_scale), _dtype_code(ref), _ptr(lam),
-        lam.numel(), _ptr(lse), _ptr(work), nz(dq_d, n_d), nz(dk_d, n_d), nz(dv_d, n_d),
-        nz(dq_g, n_g), nz(dk_g, n_g), nz(dv_g, n_g), _ptr(dlam), s))
+                 lib().atlas_diff_attn_bwd_workspace(ly.batch, n_d, n_g, heads, hd, code))
+    _run("atlas_diff_attn_bwd", dev, stream, lib().atlas_diff_attn_bwd, *d[:6], n_d, *g[:6], n_g,
+         ctypes.byref(ly), heads, hd, float(softmax_scale), code, _at(lam), lam.numel(), _at(lse),
+         _at(work), *d[6:], *g[6:], _at(dlam))
     return dq_d, dk_d, dv_d, dq_g, dk_g, dv_g, dlam
 
 
@@ -758,15 +770,17 @@ def diff_attn_bwd_workspace(batch, n_detail, n_global, heads, head_dim, dtype) -
 
 
 def _norm_sizes(x, rows, groups, tensors, vectors, stats):
-    _require(x.dim() == 2 and int(rows) >= 1 and x.shape[0] % int(rows) == 0,
+    rows = int(rows)
+    _require(x.dim() == 2 and rows >= 1 and x.shape[0] % rows == 0,
              "group_norm: x is [samples*rows, channels]")
-    _same_device(x, *tensors, *vectors, stats)
-    _require(all(t.shape == x.shape and t.dtype == x.dtype for t in tensors),
-             "group_norm: tensors of x's shape and dtype")
+    _on(x.get_device(), x, *tensors, *vectors, stats)
+    for t in tensors:
+        _require(t.shape == x.shape and t.dtype == x.dtype,
+                 "group_norm: tensors of x's shape and dtype")
     _fp32(x.shape[1], "group_norm gamma and beta", *vectors)
-    samples = x.shape[0] // int(rows)
+    samples = x.shape[0] // rows
     _fp32(2 * samples * int(groups), "group_norm stats", stats)
-    return samples
+    return samples, rows, x.shape[1], int(groups)
 
 
 def group_norm(x, gamma, beta, y, rows, groups, *, eps=1e-5, activation="none", stats=None,
@@ -775,11 +789,10 @@ def group_norm(x, gamma, beta, y, rows, groups, *, eps=1e-5, activation="none", 
     consecutive rows (rows 1, groups = heads: each head of a token by itself).
     gamma, beta: fp32 [channels] or None. stats: fp32 [samples, groups, 2],
     needed by ``group_norm_bwd``. activation "none" or "silu"."""
-    samples = _norm_sizes(x, rows, groups, (y,), (gamma, beta), stats)
-    work = _work(workspace, x, stream, group_norm_workspace(x, rows, groups, False))
-    _run("atlas_group_norm", x, stream, lambda s: lib().atlas_group_norm(
-        _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), samples, int(rows), x.shape[1], int(groups),
-        float(eps), ACTIVATIONS[activation], _dtype_code(x), _ptr(stats), _ptr(work), s))
+    sizes, code = _norm_sizes(x, rows, groups, (y,), (gamma, beta), stats), _dtype_code(x)
+    work = _work(workspace, x, stream, lib().atlas_group_norm_workspace(*sizes, code, 0))
+    _run("atlas_group_norm", x.get_device(), stream, lib().atlas_group_norm, _at(x), _at(gamma),
+         _at(beta), _at(y), *sizes, float(eps), ACTIVATIONS[activation], code, _at(stats), _at(work))
     return y
 
 
@@ -788,12 +801,12 @@ def group_norm_bwd(dy, x, gamma, beta, stats, dx, dgamma, dbeta, rows, groups, *
     """dx, and dgamma and dbeta (fp32 [channels], or None), of ``group_norm``
     from dy and the forward's x and stats."""
     _require(stats is not None, "group_norm_bwd: the forward's stats")
-    samples = _norm_sizes(x, rows, groups, (dy, dx), (gamma, beta, dgamma, dbeta), stats)
-    work = _work(workspace, x, stream, group_norm_workspace(x, rows, groups, True))
-    _run("atlas_group_norm_bwd", x, stream, lambda s: lib().atlas_group_norm_bwd(
-        _ptr(dy), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(stats), _ptr(dx), _ptr(dgamma),
-        _ptr(dbeta), samples, int(rows), x.shape[1], int(groups), ACTIVATIONS[activation],
-        _dtype_code(x), _ptr(work), s))
+    sizes = _norm_sizes(x, rows, groups, (dy, dx), (gamma, beta, dgamma, dbeta), stats)
+    code = _dtype_code(x)
+    work = _work(workspace, x, stream, lib().atlas_group_norm_workspace(*sizes, code, 1))
+    _run("atlas_group_norm_bwd", x.get_device(), stream, lib().atlas_group_norm_bwd, _at(dy), _at(x),
+         _at(gamma), _at(beta), _at(stats), _at(dx), _at(dgamma), _at(dbeta), *sizes,
+         ACTIVATIONS[activation], code, _at(work))
     return dx, dgamma, dbeta
 
 

@@ -36,7 +36,10 @@ constexpr int kThreads = 256;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kSms = 148;                    // of a B200: grids and workspaces are sized by it
 constexpr int64_t kResidentBytes = 96 * 1024;
-constexpr int64_t kSplitBlocks = 8 * kSms;   // blocks of a split pass
+// Blocks of a split pass. Decoder latents (2 x 322,560 x 128), microseconds of the
+// four passes: 2, 4, 8 and 16 blocks an SM 294, 299, 309 and 412: few blocks with
+// long loops. Four fill the SMs at every register count.
+constexpr int64_t kSplitBlocks = 4 * kSms;
 constexpr int64_t kPartBlocks = 4 * kSms;    // blocks of a backward pass that keep dgamma sums
 
 struct Params {
@@ -393,7 +396,7 @@ __device__ __forceinline__ Slot slot_of(const Params &p, int64_t nv) {
 // dz xhat, sum dz).
 template <typename T, int V, bool BWD>
 __global__ void __launch_bounds__(kThreads) norm_split_sums_kernel(const Params p) {
-    constexpr int kFlight = BWD ? 4 : 8;
+    constexpr int kFlight = 4;
     __shared__ float2 sums[kThreads][V + 1];
     const Slot t = slot_of(p, p.channels / V);
     const int64_t ch = static_cast<int64_t>(t.col) * V;
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(kThreads) norm_split_join_kernel(const Params 
 // The result, rows of all samples last to first.
 template <typename T, int V, bool BWD>
 __global__ void __launch_bounds__(kThreads) norm_split_apply_kernel(const Params p) {
-    constexpr int kFlight = 4;
+    constexpr int kFlight = BWD ? 4 : 8;
     const Slot t = slot_of(p, p.channels / V);
     if (!t.active) return;
     const int64_t ch = static_cast<int64_t>(t.col) * V;
@@ -647,7 +650,7 @@ Plan plan_of(const NormArgs &a, bool bwd) {
             p.lanes = static_cast<int>(lanes);
             slice_columns(a.channels / vec, &p);
             const int64_t tokens = (a.samples + p.per_block - 1) / p.per_block;
-            p.grid = std::min<int64_t>(tokens, bwd ? kPartBlocks : 16 * kSms);
+            p.grid = std::min<int64_t>(tokens, bwd ? kPartBlocks : 8 * kSms);
             p.parts = static_cast<int32_t>(p.grid);
             p.part_bytes = bwd ? p.parts * a.channels * 8 : 0;
             return p;
