@@ -898,7 +898,7 @@ ATLAS_API atlas_status atlas_diff_attn(const void *q_d, const void *k_d, const v
     d.s_d = s_d;
     d.s_g = s_g;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    return dtype == ATLAS_BF16 ? launch_diff_attn_tc(d, cs) : launch_diff_attn_simt(d, cs);
+    return dtype == ATLAS_BF16 ? launch_diff_attn_tc(d, cs) : launch_diff_attn_simt_f32(d, cs);
 }
 
 ATLAS_API int64_t atlas_diff_attn_bwd_workspace(int64_t batch, int64_t n_detail,
@@ -964,7 +964,7 @@ ATLAS_API atlas_status atlas_diff_attn_bwd(
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (rows > 0) {
         if ((st = launch_diff_bwd_delta(b, s)) != ATLAS_OK) return st;
-        st = dtype == ATLAS_BF16 ? launch_diff_bwd_tc(b, s) : launch_diff_bwd_simt(b, s);
+        st = dtype == ATLAS_BF16 ? launch_diff_bwd_tc(b, s) : launch_diff_bwd_simt_f32(b, s);
         if (st != ATLAS_OK) return st;
     }
     return launch_diff_dlambda(b, s);

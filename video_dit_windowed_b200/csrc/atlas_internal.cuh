@@ -209,11 +209,11 @@ constexpr int kDiffLambdaParts = 64;
 int diff_split_plan(int64_t batch, int64_t n_detail, int64_t n_global, int32_t heads);
 atlas_status launch_diff_lambda(const DiffLambdaArgs &a, bool bwd, cudaStream_t stream);
 atlas_status launch_diff_attn_tc(const DiffArgs &a, cudaStream_t stream);   // bf16
-atlas_status launch_diff_attn_simt(const DiffArgs &a, cudaStream_t stream);
+atlas_status launch_diff_attn_simt_f32(const DiffArgs &a, cudaStream_t stream);
 atlas_status launch_diff_bwd_delta(const DiffBwdArgs &a, cudaStream_t stream);
 atlas_status launch_diff_dlambda(const DiffBwdArgs &a, cudaStream_t stream);
 atlas_status launch_diff_bwd_tc(const DiffBwdArgs &a, cudaStream_t stream);      // bf16
-atlas_status launch_diff_bwd_simt(const DiffBwdArgs &a, cudaStream_t stream);
+atlas_status launch_diff_bwd_simt_f32(const DiffBwdArgs &a, cudaStream_t stream);
 
 // Group norm (group_norm.cu).
 struct NormArgs {

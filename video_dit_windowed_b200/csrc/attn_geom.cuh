@@ -1,6 +1,6 @@
 // attn_geom.cuh -- which keys a query row sees, and which queries see a key:
 // the windows, global tokens and aligned ranges of atlas_attn_layout, for the
-// differential attention's SIMT kernels. All counts are per problem. Ranges from
+// differential attention's row-sum and fp32 kernels. All counts are per problem. Ranges from
 // offset arrays are clamped, so any contents keep every access in bounds; a
 // detail row always sees its own key.
 #pragma once

@@ -1,5 +1,6 @@
 // diff_attn.cu -- differential attention: the weight lambda and its gradient,
-// the backward pass' row sums, and SIMT kernels of the attention.
+// and the backward pass' row sums (the attention itself: diff_attn_tc.cu,
+// diff_attn_bwd_tc.cu, diff_attn_simt.cu).
 //
 // With s_m = scale <q_m, k_m> of the two maps of a head (the halves of its
 // channels) over a row's allowed keys:
@@ -160,207 +161,6 @@ __global__ void __launch_bounds__(32) dlambda_join_kernel(const float *part, flo
 }
 
 // ---------------------------------------------------------------------------
-// SIMT attention: one warp per (row, head), exact fp32 products, online softmax
-// of both maps. A lane's channels lane + 32 e belong to map e / (HD / 64).
-// ---------------------------------------------------------------------------
-template <typename T>
-struct FwdPtr {
-    const T *q_d, *k_d, *v_d, *q_g, *k_g, *v_g;
-    T *o_d, *o_g, *s_d, *s_g;
-    const float *lambda;
-    int32_t n_lambda;
-    float *lse;
-    float scale;
-};
-
-template <int HD>
-struct Row {
-    static constexpr int kE = HD / 32, kMap = HD / 64;
-    float x[kE];
-    template <typename T>
-    __device__ __forceinline__ void load(const T *p) {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) x[e] = to_f(p[lane + 32 * e]);
-    }
-    template <typename T>
-    __device__ __forceinline__ void store(T *p, float f) const {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) p[lane + 32 * e] = from_f<T>(x[e] * f);
-    }
-    // <x, y> of map m, and of the whole row.
-    __device__ __forceinline__ float dot(const Row &y, int m) const {
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < kMap; ++e) s = fmaf(x[m * kMap + e], y.x[m * kMap + e], s);
-        return warp_sum(s);
-    }
-    __device__ __forceinline__ float dot(const Row &y) const {
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) s = fmaf(x[e], y.x[e], s);
-        return warp_sum(s);
-    }
-    __device__ __forceinline__ void add(float f, const Row &y) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) x[e] = fmaf(f, y.x[e], x[e]);
-    }
-    // x += (f1, f2) y, a factor for each map.
-    __device__ __forceinline__ void add(float f1, float f2, const Row &y) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) x[e] = fmaf(e < kMap ? f1 : f2, y.x[e], x[e]);
-    }
-    __device__ __forceinline__ void times(float f) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) x[e] *= f;
-    }
-    __device__ __forceinline__ void zero() { times(0.f); }
-};
-
-template <typename T, int HD>
-__global__ void __launch_bounds__(kWarps * 32) diff_simt_kernel(const FwdPtr<T> p,
-                                                                const AttnGeom g) {
-    const int lane = threadIdx.x & 31, head = blockIdx.y;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
-    if (row >= g.batch * (g.N + g.G)) return;
-    const geo::RowAt at = geo::row_at(g, row);
-    const int64_t stride = static_cast<int64_t>(g.heads) * HD, off = at.row * stride + head * HD;
-    Row<HD> q, o[2], k, v;
-    q.load((at.detail ? p.q_d : p.q_g) + off);
-#pragma unroll
-    for (int e = 0; e < Row<HD>::kE; ++e) o[0].x[e] = o[1].x[e] = 0.f;
-    float m[2] = {-__builtin_huge_valf(), -__builtin_huge_valf()}, l[2] = {0.f, 0.f};
-    auto keys = [&](const T *kp, const T *vp, int64_t k0, int64_t k1) {
-        for (int64_t j = k0; j < k1; ++j) {
-            k.load(kp + j * stride);
-            v.load(vp + j * stride);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float s = q.dot(k, i) * p.scale;
-                const float m_new = fmaxf(m[i], s);
-                const float corr = expf(m[i] - m_new), pr = expf(s - m_new);
-                l[i] = fmaf(l[i], corr, pr);
-                o[i].times(corr);
-                o[i].add(pr, v);
-                m[i] = m_new;
-            }
-        }
-    };
-    int64_t g_lo = 0, g_hi = g.G;
-    if (at.detail) {
-        int64_t lo, hi;
-        const int64_t w = geo::window_at(g, at.local, lo, hi);
-        geo::global_keys(g, w, g_lo, g_hi);
-        keys(p.k_d + at.b * g.N * stride + head * HD, p.v_d + at.b * g.N * stride + head * HD, lo,
-             hi);
-    }
-    keys(p.k_g + at.b * g.G * stride + head * HD, p.v_g + at.b * g.G * stride + head * HD, g_lo,
-         g_hi);
-    const float lam = p.lambda[p.n_lambda == 1 ? 0 : head];
-    o[1].times(1.f / l[1]);
-    T *s_out = at.detail ? p.s_d : p.s_g;
-    if (s_out != nullptr) o[1].store(s_out + off, 1.f);
-    o[0].times(1.f / l[0]);
-    o[0].add(-lam, o[1]);
-    o[0].store((at.detail ? p.o_d : p.o_g) + off, 1.f);
-    if (p.lse != nullptr && lane < 2) {
-        const int64_t rows = g.N + g.G;
-        p.lse[((at.b * g.heads + head) * 2 + lane) * rows + (at.detail ? at.local : g.N + at.local)] =
-            lane == 0 ? m[0] + logf(l[0]) : m[1] + logf(l[1]);
-    }
-}
-
-template <typename T>
-struct BwdPtr {
-    const T *q_d, *k_d, *v_d, *do_d, *q_g, *k_g, *v_g, *do_g;
-    const float *lse, *delta, *lambda;
-    int32_t n_lambda;
-    T *dq_d, *dk_d, *dv_d, *dq_g, *dk_g, *dv_g;
-    float scale;
-};
-
-template <typename T, int HD>
-__global__ void __launch_bounds__(kWarps * 32) diff_dq_simt_kernel(const BwdPtr<T> p,
-                                                                   const AttnGeom g) {
-    const int head = blockIdx.y;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
-    if (row >= g.batch * (g.N + g.G)) return;
-    const geo::RowAt at = geo::row_at(g, row);
-    const int64_t stride = static_cast<int64_t>(g.heads) * HD, off = at.row * stride + head * HD;
-    const int64_t rows = g.N + g.G;
-    const int64_t col = (at.b * g.heads + head) * 2 * rows + (at.detail ? at.local : g.N + at.local);
-    const float lam = p.lambda[p.n_lambda == 1 ? 0 : head];
-    const float lse1 = p.lse[col], lse2 = p.lse[col + rows];
-    const float d1 = p.delta[col], d2 = p.delta[col + rows];
-    Row<HD> q, go, dq, k, v;
-    q.load((at.detail ? p.q_d : p.q_g) + off);
-    go.load((at.detail ? p.do_d : p.do_g) + off);
-#pragma unroll
-    for (int e = 0; e < Row<HD>::kE; ++e) dq.x[e] = 0.f;
-    auto keys = [&](const T *kp, const T *vp, int64_t k0, int64_t k1) {
-        for (int64_t j = k0; j < k1; ++j) {
-            k.load(kp + j * stride);
-            v.load(vp + j * stride);
-            const float dp = go.dot(v);
-            const float p1 = expf(q.dot(k, 0) * p.scale - lse1);
-            const float p2 = expf(q.dot(k, 1) * p.scale - lse2);
-            dq.add(p1 * (dp - d1), -lam * (p2 * (dp - d2)), k);
-        }
-    };
-    int64_t g_lo = 0, g_hi = g.G;
-    if (at.detail) {
-        int64_t lo, hi;
-        const int64_t w = geo::window_at(g, at.local, lo, hi);
-        geo::global_keys(g, w, g_lo, g_hi);
-        keys(p.k_d + at.b * g.N * stride + head * HD, p.v_d + at.b * g.N * stride + head * HD, lo,
-             hi);
-    }
-    keys(p.k_g + at.b * g.G * stride + head * HD, p.v_g + at.b * g.G * stride + head * HD, g_lo,
-         g_hi);
-    dq.store((at.detail ? p.dq_d : p.dq_g) + off, p.scale);
-}
-
-template <typename T, int HD>
-__global__ void __launch_bounds__(kWarps * 32) diff_dkdv_simt_kernel(const BwdPtr<T> p,
-                                                                     const AttnGeom g) {
-    const int head = blockIdx.y;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
-    if (row >= g.batch * (g.N + g.G)) return;
-    const geo::RowAt at = geo::row_at(g, row);
-    const int64_t stride = static_cast<int64_t>(g.heads) * HD, off = at.row * stride + head * HD;
-    const int64_t rows = g.N + g.G, base = (at.b * g.heads + head) * 2 * rows;
-    const float lam = p.lambda[p.n_lambda == 1 ? 0 : head];
-    Row<HD> k, v, dk, dv, q, go;
-    k.load((at.detail ? p.k_d : p.k_g) + off);
-    v.load((at.detail ? p.v_d : p.v_g) + off);
-#pragma unroll
-    for (int e = 0; e < Row<HD>::kE; ++e) dk.x[e] = dv.x[e] = 0.f;
-    auto queries = [&](const T *qp, const T *gp, int64_t col0, int64_t q0, int64_t q1) {
-        for (int64_t i = q0; i < q1; ++i) {
-            q.load(qp + i * stride);
-            go.load(gp + i * stride);
-            const int64_t col = base + col0 + i;
-            const float dp = go.dot(v);
-            const float p1 = expf(q.dot(k, 0) * p.scale - p.lse[col]);
-            const float p2 = expf(q.dot(k, 1) * p.scale - p.lse[col + rows]);
-            dk.add(p1 * (dp - p.delta[col]), -lam * (p2 * (dp - p.delta[col + rows])), q);
-            dv.add(p1 - lam * p2, go);
-        }
-    };
-    int64_t lo, hi;
-    if (at.detail) geo::window_at(g, at.local, lo, hi);
-    else geo::global_queries(g, at.local, lo, hi);
-    queries(p.q_d + at.b * g.N * stride + head * HD, p.do_d + at.b * g.N * stride + head * HD, 0, lo,
-            hi);
-    if (!at.detail)
-        queries(p.q_g + at.b * g.G * stride + head * HD, p.do_g + at.b * g.G * stride + head * HD,
-                g.N, 0, g.G);
-    dk.store((at.detail ? p.dk_d : p.dk_g) + off, p.scale);
-    dv.store((at.detail ? p.dv_d : p.dv_g) + off, 1.f);
-}
-
-// ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
 atlas_status launched() {
@@ -381,29 +181,6 @@ void log_rows(const char *kernel, const AttnArgs &a) {
 }
 
 template <typename T, int HD>
-atlas_status fwd_simt(const DiffArgs &d, cudaStream_t stream) {
-    const AttnArgs &a = d.attn;
-    FwdPtr<T> p;
-    p.q_d = static_cast<const T *>(a.q_d);
-    p.k_d = static_cast<const T *>(a.k_d);
-    p.v_d = static_cast<const T *>(a.v_d);
-    p.q_g = static_cast<const T *>(a.q_g);
-    p.k_g = static_cast<const T *>(a.k_g);
-    p.v_g = static_cast<const T *>(a.v_g);
-    p.o_d = static_cast<T *>(a.o_d);
-    p.o_g = static_cast<T *>(a.o_g);
-    p.s_d = static_cast<T *>(d.s_d);
-    p.s_g = static_cast<T *>(d.s_g);
-    p.lambda = d.lambda;
-    p.n_lambda = d.n_lambda;
-    p.lse = a.lse;
-    p.scale = a.scale;
-    log_rows("diff_simt_kernel", a);
-    diff_simt_kernel<T, HD><<<row_grid(a), kWarps * 32, 0, stream>>>(p, attn_geom_of(a));
-    return launched();
-}
-
-template <typename T, int HD>
 atlas_status delta_hd(const DiffBwdArgs &b, cudaStream_t stream) {
     const AttnArgs &a = b.fwd.attn;
     DeltaPtr<T> p;
@@ -419,37 +196,6 @@ atlas_status delta_hd(const DiffBwdArgs &b, cudaStream_t stream) {
     p.delta = b.delta;
     log_rows("diff_delta_kernel", a);
     diff_delta_kernel<T, HD><<<row_grid(a), kWarps * 32, 0, stream>>>(p, attn_geom_of(a));
-    return launched();
-}
-
-template <typename T, int HD>
-atlas_status bwd_simt(const DiffBwdArgs &b, cudaStream_t stream) {
-    const AttnArgs &a = b.fwd.attn;
-    BwdPtr<T> p;
-    p.q_d = static_cast<const T *>(a.q_d);
-    p.k_d = static_cast<const T *>(a.k_d);
-    p.v_d = static_cast<const T *>(a.v_d);
-    p.do_d = static_cast<const T *>(b.do_d);
-    p.q_g = static_cast<const T *>(a.q_g);
-    p.k_g = static_cast<const T *>(a.k_g);
-    p.v_g = static_cast<const T *>(a.v_g);
-    p.do_g = static_cast<const T *>(b.do_g);
-    p.lse = a.lse;
-    p.delta = b.delta;
-    p.lambda = b.fwd.lambda;
-    p.n_lambda = b.fwd.n_lambda;
-    p.dq_d = static_cast<T *>(b.dq_d);
-    p.dk_d = static_cast<T *>(b.dk_d);
-    p.dv_d = static_cast<T *>(b.dv_d);
-    p.dq_g = static_cast<T *>(b.dq_g);
-    p.dk_g = static_cast<T *>(b.dk_g);
-    p.dv_g = static_cast<T *>(b.dv_g);
-    p.scale = a.scale;
-    const AttnGeom g = attn_geom_of(a);
-    log_rows("diff_dq_simt_kernel", a);
-    diff_dq_simt_kernel<T, HD><<<row_grid(a), kWarps * 32, 0, stream>>>(p, g);
-    log_rows("diff_dkdv_simt_kernel", a);
-    diff_dkdv_simt_kernel<T, HD><<<row_grid(a), kWarps * 32, 0, stream>>>(p, g);
     return launched();
 }
 
@@ -480,14 +226,6 @@ atlas_status launch_diff_lambda(const DiffLambdaArgs &a, bool bwd, cudaStream_t 
     return launched();
 }
 
-atlas_status launch_diff_attn_simt(const DiffArgs &d, cudaStream_t stream) {
-    if (d.elem_bytes == 2)
-        return d.attn.head_dim == 128 ? fwd_simt<__nv_bfloat16, 128>(d, stream)
-                                      : fwd_simt<__nv_bfloat16, 64>(d, stream);
-    return d.attn.head_dim == 128 ? fwd_simt<float, 128>(d, stream)
-                                  : fwd_simt<float, 64>(d, stream);
-}
-
 atlas_status launch_diff_bwd_delta(const DiffBwdArgs &b, cudaStream_t stream) {
     if (b.fwd.elem_bytes == 2)
         return b.fwd.attn.head_dim == 128 ? delta_hd<__nv_bfloat16, 128>(b, stream)
@@ -505,14 +243,6 @@ atlas_status launch_diff_dlambda(const DiffBwdArgs &b, cudaStream_t stream) {
     dlambda_join_kernel<<<n, 32, 0, stream>>>(b.part, b.dlambda,
                                               kDiffLambdaParts * (n == 1 ? a.heads : 1));
     return launched();
-}
-
-atlas_status launch_diff_bwd_simt(const DiffBwdArgs &b, cudaStream_t stream) {
-    if (b.fwd.elem_bytes == 2)
-        return b.fwd.attn.head_dim == 128 ? bwd_simt<__nv_bfloat16, 128>(b, stream)
-                                          : bwd_simt<__nv_bfloat16, 64>(b, stream);
-    return b.fwd.attn.head_dim == 128 ? bwd_simt<float, 128>(b, stream)
-                                      : bwd_simt<float, 64>(b, stream);
 }
 
 }  // namespace atlas
