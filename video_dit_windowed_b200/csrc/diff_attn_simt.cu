@@ -1,15 +1,16 @@
 // diff_attn_simt.cu -- differential attention and its backward pass, fp32 I/O,
 // exact fp32 products on the FMA pipe (formulas: diff_attn.cu).
 //
-// A block of 256 threads takes 64 rows of one head of one problem (queries, or
-// keys for dK/dV) and streams the rows they meet in tiles of 32 through shared
-// memory. Threads form 16 x 16: thread (ty, tx) owns rows 4 ty .. 4 ty + 3; of a
-// 64 x 32 score tile columns tx and tx + 16; of an accumulator columns 4 tx .. +3
-// (and + 64). Scores, weights and accumulators stay in registers; the weights
-// pass through shared memory within a half-warp only, whose rows they are. At 64
-// FMAs per 8 to 12 shared-memory accesses the FMA pipe bounds a long call; a
-// short one its chain of tiles. Row pitch D + 4 floats: the 16 rows that a
-// half-warp reads side by side fall into different banks.
+// A block of 512 threads takes 64 rows of one head of one problem (queries, or
+// keys for dK/dV) and streams the rows they meet in tiles of 64 through shared
+// memory. Warp ty owns rows 4 ty .. 4 ty + 3: lane tx columns tx and tx + 32 of
+// their scores, and D / 32 columns of their accumulators. Scores, weights and
+// accumulators stay in registers; the weights pass through shared memory within
+// the warp whose rows they are. The row pitch of D + 4 floats spreads the 32 rows
+// that a warp reads side by side over the banks. Bound by latency, not by the FMA
+// pipe or shared memory (2 x 3 heads of 3,600 + 1,000 rows, D = 128, training: 256
+// threads with 4 x 4 scores each took 4.43 ms at 50 % issue, 4 x 2 over 32-row tiles
+// 5.37 ms).
 // Masked pairs get weight 0. 0 * NaN would still reach a row, so streamed rows
 // that enter a product by their weight are zeroed where they hold a non-finite
 // value, and pairs that do see such a row get the weight NaN.
@@ -18,9 +19,10 @@
 namespace atlas {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kRows = 64;     // rows of a block
-constexpr int kTile = 32;     // streamed rows of a tile
+constexpr int kTile = 64;     // streamed rows of a tile
+constexpr int kJ = kTile / 32;   // score columns of a thread
 constexpr int kPitchW = kTile + 4;
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -167,109 +169,123 @@ __device__ __forceinline__ float dot4(const float4 &a, const float4 &b, float s)
     return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, s))));
 }
 
-// s[i][j] = <a row 4 ty + i, b row tx + 16 j> over channels [d0, d1).
+// s[i][j] = <a row 4 ty + i, b row tx + 32 j> over channels [d0, d1).
 template <int HD>
 __device__ __forceinline__ void scores(const float *a, const float *b, int d0, int d1,
-                                       float (&s)[4][2]) {
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+                                       float (&s)[4][kJ]) {
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = 0.f;
-#pragma unroll 4
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) s[i][j] = 0.f;
+#pragma unroll 2
     for (int d = d0; d < d1; d += 4) {
-        float4 x[4], y[2];
+        float4 x[4], y[kJ];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             x[i] = *reinterpret_cast<const float4 *>(a + (4 * ty + i) * (HD + 4) + d);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            y[j] = *reinterpret_cast<const float4 *>(b + (tx + 16 * j) * (HD + 4) + d);
+        for (int j = 0; j < kJ; ++j)
+            y[j] = *reinterpret_cast<const float4 *>(b + (tx + 32 * j) * (HD + 4) + d);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) s[i][j] = dot4(x[i], y[j], s[i][j]);
+            for (int j = 0; j < kJ; ++j) s[i][j] = dot4(x[i], y[j], s[i][j]);
     }
 }
 
-// An accumulator of the thread's 4 rows: columns 4 tx .. +3 (+ 64 for D = 128).
+// An accumulator of the thread's 4 rows: W = D / 32 columns from W tx on. The
+// second map's channels are those of lanes 16 to 31.
+template <int W>
+struct alignas(4 * W) Cols {
+    float x[W];
+};
 template <int HD>
 struct Acc {
-    static constexpr int kC = HD / 64;
-    float4 v[4][kC];
+    static constexpr int kW = HD / 32;
+    float v[4][kW];
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int c = 0; c < kC; ++c) v[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < kW; ++c) v[i][c] = 0.f;
     }
     __device__ __forceinline__ void scale(int i, float f) {
 #pragma unroll
-        for (int c = 0; c < kC; ++c) {
-            v[i][c].x *= f;
-            v[i][c].y *= f;
-            v[i][c].z *= f;
-            v[i][c].w *= f;
-        }
+        for (int c = 0; c < kW; ++c) v[i][c] *= f;
     }
 };
-__device__ __forceinline__ void fma4(float4 &a, float f, const float4 &b) {
-    a.x = fmaf(f, b.x, a.x);
-    a.y = fmaf(f, b.y, a.y);
-    a.z = fmaf(f, b.z, a.z);
-    a.w = fmaf(f, b.w, a.w);
-}
 
-// acc += w b: w [64][kPitchW] (weights of the thread's rows), b [32][D + 4].
-// MAPS: column block c takes the weights of its map (w0 map 1, w1 map 2).
-template <int HD, bool MAPS>
-__device__ __forceinline__ void weighted(Acc<HD> &acc, const float *w0, const float *w1,
-                                         const float *b) {
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+// acc += w b: w [64][kPitchW] (weights of the thread's rows), b [64][D + 4].
+template <int HD>
+__device__ __forceinline__ void weighted(Acc<HD> &acc, const float *w, const float *b) {
+    constexpr int W = Acc<HD>::kW;
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
 #pragma unroll 2
     for (int k = 0; k < kTile; k += 4) {
-        float4 y[4][Acc<HD>::kC];
+        Cols<W> y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
+            y[e] = *reinterpret_cast<const Cols<W> *>(b + (k + e) * (HD + 4) + W * tx);
 #pragma unroll
-            for (int c = 0; c < Acc<HD>::kC; ++c)
-                y[e][c] = *reinterpret_cast<const float4 *>(b + (k + e) * (HD + 4) + 4 * tx + 64 * c);
+        for (int i = 0; i < 4; ++i) {
+            const float4 x = *reinterpret_cast<const float4 *>(w + (4 * ty + i) * kPitchW + k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int c = 0; c < W; ++c)
+                acc.v[i][c] = fmaf(x.w, y[3].x[c],
+                                   fmaf(x.z, y[2].x[c],
+                                        fmaf(x.y, y[1].x[c], fmaf(x.x, y[0].x[c], acc.v[i][c]))));
+        }
+    }
+}
+
+// Both maps' accumulators over the same b: each row of b is read once.
+template <int HD>
+__device__ __forceinline__ void weighted2(Acc<HD> &a0, Acc<HD> &a1, const float *w0,
+                                          const float *w1, const float *b) {
+    constexpr int W = Acc<HD>::kW;
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+#pragma unroll 2
+    for (int k = 0; k < kTile; k += 4) {
+        Cols<W> y[4];
 #pragma unroll
-            for (int c = 0; c < Acc<HD>::kC; ++c) {
-                const bool second = MAPS && (HD == 128 ? c == 1 : tx >= 8);
-                const float4 x = *reinterpret_cast<const float4 *>((second ? w1 : w0) +
-                                                                   (4 * ty + i) * kPitchW + k);
-                fma4(acc.v[i][c], x.x, y[0][c]);
-                fma4(acc.v[i][c], x.y, y[1][c]);
-                fma4(acc.v[i][c], x.z, y[2][c]);
-                fma4(acc.v[i][c], x.w, y[3][c]);
+        for (int e = 0; e < 4; ++e)
+            y[e] = *reinterpret_cast<const Cols<W> *>(b + (k + e) * (HD + 4) + W * tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 x0 = *reinterpret_cast<const float4 *>(w0 + (4 * ty + i) * kPitchW + k);
+            const float4 x1 = *reinterpret_cast<const float4 *>(w1 + (4 * ty + i) * kPitchW + k);
+#pragma unroll
+            for (int c = 0; c < W; ++c) {
+                a0.v[i][c] = fmaf(x0.w, y[3].x[c],
+                                  fmaf(x0.z, y[2].x[c],
+                                       fmaf(x0.y, y[1].x[c], fmaf(x0.x, y[0].x[c], a0.v[i][c]))));
+                a1.v[i][c] = fmaf(x1.w, y[3].x[c],
+                                  fmaf(x1.z, y[2].x[c],
+                                       fmaf(x1.y, y[1].x[c], fmaf(x1.x, y[0].x[c], a1.v[i][c]))));
             }
+        }
     }
 }
 
 template <int HD>
 __device__ __forceinline__ void store(float *out, const Acc<HD> &acc, int i, float f0, float f1) {
-    const int tx = threadIdx.x % 16;
+    constexpr int W = Acc<HD>::kW;
+    const int tx = threadIdx.x % 32;
+    Cols<W> v;
 #pragma unroll
-    for (int c = 0; c < Acc<HD>::kC; ++c) {
-        const float f = (HD == 128 ? c == 1 : tx >= 8) ? f1 : f0;
-        float4 v = acc.v[i][c];
-        v.x *= f;
-        v.y *= f;
-        v.z *= f;
-        v.w *= f;
-        *reinterpret_cast<float4 *>(out + 4 * tx + 64 * c) = v;
-    }
+    for (int c = 0; c < W; ++c) v.x[c] = acc.v[i][c] * (tx >= 16 ? f1 : f0);
+    *reinterpret_cast<Cols<W> *>(out + W * tx) = v;
 }
 
-__device__ __forceinline__ float half_max(float v) {
+__device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-__device__ __forceinline__ float half_sum(float v) {
+__device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
@@ -283,22 +299,22 @@ struct Ptr {
 };
 
 template <int HD>
-__global__ void __launch_bounds__(kThreads, 2) diff_simt_kernel(const Ptr p, const AttnGeom g) {
+__global__ void __launch_bounds__(kThreads) diff_simt_kernel(const Ptr p, const AttnGeom g) {
     extern __shared__ float sm[];
     float *qs = sm, *ks = qs + kRows * (HD + 4), *vs = ks + kTile * (HD + 4),
           *w = vs + kTile * (HD + 4);
     __shared__ uint8_t bad[kTile];
+    __shared__ Sees sees[kRows];
     const Span S = query_span(g);
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, side = S.detail ? 0 : 1;
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, side = S.detail ? 0 : 1;
     const int64_t stride = static_cast<int64_t>(g.heads) * HD;
     const int64_t own = (S.b * (S.detail ? g.N : g.G) + S.r0) * stride + S.head * HD;
     load_rows<HD, kRows, false>(qs, p.q[side] + own, stride, static_cast<int>(S.rend - S.r0), nullptr);
-    Sees sees[4];
     float m[2][4], l[2][4];
     Acc<HD> o[2];
+    if (threadIdx.x < kRows) sees[threadIdx.x] = query_sees(g, S, S.r0 + threadIdx.x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        sees[i] = query_sees(g, S, S.r0 + 4 * ty + i);
         m[0][i] = m[1][i] = kNegInf;
         l[0][i] = l[1][i] = 0.f;
     }
@@ -314,49 +330,49 @@ __global__ void __launch_bounds__(kThreads, 2) diff_simt_kernel(const Ptr p, con
         __syncthreads();
 #pragma unroll
         for (int map = 0; map < 2; ++map) {
-            float s[4][2];
+            float s[4][kJ];
             scores<HD>(qs, ks, map * (HD / 2), (map + 1) * (HD / 2), s);
             float *wm = w + map * kRows * kPitchW;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                bool see[2];
+                bool see[kJ];
                 float top = m[map][i];
+                const Sees mine = sees[4 * ty + i];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    see[e] = sees[i].at(det, x0 + tx + 16 * e);
+                for (int e = 0; e < kJ; ++e) {
+                    see[e] = mine.at(det, x0 + tx + 32 * e);
                     s[i][e] = see[e] ? s[i][e] * p.scale : kNegInf;
                     top = fmaxf(top, s[i][e]);
                 }
-                top = half_max(top);
+                top = row_max(top);
                 const float ref = top == kNegInf ? 0.f : top;
                 const float alpha = expf(m[map][i] - ref);
                 m[map][i] = top;
                 float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < kJ; ++e) {
                     float pr = see[e] ? expf(s[i][e] - ref) : 0.f;
                     sum += pr;
-                    if (see[e] && bad[tx + 16 * e]) pr = nan_f();
-                    wm[(4 * ty + i) * kPitchW + tx + 16 * e] = pr;
+                    if (see[e] && bad[tx + 32 * e]) pr = nan_f();
+                    wm[(4 * ty + i) * kPitchW + tx + 32 * e] = pr;
                 }
                 l[map][i] = fmaf(l[map][i], alpha, sum);
                 o[map].scale(i, alpha);
             }
         }
         __syncwarp();
-        weighted<HD, false>(o[0], w, w, vs);
-        weighted<HD, false>(o[1], w + kRows * kPitchW, w, vs);
+        weighted2<HD>(o[0], o[1], w, w + kRows * kPitchW, vs);
     }
     const float lam = p.lambda[p.n_lambda == 1 ? 0 : S.head];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t r = S.r0 + 4 * ty + i;
-        const float l1 = half_sum(l[0][i]), l2 = half_sum(l[1][i]);
+        const float l1 = row_sum(l[0][i]), l2 = row_sum(l[1][i]);
         if (r >= S.rend) continue;
         o[1].scale(i, 1.f / l2);
         o[0].scale(i, 1.f / l1);
 #pragma unroll
-        for (int c = 0; c < Acc<HD>::kC; ++c) fma4(o[0].v[i][c], -lam, o[1].v[i][c]);
+        for (int c = 0; c < Acc<HD>::kW; ++c) o[0].v[i][c] = fmaf(-lam, o[1].v[i][c], o[0].v[i][c]);
         const int64_t off = own + (4 * ty + i) * stride;
         store<HD>(p.o[side] + off, o[0], i, 1.f, 1.f);
         if (p.s[side] != nullptr) store<HD>(p.s[side] + off, o[1], i, 1.f, 1.f);
@@ -374,28 +390,25 @@ __global__ void __launch_bounds__(kThreads) diff_dq_simt_kernel(const Ptr p, con
     float *qs = sm, *gs = qs + kRows * (HD + 4), *ks = gs + kRows * (HD + 4),
           *vs = ks + kTile * (HD + 4), *w = vs + kTile * (HD + 4);
     __shared__ uint8_t bad[kTile];
+    __shared__ Sees sees[kRows];
+    __shared__ float lse[2][kRows], del[2][kRows];
     const Span S = query_span(g);
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, side = S.detail ? 0 : 1;
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, side = S.detail ? 0 : 1;
     const int64_t stride = static_cast<int64_t>(g.heads) * HD, rows = g.N + g.G;
     const int64_t own = (S.b * (S.detail ? g.N : g.G) + S.r0) * stride + S.head * HD;
     const int n = static_cast<int>(S.rend - S.r0);
     load_rows<HD, kRows, false>(qs, p.q[side] + own, stride, n, nullptr);
     load_rows<HD, kRows, false>(gs, p.go[side] + own, stride, n, nullptr);
-    Sees sees[4];
-    float lse[2][4], del[2][4];
     Acc<HD> dq;
     dq.zero();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = S.r0 + 4 * ty + i;
-        sees[i] = query_sees(g, S, r);
-        const int64_t col = (S.b * g.heads + S.head) * 2 * rows +
+    if (threadIdx.x < 2 * kRows) {
+        const int map = threadIdx.x / kRows, i = threadIdx.x % kRows;
+        const int64_t r = S.r0 + i;
+        if (map == 0) sees[i] = query_sees(g, S, r);
+        const int64_t col = ((S.b * g.heads + S.head) * 2 + map) * rows +
                             (S.detail ? 0 : g.N) + (r < S.rend ? r : S.r0);
-#pragma unroll
-        for (int map = 0; map < 2; ++map) {
-            lse[map][i] = p.lse[col + map * rows];
-            del[map][i] = p.delta[col + map * rows];
-        }
+        lse[map][i] = p.lse[col];
+        del[map][i] = p.delta[col];
     }
     for (int j = 0; j < S.na + S.nb; ++j) {
         const bool det = j < S.na;
@@ -405,23 +418,27 @@ __global__ void __launch_bounds__(kThreads) diff_dq_simt_kernel(const Ptr p, con
         load_rows<HD, kTile, true>(ks, p.k[det ? 0 : 1] + at, stride, S.rows(j), bad);
         load_rows<HD, kTile, false>(vs, p.v[det ? 0 : 1] + at, stride, S.rows(j), nullptr);
         __syncthreads();
-        float dp[4][2], s[4][2];
+        float dp[4][kJ], s[4][kJ];
         scores<HD>(gs, vs, 0, HD, dp);
 #pragma unroll
         for (int map = 0; map < 2; ++map) {
             scores<HD>(qs, ks, map * (HD / 2), (map + 1) * (HD / 2), s);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * ty + i;
+                const Sees mine = sees[r];
+                const float ls = lse[map][r], de = del[map][r];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float ds = expf(fmaf(s[i][e], p.scale, -lse[map][i])) * (dp[i][e] - del[map][i]);
-                    if (bad[tx + 16 * e]) ds = nan_f();
-                    if (!sees[i].at(det, x0 + tx + 16 * e)) ds = 0.f;
-                    w[(map * kRows + 4 * ty + i) * kPitchW + tx + 16 * e] = ds;
+                for (int e = 0; e < kJ; ++e) {
+                    float ds = expf(fmaf(s[i][e], p.scale, -ls)) * (dp[i][e] - de);
+                    if (bad[tx + 32 * e]) ds = nan_f();
+                    if (!mine.at(det, x0 + tx + 32 * e)) ds = 0.f;
+                    w[(map * kRows + r) * kPitchW + tx + 32 * e] = ds;
                 }
+            }
         }
         __syncwarp();
-        weighted<HD, true>(dq, w, w + kRows * kPitchW, ks);
+        weighted<HD>(dq, w + (tx >= 16 ? kRows * kPitchW : 0), ks);
     }
     const float lam = p.lambda[p.n_lambda == 1 ? 0 : S.head];
 #pragma unroll
@@ -438,16 +455,15 @@ __global__ void __launch_bounds__(kThreads) diff_dkdv_simt_kernel(const Ptr p, c
     __shared__ float lse[2][kTile], del[2][kTile];
     __shared__ uint8_t bad[2][kTile];
     const Span S = key_span(g);
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, side = S.detail ? 0 : 1;
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, side = S.detail ? 0 : 1;
     const int64_t stride = static_cast<int64_t>(g.heads) * HD, rows = g.N + g.G;
     const int64_t own = (S.b * (S.detail ? g.N : g.G) + S.r0) * stride + S.head * HD;
     const int n = static_cast<int>(S.rend - S.r0);
     load_rows<HD, kRows, false>(ks, p.k[side] + own, stride, n, nullptr);
     load_rows<HD, kRows, false>(vs, p.v[side] + own, stride, n, nullptr);
     const float lam = p.lambda[p.n_lambda == 1 ? 0 : S.head];
-    Sees sees[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sees[i] = key_sees(g, S, S.r0 + 4 * ty + i);
+    __shared__ Sees sees[kRows];
+    if (threadIdx.x < kRows) sees[threadIdx.x] = key_sees(g, S, S.r0 + threadIdx.x);
     Acc<HD> dk, dv;
     dk.zero();
     dv.zero();
@@ -459,37 +475,39 @@ __global__ void __launch_bounds__(kThreads) diff_dkdv_simt_kernel(const Ptr p, c
         __syncthreads();
         load_rows<HD, kTile, true>(qs, p.q[det ? 0 : 1] + at, stride, nt, bad[0]);
         load_rows<HD, kTile, true>(gs, p.go[det ? 0 : 1] + at, stride, nt, bad[1]);
-        if (threadIdx.x < 2 * kTile) {
-            const int map = threadIdx.x / kTile, c = threadIdx.x % kTile;
+        for (int t = threadIdx.x; t < 2 * kTile; t += kThreads) {
+            const int map = t / kTile, c = t % kTile;
             const int64_t col = ((S.b * g.heads + S.head) * 2 + map) * rows + (det ? 0 : g.N) + x0 + c;
             lse[map][c] = c < nt ? p.lse[col] : 0.f;
             del[map][c] = c < nt ? p.delta[col] : 0.f;
         }
         __syncthreads();
-        float dp[4][2], s[4][2], wt[4][2];
+        float dp[4][kJ], s[4][kJ], wt[4][kJ];
         scores<HD>(vs, gs, 0, HD, dp);
 #pragma unroll
         for (int map = 0; map < 2; ++map) {
             scores<HD>(ks, qs, map * (HD / 2), (map + 1) * (HD / 2), s);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                const Sees mine = sees[4 * ty + i];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int c = tx + 16 * e;
+                for (int e = 0; e < kJ; ++e) {
+                    const int c = tx + 32 * e;
                     float pr = expf(fmaf(s[i][e], p.scale, -lse[map][c]));
                     // a query with a non-finite value (its D is NaN; a row of zeros
                     // here) gives NaN to the keys it sees
                     if (bad[0][c] || bad[1][c]) pr = nan_f();
-                    const bool see = sees[i].at(det, x0 + c);
+                    const bool see = mine.at(det, x0 + c);
                     const float ds = see ? pr * (dp[i][e] - del[map][c]) : 0.f;
                     wt[i][e] = map == 0 ? pr : (see ? fmaf(-lam, pr, wt[i][e]) : 0.f);
                     w[((1 + map) * kRows + 4 * ty + i) * kPitchW + c] = ds;
                     if (map == 1) w[(4 * ty + i) * kPitchW + c] = wt[i][e];
                 }
+            }
         }
         __syncwarp();
-        weighted<HD, false>(dv, w, w, gs);
-        weighted<HD, true>(dk, w + kRows * kPitchW, w + 2 * kRows * kPitchW, qs);
+        weighted<HD>(dv, w, gs);
+        weighted<HD>(dk, w + (tx >= 16 ? 2 : 1) * kRows * kPitchW, qs);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
