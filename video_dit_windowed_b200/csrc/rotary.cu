@@ -38,7 +38,7 @@ using geom::Geom;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = kRotaryMaxHeadDim / 2;
-constexpr int kTileAngles = 512;      // (row, pair) angles of a tile, at least one row's
+constexpr int kTileAngles = 2048;     // (row, pair) angles of a tile
 constexpr int kMaxTileRows = 32;
 constexpr int kStageBytes = 2048;     // half layout: one warp's staging buffer
 
@@ -54,6 +54,7 @@ struct Params {
     Tensor t[kRotaryMaxTensors];
     uint32_t rows, total_rows;        // tokens of one problem, of all problems
     uint32_t tile_rows, n_tiles;
+    int32_t n_tensors;
     uint32_t head_bytes, vph;         // bytes and 16-byte vectors of one head
     uint32_t n_pairs;                 // rotated pairs of a head
     uint32_t pair_end[2];             // pairs of axis t; of axes t and h
@@ -173,82 +174,84 @@ __device__ __forceinline__ void st_ch(uint8_t *s, uint32_t c, float v) {
 
 template <int EB, bool HALF>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Params p) {
-    __shared__ Row rows[2][kMaxTileRows];
-    __shared__ float2 cs[2][kTileAngles];
+    __shared__ Row rows[kMaxTileRows];
+    __shared__ float2 cs[kTileAngles];
     __shared__ double turn[kMaxPairs];
     __shared__ alignas(16) uint8_t stage[HALF ? kWarps : 1][HALF ? kStageBytes : 16];
-    const Tensor &t = p.t[blockIdx.y];
     const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     for (uint32_t k = tid; k < p.n_pairs; k += kThreads) turn[k] = p.turn[k];
-    uint32_t buf = 0;
-    for (uint32_t tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x, buf ^= 1) {
+    for (uint32_t tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x) {
         const uint32_t first = tile * p.tile_rows;
         const uint32_t n = min(p.tile_rows, p.total_rows - first);
-        if (tid < n) rows[buf][tid] = row_of(p, first + tid);
+        __syncthreads();   // the previous tile's rows have been moved
+        if (tid < n) rows[tid] = row_of(p, first + tid);
         __syncthreads();
-        if (t.rotate) {
-            for (uint32_t i = tid; i < n * p.n_pairs; i += kThreads) {
-                const uint32_t r = p.by_pairs.div(i);
-                cs[buf][i] = angle_of(p, turn, rows[buf][r], i - r * p.n_pairs);
-            }
+        for (uint32_t i = tid; i < n * p.n_pairs; i += kThreads) {
+            const uint32_t r = p.by_pairs.div(i);
+            cs[i] = angle_of(p, turn, rows[r], i - r * p.n_pairs);
         }
         __syncthreads();
-        if (!HALF || !t.rotate) {
-            // (row, head, vector) of the tile, vectors fastest; kFlight loads
-            // of a thread in flight.
-            constexpr int kFlight = 4;
-            const uint32_t per_row = t.heads * p.vph, total = n * per_row;
-            for (uint32_t i0 = tid; i0 < total; i0 += kFlight * kThreads) {
-                uint4 v[kFlight];
-                uint32_t rr[kFlight], off[kFlight], k0[kFlight];
+        for (int32_t x = 0; x < p.n_tensors; ++x) {
+            const Tensor &t = p.t[x];
+            if (!HALF || !t.rotate) {
+                // (row, head, vector) of the tile, vectors fastest; kFlight
+                // loads of a thread in flight.
+                constexpr int kFlight = 4;
+                const uint32_t per_row = t.heads * p.vph, total = n * per_row;
+                for (uint32_t i0 = tid; i0 < total; i0 += kFlight * kThreads) {
+                    uint4 v[kFlight];
+                    uint32_t rr[kFlight], off[kFlight], k0[kFlight];
 #pragma unroll
-                for (int f = 0; f < kFlight; ++f) {
-                    const uint32_t i = i0 + f * kThreads;
-                    if (i >= total) continue;
-                    const uint32_t hv = p.by_vph.div(i);        // (row, head)
-                    rr[f] = t.by_heads.div(hv);
-                    off[f] = (i - rr[f] * per_row) * 16u;
-                    k0[f] = (i - hv * p.vph) * (8 / EB);
-                    v[f] = ld_row(t.src + rows[buf][rr[f]].src * t.src_stride + off[f]);
-                }
+                    for (int f = 0; f < kFlight; ++f) {
+                        const uint32_t i = i0 + f * kThreads;
+                        if (i >= total) continue;
+                        const uint32_t hv = p.by_vph.div(i);        // (row, head)
+                        rr[f] = t.by_heads.div(hv);
+                        off[f] = (i - rr[f] * per_row) * 16u;
+                        k0[f] = (i - hv * p.vph) * (8 / EB);
+                        v[f] = ld_row(t.src + rows[rr[f]].src * t.src_stride + off[f]);
+                    }
 #pragma unroll
-                for (int f = 0; f < kFlight; ++f) {
-                    if (i0 + f * kThreads >= total) continue;
-                    if (t.rotate)
-                        v[f] = rotate_vec<EB>(v[f], cs[buf] + rr[f] * p.n_pairs, k0[f], p.n_pairs);
-                    st_row(t.dst + rows[buf][rr[f]].dst * t.dst_stride + off[f], v[f]);
-                }
-            }
-        } else {
-            // Jobs of one warp: up to `chunk` heads of one row.
-            uint8_t *s = stage[warp];
-            const uint32_t chunk = kStageBytes / p.head_bytes;
-            const uint32_t per_row = (t.heads + chunk - 1) / chunk;
-            for (uint32_t job = warp; job < n * per_row; job += kWarps) {
-                const uint32_t r = job / per_row, h0 = (job - r * per_row) * chunk;
-                const uint32_t nh = min(chunk, static_cast<uint32_t>(t.heads) - h0);
-                const uint32_t nv = nh * p.vph;
-                const uint8_t *src = t.src + rows[buf][r].src * t.src_stride + h0 * p.head_bytes;
-                uint8_t *dst = t.dst + rows[buf][r].dst * t.dst_stride + h0 * p.head_bytes;
-                for (uint32_t i = lane; i < nv; i += 32)
-                    *reinterpret_cast<uint4 *>(s + i * 16) = ld_row(src + i * 16);
-                __syncwarp();
-                for (uint32_t k = lane; k < p.n_pairs; k += 32) {
-                    const float2 c = cs[buf][r * p.n_pairs + k];
-                    const int a = k < p.pair_end[0] ? 0 : (k < p.pair_end[1] ? 1 : 2);
-                    const uint32_t c1 = p.seg_first[a] + k - (a == 0 ? 0 : p.pair_end[a - 1]);
-                    const uint32_t c2 = c1 + p.seg_half[a];
-                    for (uint32_t h = 0; h < nh; ++h) {
-                        uint8_t *head = s + h * p.head_bytes;
-                        const float2 y = turned(ld_ch<EB>(head, c1), ld_ch<EB>(head, c2), c);
-                        st_ch<EB>(head, c1, y.x);
-                        st_ch<EB>(head, c2, y.y);
+                    for (int f = 0; f < kFlight; ++f) {
+                        if (i0 + f * kThreads >= total) continue;
+                        if (t.rotate)
+                            v[f] = rotate_vec<EB>(v[f], cs + rr[f] * p.n_pairs, k0[f], p.n_pairs);
+                        st_row(t.dst + rows[rr[f]].dst * t.dst_stride + off[f], v[f]);
                     }
                 }
-                __syncwarp();
-                for (uint32_t i = lane; i < nv; i += 32)
-                    st_row(dst + i * 16, *reinterpret_cast<const uint4 *>(s + i * 16));
-                __syncwarp();
+            } else {
+                // Jobs of one warp: up to `chunk` heads of one row.
+                uint8_t *s = stage[warp];
+                const uint32_t chunk = kStageBytes / p.head_bytes;
+                const uint32_t per_row = (t.heads + chunk - 1) / chunk;
+                for (uint32_t job = warp; job < n * per_row; job += kWarps) {
+                    const uint32_t r = job / per_row, h0 = (job - r * per_row) * chunk;
+                    const uint32_t nh = min(chunk, static_cast<uint32_t>(t.heads) - h0);
+                    const uint32_t nv = nh * p.vph;
+                    const uint8_t *src = t.src + rows[r].src * t.src_stride + h0 * p.head_bytes;
+                    uint8_t *dst = t.dst + rows[r].dst * t.dst_stride + h0 * p.head_bytes;
+#pragma unroll 4
+                    for (uint32_t i = lane; i < nv; i += 32)
+                        *reinterpret_cast<uint4 *>(s + i * 16) = ld_row(src + i * 16);
+                    __syncwarp();
+                    for (uint32_t k = lane; k < p.n_pairs; k += 32) {
+                        const float2 c = cs[r * p.n_pairs + k];
+                        const int a = k < p.pair_end[0] ? 0 : (k < p.pair_end[1] ? 1 : 2);
+                        const uint32_t c1 = p.seg_first[a] + k - (a == 0 ? 0 : p.pair_end[a - 1]);
+                        const uint32_t c2 = c1 + p.seg_half[a];
+#pragma unroll 4
+                        for (uint32_t h = 0; h < nh; ++h) {
+                            uint8_t *head = s + h * p.head_bytes;
+                            const float2 y = turned(ld_ch<EB>(head, c1), ld_ch<EB>(head, c2), c);
+                            st_ch<EB>(head, c1, y.x);
+                            st_ch<EB>(head, c2, y.y);
+                        }
+                    }
+                    __syncwarp();
+                    for (uint32_t i = lane; i < nv; i += 32)
+                        st_row(dst + i * 16, *reinterpret_cast<const uint4 *>(s + i * 16));
+                    __syncwarp();
+                }
             }
         }
     }
@@ -270,14 +273,12 @@ double omega_of(const atlas_rotary &r, int axis, int32_t d, int32_t k) {
 }
 
 template <int EB, bool HALF>
-atlas_status launch(const Params &p, int n_tensors, const DeviceInfo &dev, cudaStream_t stream) {
-    // Enough blocks to fill every SM eight times over, shared by the tensors.
-    const uint32_t fill = std::max(1u, static_cast<uint32_t>(dev.sm_count) * 8u / n_tensors);
-    const dim3 grid(std::min(p.n_tiles, fill), n_tensors);
+atlas_status launch(const Params &p, const DeviceInfo &dev, cudaStream_t stream) {
+    const uint32_t grid = std::min(p.n_tiles, static_cast<uint32_t>(dev.sm_count) * 8u);
     if (log_enabled())
-        log_launch(HALF ? "rotary_kernel<half>" : "rotary_kernel", static_cast<int>(grid.x * grid.y),
+        log_launch(HALF ? "rotary_kernel<half>" : "rotary_kernel", static_cast<int>(grid),
                    kThreads, 0, "elem_bytes %d rows %u tensors %d head_bytes %u pairs %u tile %u order %d",
-                   EB, p.total_rows, n_tensors, p.head_bytes, p.n_pairs, p.tile_rows, p.order);
+                   EB, p.total_rows, p.n_tensors, p.head_bytes, p.n_pairs, p.tile_rows, p.order);
     rotary_kernel<EB, HALF><<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
@@ -341,9 +342,11 @@ atlas_status launch_rotary(const RotaryArgs &a, cudaStream_t stream) {
         widest = std::max(widest, width * a.elem_bytes);
     }
     if (n_tensors == 0) return ATLAS_OK;
+    p.n_tensors = n_tensors;
+    if (!turns) p.n_pairs = 0;   // nothing rotates: no angles
     // Rows of a tile: as many as their angles fit the buffer, no more than
     // leave every SM two tiles, and vectors of a tile below 2^31.
-    uint32_t tile = n > 0 ? std::max(1u, kTileAngles / n) : kMaxTileRows;
+    uint32_t tile = n > 0 ? kTileAngles / n : kMaxTileRows;
     tile = std::min<uint32_t>(tile, kMaxTileRows);
     tile = std::min(tile, std::max(1u, p.total_rows / (2u * dev.sm_count)));
     tile = std::min<uint32_t>(tile, std::max<int64_t>(1, (1ll << 30) / (widest / 16)));
@@ -351,10 +354,10 @@ atlas_status launch_rotary(const RotaryArgs &a, cudaStream_t stream) {
     p.n_tiles = (p.total_rows + tile - 1) / tile;
     const bool half = r.layout == ATLAS_ROTARY_HALF && turns;
     if (a.elem_bytes == 2)
-        return half ? launch<2, true>(p, n_tensors, dev, stream)
-                    : launch<2, false>(p, n_tensors, dev, stream);
-    return half ? launch<4, true>(p, n_tensors, dev, stream)
-                : launch<4, false>(p, n_tensors, dev, stream);
+        return half ? launch<2, true>(p, dev, stream)
+                    : launch<2, false>(p, dev, stream);
+    return half ? launch<4, true>(p, dev, stream)
+                : launch<4, false>(p, dev, stream);
 }
 
 }  // namespace atlas
