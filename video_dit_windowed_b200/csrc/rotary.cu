@@ -220,20 +220,38 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
                     }
                 }
             } else {
-                // Jobs of one warp: up to `chunk` heads of one row.
+                // Jobs of one warp: up to `chunk` heads of one row, the next one's
+                // loads in flight while this one is rotated and stored.
+                constexpr int kVecs = kStageBytes / 16 / 32;
                 uint8_t *s = stage[warp];
                 const uint32_t chunk = kStageBytes / p.head_bytes;
                 const uint32_t per_row = (t.heads + chunk - 1) / chunk;
-                for (uint32_t job = warp; job < n * per_row; job += kWarps) {
-                    const uint32_t r = job / per_row, h0 = (job - r * per_row) * chunk;
-                    const uint32_t nh = min(chunk, static_cast<uint32_t>(t.heads) - h0);
-                    const uint32_t nv = nh * p.vph;
+                const uint32_t jobs = n * per_row;
+                uint4 v[kVecs];
+                auto where = [&](uint32_t job, uint32_t &r, uint32_t &h0, uint32_t &nh) {
+                    r = job / per_row;
+                    h0 = (job - r * per_row) * chunk;
+                    nh = min(chunk, static_cast<uint32_t>(t.heads) - h0);
+                };
+                auto fetch = [&](uint32_t job) {
+                    uint32_t r, h0, nh;
+                    where(job, r, h0, nh);
                     const uint8_t *src = t.src + rows[r].src * t.src_stride + h0 * p.head_bytes;
-                    uint8_t *dst = t.dst + rows[r].dst * t.dst_stride + h0 * p.head_bytes;
-#pragma unroll 4
-                    for (uint32_t i = lane; i < nv; i += 32)
-                        *reinterpret_cast<uint4 *>(s + i * 16) = ld_row(src + i * 16);
+#pragma unroll
+                    for (int f = 0; f < kVecs; ++f)
+                        if (f * 32 + lane < nh * p.vph) v[f] = ld_row(src + (f * 32 + lane) * 16);
+                };
+                if (warp < jobs) fetch(warp);
+                for (uint32_t job = warp; job < jobs; job += kWarps) {
+                    uint32_t r, h0, nh;
+                    where(job, r, h0, nh);
+                    const uint32_t nv = nh * p.vph;
+#pragma unroll
+                    for (int f = 0; f < kVecs; ++f)
+                        if (f * 32 + lane < nv)
+                            *reinterpret_cast<uint4 *>(s + (f * 32 + lane) * 16) = v[f];
                     __syncwarp();
+                    if (job + kWarps < jobs) fetch(job + kWarps);
                     for (uint32_t k = lane; k < p.n_pairs; k += 32) {
                         const float2 c = cs[r * p.n_pairs + k];
                         const int a = k < p.pair_end[0] ? 0 : (k < p.pair_end[1] ? 1 : 2);
@@ -248,8 +266,12 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
                         }
                     }
                     __syncwarp();
-                    for (uint32_t i = lane; i < nv; i += 32)
-                        st_row(dst + i * 16, *reinterpret_cast<const uint4 *>(s + i * 16));
+                    uint8_t *dst = t.dst + rows[r].dst * t.dst_stride + h0 * p.head_bytes;
+#pragma unroll
+                    for (int f = 0; f < kVecs; ++f)
+                        if (f * 32 + lane < nv)
+                            st_row(dst + (f * 32 + lane) * 16,
+                                   *reinterpret_cast<const uint4 *>(s + (f * 32 + lane) * 16));
                     __syncwarp();
                 }
             }
