@@ -712,8 +712,8 @@ const char *atlas_status_string(atlas_status status);
 atlas_status atlas_last_device_error(atlas_stream_t stream, uint32_t *code);
 
 /*
- * Failure-path test hook. The next bf16 atlas_local_global_attn launch (any
- * thread, any device) leaves the first K tile of its first work unit
+ * Failure-path test hook. The next bf16 atlas_local_global_attn or
+ * atlas_diff_attn launch (any thread, any device) leaves the first K tile of its first work unit
  * unloaded. The waits that depend on it expire after their bounded limit
  * (about 2 s): that CTA records ATLAS_ERR_TIMEOUT bits in the device error
  * word, drains its in-flight copies and MMAs, frees tensor memory and exits,

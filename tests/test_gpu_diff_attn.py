@@ -332,3 +332,18 @@ def test_gradients_against_differences():
         assert abs((ends[0] - ends[1]) / (2 * h) - want) <= 10 * h * h + 2.0 ** -20 * scale / h * 0.1, n
     ends = [loss(t, lam + sg * h) for sg in (1, -1)]     # linear in lambda
     assert abs((ends[0] - ends[1]) / (2 * h) - float(out["dlam"])) <= 2.0 ** -20 * scale / h * 0.1
+
+
+def test_an_expired_wait_is_reported():
+    """The forward kernel's first K tile left unloaded: its waits run out, the
+    error word says so, and the context stays usable."""
+    t = make(1, 256, 100, 1, 64, "bf16")
+    lam = torch.tensor([0.5], device=DEV)
+    o = {n: torch.empty_like(t["q_" + n]) for n in "dg"}
+    args = [t[n] for n in ("q_d", "k_d", "v_d", "q_g", "k_g", "v_g")]
+    atlas.debug_stall_next_attention()
+    atlas.diff_attn(*args, lam, o["d"], o["g"], window_len=128)
+    assert atlas.last_device_error() != 0
+    assert atlas.last_device_error() == 0
+    out = run(t, lam, 1, 256, 100, 1, window_len=128)
+    against_reference(t, out, lam, 1, 256, 100, 1, 64, "bf16", [0, 128, 256])

@@ -208,3 +208,21 @@ def test_streams_and_graph():
     atlas.rotary([(x, z)], grid, rot, cube=(2, 4, 4), order="reorder", stream=s)
     torch.cuda.synchronize()
     assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_small_part_of_a_wide_head(layout, dtype):
+    """A quarter of a 512-channel head rotates, in many tiles: the vectors behind
+    the rotated part touch no coefficient."""
+    rows, hd, split = 12000, 512, (128, 0, 0)
+    rot = atlas.make_rotary(10000.0, split, layout=layout)
+    x = inputs(rows, 1, hd, dtype)
+    y = torch.empty_like(x)
+    atlas.rotary([(x, y)], (1, 1, rows), rot, positions=torch.arange(rows, dtype=torch.int32, device=DEV))
+    pick = torch.tensor([0, 1, 31, 32, 5000, 11999])
+    pos = np.zeros((len(pick), 3))
+    pos[:, 0] = pick.numpy()
+    want, bound = expect(x[pick], pos, dtype, None, "raster", 10000.0, split, (1, 1, 1), layout)
+    diff_ref.check("y", f64(y[pick]), want, bound)
+    assert torch.equal(y[..., 128:], x[..., 128:])

@@ -141,7 +141,8 @@ atlas_status launch_attn_tc_bf16(const AttnArgs &a, cudaStream_t stream);
 bool make_rows_map(CUtensorMap *m, const void *base, int64_t rows, int heads, int hd,
                    int box_rows = 128);
 // One-shot request (atlas_debug_stall_next_attention): true once, for the
-// next bf16 attention launch, which then leaves one K tile unloaded.
+// next bf16 attention launch (differential or not), which then leaves one K tile
+// unloaded.
 bool take_stall_request();
 atlas_status launch_attn_simt_f32(const AttnArgs &a, cudaStream_t stream);
 

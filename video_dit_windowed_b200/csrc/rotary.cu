@@ -139,7 +139,8 @@ __device__ __forceinline__ float2 turned(float a, float b, float2 cs) {
 }
 
 // The pairs of a 16-byte vector, from pair k0 on; pairs past the rotated part
-// keep their bits. cs + k0 is 16-byte aligned.
+// keep their bits. cs + k0 is 16-byte aligned, and the pitch even: the second entry
+// of the last float4 is the row's own.
 template <int EB>
 __device__ __forceinline__ uint4 rotate_vec(uint4 v, const float2 *cs, uint32_t k0,
                                             uint32_t n_pairs) {
@@ -147,6 +148,7 @@ __device__ __forceinline__ uint4 rotate_vec(uint4 v, const float2 *cs, uint32_t 
     uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < kPairs; j += 2) {
+        if (k0 + j >= n_pairs) break;
         const float4 q = *reinterpret_cast<const float4 *>(cs + k0 + j);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -186,7 +188,7 @@ __device__ __forceinline__ void st_ch(uint8_t *s, uint32_t c, float v) {
 template <int EB, bool HALF>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Params p) {
     __shared__ Row rows[kMaxTileRows];
-    __shared__ alignas(16) float2 cs[kTileAngles + 4];   // (vectors read past a row's last pair)
+    __shared__ alignas(16) float2 cs[kTileAngles];   // [row][pitch]
     __shared__ double turn[kMaxPairs];
     __shared__ alignas(16) uint8_t stage[HALF ? kWarps : 1][HALF ? kStageBytes : 16];
     const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
