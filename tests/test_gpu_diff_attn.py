@@ -308,6 +308,67 @@ def test_lambda(n, d, dtype):
                        (diff_ref.unit(DT[dtype]) + 2.0 ** -22 * (d + 8)) * want.abs())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("N,G,L", [(512, 100, 256), (300, 60, 30), (640, 0, 640), (0, 332, 1)])
+def test_dlambda_has_no_rounding_of_the_stored_output(N, G, L, hd, dtype):
+    """Zero keys weigh all alike, and a quarter of the values are one bf16 step above
+    1: every s is 1 + 2^-9, which bf16 stores as 1. With do = 1, dlambda = -(rows) D
+    (1 + 2^-9). Relative errors: of a weight 2^-22 (n + 16) (diff_ref.py), of sums of
+    terms of one sign over the n keys or over channels and rows below 2^-24 (n + 64)
+    each; the stored s would be off by 2^-9."""
+    B, H = 2, 2
+    lam = torch.tensor([0.4, 0.7], device=DEV)
+    t = make(B, N, G, H, hd, dtype)
+    for p in "dg":
+        t["k_" + p].zero_()
+        t["do_" + p].fill_(1.0)
+        t["v_" + p].fill_(1.0)
+        t["v_" + p][::4] = 1.0 + 2.0 ** -7
+    # windows, global rows and problems hold a multiple of four rows, or a share
+    # of the raised values that the reference counts
+    out = run(t, lam, B, N, G, H, window_len=L)
+    mask = diff_ref.mask_of(N, G, list(range(0, N + 1, L)) if N else [0]).to(DEV).double()
+    want = 0.0
+    for b in range(B):
+        v = torch.cat([t["v_d"][b * N:(b + 1) * N, 0, 0], t["v_g"][b * G:(b + 1) * G, 0, 0]]).double()
+        want -= float((mask @ v / mask.sum(1)).sum()) * hd
+    n = int(mask.sum(1).max())
+    err = (out["dlam"].double() - want).abs() / abs(want)
+    assert float(err.max()) <= 2.0 ** -22 * (n + 16) + 2 * 2.0 ** -24 * (n + 64), err
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("case", ["one global row", "windows of one row", "one row in a long list"])
+def test_the_one_key_of_a_row_has_no_gradient(case, hd, dtype):
+    """A softmax over one key is 1 whatever the key: dq of the row and dk from it
+    are 0, not a rounding; dv is the row's (1 - lambda) do."""
+    B, H = 2, 2
+    lam = torch.tensor([0.3, 0.6], device=DEV)
+    if case == "one global row":
+        N, G, lone, off = 130, 1, [130], None
+    elif case == "windows of one row":
+        N, G, lone, off = 150, 0, list(range(150)), None
+    else:                          # window form: windows of 200, 1 and 150 rows
+        N, G, lone, off = 351, 0, [200], [0, 200, 201, 351]
+    t = make(B, N, G, H, hd, dtype, seed=5)
+    layout = {"window_offsets": torch.tensor(off, dtype=torch.int32, device=DEV)} if off else \
+        {"window_len": 130 if G else 1}
+    out = run(t, lam, B, N, G, H, **layout)
+    cat = lambda src, name: torch.cat([src[name + "_" + p].view(B, -1, H, hd) for p in "dg"], 1)  # noqa: E731
+    dq = cat(out, "dq")[:, lone]
+    assert not dq.any(), float(dq.abs().max())
+    if not G:                      # (the key of a global row is seen by detail rows too)
+        assert not cat(out, "dk")[:, lone].any()
+        want = cat(t, "do")[:, lone].double() * (1 - lam.double())[:, None]
+        err = (cat(out, "dv")[:, lone].double() - want).abs()
+        # W = 1 - lambda: each weight's logit and sum 2^-22 (hd/2 |s| + 17), W rounded (bf16), dv rounded
+        u = diff_ref.unit(DT[dtype])
+        assert bool((err <= want.abs() * (2 * u if dtype == "bf16" else u) + 2.0 ** -22 * (8 * hd + 17) *
+                     cat(t, "do")[:, lone].double().abs()).all())
+
+
 def test_gradients_against_differences():
     """Central differences of the fp32 forward along random directions, every
     input and lambda: truncation h^2 / 6 of the third derivative (bounded by 60

@@ -117,7 +117,7 @@ def reference(t, n, m, hd, split, layout):
         v.append(x[p][:, 2 * H:])
     q, k, v = torch.cat(q), torch.cat(k), torch.cat(v)
     pos = positions(GRID)
-    cube = (pos // torch.tensor(CUBE, device=DEV)) @ torch.tensor([10000, 100, 1], device=DEV)
+    cube = ((pos // torch.tensor(CUBE, device=DEV)) * torch.tensor([10000, 100, 1], device=DEV)).sum(1)
     mask = torch.zeros(n + m, n + m, dtype=torch.bool, device=DEV)
     mask[:n, :n] = cube[:, None] == cube[None, :]
     mask[:, n:] = True

@@ -276,6 +276,13 @@ __device__ __forceinline__ void key_ranges(const Shape &p, const Unit &U, int32_
     }
 }
 
+// Whether the queries of detail key r's window see no global key.
+__device__ __forceinline__ bool no_global_key(const Shape &p, const Unit &U, int32_t r) {
+    int32_t ga, gb;
+    global_keys(p, U.win >= 0 ? U.win : window_of(p, min(r, p.N - 1)), ga, gb);
+    return ga == gb;
+}
+
 // The fields that the tile functions above read, as uniform values of a
 // converged warp.
 __device__ __forceinline__ void make_uniform(Unit &U) {

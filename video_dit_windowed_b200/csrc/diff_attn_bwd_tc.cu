@@ -26,6 +26,11 @@
 // issued as soon as the compute threads have loaded this tile's, and run while
 // those compute; the products that read P and dS follow when they are stored.
 //
+// D comes from outputs that were rounded to 16 bits, which dlambda = -sum D_2, a
+// sum of terms of both signs, would show (0.7% of it at head width 128). The sum of
+// a row's dS is what D lacks, so DQ, which runs first, adds it: D is then as exact
+// as P and dP. A query with one key has dS = 0 whatever D's rounding: set so.
+//
 // Warps (352 threads): 0-7 compute (thread = resident row = lane; warpgroup g
 // takes half of a tile's columns), 8 TMA producer, 9 / 10 MMA issuers (S and dP;
 // the accumulating products).
@@ -94,11 +99,12 @@ struct Smem {
     alignas(1024) uint8_t ys[kStages][kTileBytes];   // streamed V (DQ) or dO
     alignas(16) float lse[kStages][2][FORM == kDQ ? 4 : kStream];     // DKDV: of the streamed queries
     alignas(16) float delta[kStages][2][FORM == kDQ ? 4 : kStream];
+    float row_sum[2][2][FORM == kDQ ? kRows : 1];   // DQ: [unit & 1][map], of warpgroup 1
     uint64_t x_full, x_empty;
     uint64_t st_full[kStages], st_empty[kStages];
     uint64_t s_full;     // S_1, S_2, dP of a tile in TMEM           (commit)
-    uint64_t s_read;     // ... loaded by the compute threads        (256 arrivals)
-    uint64_t p_full;     // packed P / dS in TMEM                    (256 arrivals)
+    uint64_t s_read;     // ... loaded by the compute threads        (8 warps)
+    uint64_t p_full;     // packed P / dS in TMEM                    (8 warps)
     uint64_t acc_done;   // the products that read them are done     (commit)
     uint64_t acc_full, acc_empty;
     uint64_t drain[2];
@@ -113,7 +119,8 @@ struct Params {
     CUtensorMap st_x[2], st_y[2];     // streamed, with tile-row boxes
     __nv_bfloat16 *dv[2], *grad[2];   // DKDV: dV; dQ or dK
     const __nv_bfloat16 *row_x[2], *row_y[2];   // DQ: Q and dO rows
-    const float *lse, *delta, *lambda;
+    const float *lse, *lambda;
+    float *delta;   // DKDV reads it; DQ reads and corrects its own rows'
     int32_t n_lambda;
     uint32_t *err_word;
     float scale_log2, scale;
@@ -422,7 +429,7 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
         if constexpr (HD == 128) ptx::tmem_st64(dst, rv);
         else ptx::tmem_st32(dst, rv);
         ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_addr(&sm.x_full));
+        ptx::mbar_arrive_warp(ptx::smem_addr(&sm.x_full));
     };
     bool resident_ready = false;   // DQ: this unit's rows were written ahead
 
@@ -445,18 +452,24 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
         const float nlam = -__ldg(p.lambda + (p.n_lambda == 1 ? 0 : U.head));
         int32_t da = 0, db = 0, ga = 0, gb = 0;   // streamed rows this row meets
         float own_l[2] = {__builtin_huge_valf(), __builtin_huge_valf()}, own_d[2] = {0.f, 0.f};
+        float sum_d[2] = {0.f, 0.f};              // DQ: of this warpgroup's dS
+        bool lone_a = false, lone_b = false;      // DKDV: the query sees no other key
+        const int64_t col = (static_cast<int64_t>(U.b) * p.shape.heads + U.head) * 2 * per +
+                            (U.detail ? row : static_cast<int64_t>(N) + row);
         if (valid) {
             if (FORM == kDQ) {
                 units::query_ranges(p.shape, U, row, da, db, ga, gb);
-                const int64_t col = (static_cast<int64_t>(U.b) * p.shape.heads + U.head) * 2 * per +
-                                    (U.detail ? row : static_cast<int64_t>(N) + row);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     own_l[m] = __ldg(p.lse + col + m * per) * kLog2e;
-                    own_d[m] = __ldg(p.delta + col + m * per);
+                    own_d[m] = p.delta[col + m * per];
                 }
+                // The one key of a query has P = 1 and dS = 0 (or NaN).
+                if (db - da + gb - ga == 1 && !isnan(own_d[0])) da = db = ga = gb = 0;
             } else {
                 units::key_ranges(p.shape, U, row, da, db, ga, gb);
+                lone_a = U.detail && db - da == 1 && units::no_global_key(p.shape, U, row);
+                lone_b = !U.detail && G == 1;
             }
         }
         if (FORM == kDQ && !resident_ready) {
@@ -480,10 +493,16 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
             if constexpr (kCols == 32) ptx::tmem_ld3x32(src, src + 64, src + TM::kDP, s1, s2, dp);
             else ptx::tmem_ld3x24(src, src + 64, src + TM::kDP, s1, s2, dp);
             ptx::tc_fence_before();
-            ptx::mbar_arrive(ptx::smem_addr(&sm.s_read));
+            ptx::mbar_arrive_warp(ptx::smem_addr(&sm.s_read));
             const int32_t lo = j < U.n_a ? da : ga, hi = j < U.n_a ? db : gb;
-            const int32_t c0 = units::tile_row<kStream>(U, j) + part * kCols;   // of column 0
+            const int32_t t0 = units::tile_row<kStream>(U, j), c0 = t0 + part * kCols;   // column 0
             const bool partial = c0 < lo || c0 + kCols > hi;
+            // DKDV, a lone query at column lo: its dS is 0 unless it is marked (its
+            // range is one row, so the tile is partial).
+            int32_t hi_d = hi;
+            if (FORM == kDKDV && (j < U.n_a ? lone_a : lone_b) && lo >= t0 && lo < t0 + kStream &&
+                !isnan(sm.delta[stage][0][lo - t0]))
+                hi_d = lo;
             uint32_t pw[kPack], pd1[kPack], pd2[kPack];
 #pragma unroll
             for (int e = 0; e < kPack; ++e) {
@@ -509,7 +528,14 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
                     w[k] = FORM == kDQ ? 0.f : fmaf(dl[0], 0.f, fmaf(nlam, p2, p1));
                     d1[k] = p1 * (g - dl[0]);
                     d2[k] = p2 * (g - dl[1]);
-                    if (partial && (c0 + c < lo || c0 + c >= hi)) w[k] = d1[k] = d2[k] = 0.f;
+                    if (FORM == kDQ) {
+                        if (partial && (c0 + c < lo || c0 + c >= hi)) d1[k] = d2[k] = 0.f;
+                        sum_d[0] += d1[k];
+                        sum_d[1] += d2[k];
+                    } else {
+                        if (partial && (c0 + c < lo || c0 + c >= hi)) w[k] = 0.f;
+                        if (partial && (c0 + c < lo || c0 + c >= hi_d)) d1[k] = d2[k] = 0.f;
+                    }
                 }
                 pw[e] = ptx::pack_bf16x2(w[0], w[1]);
                 pd1[e] = ptx::pack_bf16x2(d1[0], d1[1]);
@@ -569,8 +595,14 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
                 }
             }
             if (wrote) ptx::fence_proxy_async_smem();
+            // Read by warpgroup 0 after acc_full; it has left the unit before last by
+            // the time that this unit's S is there.
+            if (FORM == kDQ && part == 1 && j == n - 1) {
+                sm.row_sum[unit_iter & 1][0][r] = sum_d[0];
+                sm.row_sum[unit_iter & 1][1][r] = sum_d[1];
+            }
             ptx::tc_fence_before();
-            ptx::mbar_arrive(ptx::smem_addr(&sm.p_full));
+            ptx::mbar_arrive_warp(ptx::smem_addr(&sm.p_full));
         }
         if (FORM == kDQ) {
             // The next unit's resident rows go in as soon as this unit's
@@ -593,6 +625,12 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
         if (!__all_sync(kAll, wait_phase(sm, sm.acc_full, unit_iter & 1, kErrTimeoutSoftmax)))
             return;
         ptx::tc_fence_after();
+        if (FORM == kDQ && part == 0 && valid) {
+            // dS sums to P (dP - D) = <do, P v> - D: what D lacks.
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                p.delta[col + m * per] = own_d[m] + (sum_d[m] + sm.row_sum[unit_iter & 1][m][r]);
+        }
         const int side = U.detail ? 0 : 1;
         const int64_t out_row = (static_cast<int64_t>(U.b) * (U.detail ? N : G) +
                                  (valid ? row : 0)) * p.shape.heads + U.head;
@@ -642,7 +680,7 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
             store_map(1);
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_addr(&sm.acc_empty));
+        ptx::mbar_arrive_warp(ptx::smem_addr(&sm.acc_empty));
         ++unit_iter;
     }
 }
@@ -655,18 +693,18 @@ __global__ void __launch_bounds__(kThreads, 1) diff_bwd_tc_kernel(const __grid_c
                                      ~static_cast<uintptr_t>(1023));
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        ptx::mbar_init(ptx::smem_addr(&sm.x_full), FORM == kDQ ? kCompute : 1);
+        ptx::mbar_init(ptx::smem_addr(&sm.x_full), FORM == kDQ ? kCompute / 32 : 1);
         ptx::mbar_init(ptx::smem_addr(&sm.x_empty), 1);
         for (int s = 0; s < SM::kStages; ++s) {
             ptx::mbar_init(ptx::smem_addr(&sm.st_full[s]), 1);
             ptx::mbar_init(ptx::smem_addr(&sm.st_empty[s]), 1);
         }
         ptx::mbar_init(ptx::smem_addr(&sm.s_full), 1);
-        ptx::mbar_init(ptx::smem_addr(&sm.s_read), kCompute);
-        ptx::mbar_init(ptx::smem_addr(&sm.p_full), kCompute);
+        ptx::mbar_init(ptx::smem_addr(&sm.s_read), kCompute / 32);
+        ptx::mbar_init(ptx::smem_addr(&sm.p_full), kCompute / 32);
         ptx::mbar_init(ptx::smem_addr(&sm.acc_done), 1);
         ptx::mbar_init(ptx::smem_addr(&sm.acc_full), 1);
-        ptx::mbar_init(ptx::smem_addr(&sm.acc_empty), kCompute);
+        ptx::mbar_init(ptx::smem_addr(&sm.acc_empty), kCompute / 32);
         ptx::mbar_init(ptx::smem_addr(&sm.drain[0]), 1);
         ptx::mbar_init(ptx::smem_addr(&sm.drain[1]), 1);
         sm.abort = 0;

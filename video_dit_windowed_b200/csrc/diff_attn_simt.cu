@@ -404,11 +404,16 @@ __global__ void __launch_bounds__(kThreads) diff_dq_simt_kernel(const Ptr p, con
     if (threadIdx.x < 2 * kRows) {
         const int map = threadIdx.x / kRows, i = threadIdx.x % kRows;
         const int64_t r = S.r0 + i;
-        if (map == 0) sees[i] = query_sees(g, S, r);
         const int64_t col = ((S.b * g.heads + S.head) * 2 + map) * rows +
                             (S.detail ? 0 : g.N) + (r < S.rend ? r : S.r0);
         lse[map][i] = p.lse[col];
         del[map][i] = p.delta[col];
+        if (map == 0) {
+            Sees v = query_sees(g, S, r);
+            // the one key of a query has P = 1 and dS = 0 (or NaN)
+            if (v.db - v.da + v.gb - v.ga == 1 && !isnan(del[0][i])) v = Sees{0, 0, 0, 0};
+            sees[i] = v;
+        }
     }
     for (int j = 0; j < S.na + S.nb; ++j) {
         const bool det = j < S.na;
@@ -463,7 +468,18 @@ __global__ void __launch_bounds__(kThreads) diff_dkdv_simt_kernel(const Ptr p, c
     load_rows<HD, kRows, false>(vs, p.v[side] + own, stride, n, nullptr);
     const float lam = p.lambda[p.n_lambda == 1 ? 0 : S.head];
     __shared__ Sees sees[kRows];
-    if (threadIdx.x < kRows) sees[threadIdx.x] = key_sees(g, S, S.r0 + threadIdx.x);
+    __shared__ uint8_t lone[kRows];   // the key's queries see no other: 1 detail, 2 global ones
+    if (threadIdx.x < kRows) {
+        const Sees v = key_sees(g, S, S.r0 + threadIdx.x);
+        sees[threadIdx.x] = v;
+        uint8_t alone = !S.detail && g.G == 1 ? 2 : 0;
+        if (S.detail && v.db - v.da == 1) {
+            int64_t lo, hi, g0 = 0, g1 = g.G;
+            geo::global_keys(g, geo::window_at(g, S.r0 + threadIdx.x, lo, hi), g0, g1);
+            if (g0 == g1) alone = 1;
+        }
+        lone[threadIdx.x] = alone;
+    }
     Acc<HD> dk, dv;
     dk.zero();
     dv.zero();
@@ -490,6 +506,7 @@ __global__ void __launch_bounds__(kThreads) diff_dkdv_simt_kernel(const Ptr p, c
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const Sees mine = sees[4 * ty + i];
+                const bool alone = lone[4 * ty + i] & (det ? 1 : 2);
 #pragma unroll
                 for (int e = 0; e < kJ; ++e) {
                     const int c = tx + 32 * e;
@@ -498,7 +515,8 @@ __global__ void __launch_bounds__(kThreads) diff_dkdv_simt_kernel(const Ptr p, c
                     // here) gives NaN to the keys it sees
                     if (bad[0][c] || bad[1][c]) pr = nan_f();
                     const bool see = mine.at(det, x0 + c);
-                    const float ds = see ? pr * (dp[i][e] - del[map][c]) : 0.f;
+                    float ds = see ? pr * (dp[i][e] - del[map][c]) : 0.f;
+                    if (alone && !isnan(del[map][c])) ds = 0.f;   // of a query with one key
                     wt[i][e] = map == 0 ? pr : (see ? fmaf(-lam, pr, wt[i][e]) : 0.f);
                     w[((1 + map) * kRows + 4 * ty + i) * kPitchW + c] = ds;
                     if (map == 1) w[(4 * ty + i) * kPitchW + c] = wt[i][e];

@@ -80,11 +80,11 @@ struct Smem {
     uint64_t kv_empty[kSlots];   // (and q_empty, o_final: a commit by each map's issuer)
     uint64_t s_lo[kMaps];        // first half of S_m(j) in TMEM            (commit)
     uint64_t s_hi[kMaps];        // second half, and O_m += P_m(j-1) V done (commit)
-    uint64_t s_read[kMaps];      // second half loaded                      (128 arrivals)
-    uint64_t p_full[kMaps];      // P_m(j) in TMEM, O_m rescaled            (128 arrivals)
+    uint64_t s_read[kMaps];      // second half loaded                      (4 warps)
+    uint64_t p_full[kMaps];      // P_m(j) in TMEM, O_m rescaled            (4 warps)
     uint64_t o_final;            // every MMA of the unit done              (commit)
-    uint64_t joined;             // both maps' inv_l written                (256 arrivals)
-    uint64_t o_empty;            // both accumulators read                  (256 arrivals)
+    uint64_t joined;             // both maps' inv_l written                (8 warps)
+    uint64_t o_empty;            // both accumulators read                  (8 warps)
     uint64_t drain[kMaps];
     uint32_t tmem_base;
     int32_t max_len;
@@ -485,7 +485,7 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 ptx::tc_fence_after();
                 ptx::tmem_ld64(t_hi, hi);
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(ptx::smem_addr(&sm.s_read[map]));
+                ptx::mbar_arrive_warp(ptx::smem_addr(&sm.s_read[map]));
                 if (PACK && j > 0) check_bad(j - 1, cnt - 1);
                 if (masked) {
 #pragma unroll
@@ -519,7 +519,7 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 }
                 ptx::tmem_ld64(t_hi, hi);
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(ptx::smem_addr(&sm.s_read[map]));
+                ptx::mbar_arrive_warp(ptx::smem_addr(&sm.s_read[map]));
                 if (PACK && j > 0) check_bad(j - 1, cnt - 1);
                 const ptx::F2 sum_lo = sum;
                 mx[0] = mx[1] = kNegInf;
@@ -590,13 +590,13 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
             ptx::unpack(sum, sum0, sum1);
             l_run += sum0 + sum1;
             ptx::tc_fence_before();
-            ptx::mbar_arrive(ptx::smem_addr(&sm.p_full[map]));
+            ptx::mbar_arrive_warp(ptx::smem_addr(&sm.p_full[map]));
         }
         // Epilogue: both maps' 1/l through shared memory; this group joins
         // columns [map * D/2, +D/2) of O_1 and O_2.
         const uint32_t par = unit_iter & 1;
         sm.inv_l[par][map][r] = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
-        ptx::mbar_arrive(ptx::smem_addr(&sm.joined));
+        ptx::mbar_arrive_warp(ptx::smem_addr(&sm.joined));
         if (p.lse != nullptr && valid) {
             const int64_t rows = static_cast<int64_t>(p.shape.N) + p.shape.G;
             p.lse[((static_cast<int64_t>(U.b) * p.shape.heads + U.head) * 2 + map) * rows +
@@ -621,7 +621,7 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
             ptx::tmem_ld32(t_o2, o2);
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_addr(&sm.o_empty));
+        ptx::mbar_arrive_warp(ptx::smem_addr(&sm.o_empty));
         ++unit_iter;
         if (!valid) continue;
         const int side = U.detail ? 0 : 1;
@@ -671,14 +671,14 @@ __global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_const
         for (int m = 0; m < kMaps; ++m) {
             ptx::mbar_init(ptx::smem_addr(&sm.s_lo[m]), 1);
             ptx::mbar_init(ptx::smem_addr(&sm.s_hi[m]), 1);
-            ptx::mbar_init(ptx::smem_addr(&sm.s_read[m]), kBM);
-            ptx::mbar_init(ptx::smem_addr(&sm.p_full[m]), kBM);
+            ptx::mbar_init(ptx::smem_addr(&sm.s_read[m]), kBM / 32);
+            ptx::mbar_init(ptx::smem_addr(&sm.p_full[m]), kBM / 32);
             ptx::mbar_init(ptx::smem_addr(&sm.drain[m]), 1);
         }
         ptx::mbar_init(ptx::smem_addr(&sm.o_final), kMaps);
         for (int i = 0; i < 4 * kBM; ++i) sm.mark[i / kBM][i % kBM] = 0;
-        ptx::mbar_init(ptx::smem_addr(&sm.joined), kMaps * kBM);
-        ptx::mbar_init(ptx::smem_addr(&sm.o_empty), kMaps * kBM);
+        ptx::mbar_init(ptx::smem_addr(&sm.joined), kMaps * kBM / 32);
+        ptx::mbar_init(ptx::smem_addr(&sm.o_empty), kMaps * kBM / 32);
         sm.abort = 0;
         sm.max_len = 0;
         sm.err_word = p.err_word;
