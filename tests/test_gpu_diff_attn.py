@@ -338,6 +338,49 @@ def test_dlambda_has_no_rounding_of_the_stored_output(N, G, L, hd, dtype):
     assert float(err.max()) <= 2.0 ** -22 * (n + 16) + 2 * 2.0 ** -24 * (n + 64), err
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("N,G,L", [(0, 1, 1), (0, 2, 1), (0, 3, 1), (60, 0, 2), (40, 0, 1), (90, 2, 3), (256, 1, 128)])
+def test_few_keys_keep_their_accuracy(N, G, L, hd):
+    """bf16 rows of one to five keys, as a whole: weights that are divided by their
+    own sum, and dP - D without the stored outputs' rounding. Each element then
+    carries independent roundings, of P (or W, or dS) and of the result, each at most
+    U of its term: 2 U sum|terms|, not U |o| / (P - D)-fold. Rounding errors of
+    independent sign add like their squares, a third of a bound on average, so the
+    norms stay below 2 U |terms|."""
+    B, H = 3, 2
+    lam = torch.tensor([0.62, 0.7], device=DEV)
+    t = make(B, N, G, H, hd, "bf16", seed=3 * N + G)
+    out = run(t, lam, B, N, G, H, window_len=L)
+    mask = diff_ref.mask_of(N, G, list(range(0, N + 1, L)) if N else [0]).to(DEV)
+    U, few = diff_ref.unit(torch.bfloat16), mask.sum(1) <= 8
+    sums = {}
+    for b in range(B):
+        for h in range(H):
+            part = lambda n: torch.cat([t[n + "_d"][b * N:(b + 1) * N, h],  # noqa: E731
+                                        t[n + "_g"][b * G:(b + 1) * G, h]]).double()
+            q, k, v, do = (part(n) for n in ("q", "k", "v", "do"))
+            r = diff_ref.Diff(q, k, v, float(lam[h]), mask, (hd // 2) ** -0.5, torch.bfloat16, do)
+            half = hd // 2
+            P = [torch.softmax((q[:, m * half:(m + 1) * half] @ k[:, m * half:(m + 1) * half].T * half ** -0.5)
+                               .masked_fill(~mask, -math.inf), 1) for m in range(2)]
+            dp = do @ v.T
+            ds = [c * p * (dp - (p * dp).sum(1, keepdim=True)) for c, p in zip((1.0, -float(lam[h])), P)]
+            # of weights that add up to one, a common relative error drops out: P (1 - P)
+            spread = sum(c * (p * (1 - p)) @ v.abs() for c, p in zip((1.0, float(lam[h])), P))
+            terms = {"o": spread + r.o.abs(),
+                     "dq": torch.cat([d.abs() @ k[:, m * half:(m + 1) * half].abs() * half ** -0.5
+                                      for m, d in enumerate(ds)], 1)}
+            for name, size in terms.items():
+                got = torch.cat([out[name + "_d"][b * N:(b + 1) * N, h], out[name + "_g"][b * G:(b + 1) * G, h]])
+                e = sums.setdefault(name, [0.0, 0.0])
+                e[0] += float((got.double() - getattr(r, name))[few].square().sum())
+                # (fp32 part: eps of the logits' terms on every weight and on dP)
+                e[1] += float((2 * U * size + r.eps * (P[0] + P[1]) @ v.abs() * (1 if name == "o" else 0))
+                              [few].square().sum())
+    for name, (e, bound) in sums.items():
+        assert e <= bound or e == 0.0, (name, e ** 0.5, bound ** 0.5)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("case", ["one global row", "windows of one row", "one row in a long list"])

@@ -353,13 +353,13 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
 
     // Columns [B, B + N) of 64 keys' S: P = exp2(S*scale*log2e - m) as bf16 pairs
     // into pk (rounding P halves the product's operand and is 2^-8 of each weight;
-    // the row sum adds the fp32 P). FAST: the maximum of the raw S joins mx, NaN
+    // the row sum adds the fp32 P). Not FAST: `rounded` sums them as rounded. FAST: the maximum of the raw S joins mx, NaN
     // kept, and one pair of eight takes its exponentials on the FMA pipe (720p, D =
     // 128 / 32,760 global tokens, D = 64: none 1628 / 906-975 us, one 1612 / 889, two
     // 1597 / 920, three 1640 / 970, four 1703 / 1015: beyond one the issue slots cost
     // what the MUFU saves).
     auto exps = [&](auto fast, auto from, auto count, const uint32_t (&sr)[64], float m,
-                    ptx::F2 &sum, float (&mx)[2], uint32_t (&pk)[16]) {
+                    ptx::F2 &sum, ptx::F2 &rounded, float (&mx)[2], uint32_t (&pk)[16]) {
         constexpr bool kFast = decltype(fast)::value;
         constexpr int B = decltype(from)::value, N = decltype(count)::value;
         const ptx::F2 scale2 = ptx::f2(sc, sc), negm2 = ptx::f2(-m, -m);
@@ -378,18 +378,23 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 p1 = ptx::ex2(p1);
             }
             sum = ptx::add2(sum, ptx::f2(p0, p1));
-            pk[(c % 32) / 2] = ptx::pack_bf16x2(p0, p1);
+            const uint32_t pp = ptx::pack_bf16x2(p0, p1);
+            pk[(c % 32) / 2] = pp;
+            if constexpr (!kFast)
+                rounded = ptx::add2(rounded, ptx::f2(__uint_as_float(pp << 16),
+                                                     __uint_as_float(pp & 0xffff0000u)));
         }
     };
     constexpr std::integral_constant<int, 0> c0{};
     constexpr std::integral_constant<int, 32> c32{};
     // All 64 with ex2, stored (masked tiles, and rows whose reference moves).
+    ptx::F2 rounded = ptx::f2(0.f, 0.f);
     auto exps_all = [&](const uint32_t (&sr)[64], float m, uint32_t dst, ptx::F2 &sum) {
         float unused[2];
         uint32_t pk[16];
-        exps(std::false_type{}, c0, c32, sr, m, sum, unused, pk);
+        exps(std::false_type{}, c0, c32, sr, m, sum, rounded, unused, pk);
         ptx::tmem_st16_nowait(dst, pk);
-        exps(std::false_type{}, c32, c32, sr, m, sum, unused, pk);
+        exps(std::false_type{}, c32, c32, sr, m, sum, rounded, unused, pk);
         ptx::tmem_st16_nowait(dst + 16, pk);
     };
     auto row_max = [&](const uint32_t (&sr)[64]) -> float {
@@ -446,7 +451,12 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
         const float lam = __ldg(p.lambda + (p.n_lambda == 1 ? 0 : U.head));
         // The reference m_run (log2 units) is whole, so that moving it scales by a
         // power of two, exactly.
-        float m_run = kNegInf, l_run = 0.f;
+        // l_fix: what the sum of the rounded weights of masked tiles differs by. O is
+        // divided by the sum of the weights as its products had them, so that a row
+        // with one key gets its V exactly and a row with few keys no common error,
+        // which o_1 - lambda o_2 would enlarge; over full tiles it averages out (and
+        // would cost two instructions a weight).
+        float m_run = kNegInf, l_run = 0.f, l_fix = 0.f;
         bool bad = false;
         // The bad rows of tile j (tile count c), which this map's threads wrote
         // before its product was issued; s_hi of the next tile and o_final follow.
@@ -468,6 +478,7 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 m_run = m_new;
             }
             l_run *= alpha;
+            l_fix *= alpha;
             if (!o_empty) rescale_o(need, alpha);
             return alpha;
         };
@@ -497,16 +508,21 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 }
                 move(fmaxf(row_max(lo), row_max(hi)) * sc, j == 0);
                 const float m = m_run == kNegInf ? 0.f : m_run;
+                rounded = ptx::f2(0.f, 0.f);
                 exps_all(lo, m, t_lo, sum);
                 exps_all(hi, m, t_lo + 32, sum);
+                float s0, s1, r0, r1;
+                ptx::unpack(sum, s0, s1);
+                ptx::unpack(rounded, r0, r1);
+                l_fix += (r0 - s0) + (r1 - s1);
             } else {
                 // Exponentials against the running reference right away; a half
                 // whose maximum turns out past the threshold (or NaN) is redone.
                 float mx[2] = {kNegInf, kNegInf};
                 uint32_t pk[16];
-                exps(std::true_type{}, c0, c32, lo, m_run, sum, mx, pk);
+                exps(std::true_type{}, c0, c32, lo, m_run, sum, rounded, mx, pk);
                 ptx::tmem_st16_nowait(t_lo, pk);
-                exps(std::true_type{}, c32, c32, lo, m_run, sum, mx, pk);
+                exps(std::true_type{}, c32, c32, lo, m_run, sum, rounded, mx, pk);
                 ptx::tmem_st16_nowait(t_lo + 16, pk);
                 if (!__all_sync(kAll, wait_phase(sm, sm.s_hi[map], cnt & 1, err))) return;
                 ptx::tc_fence_after();
@@ -524,9 +540,9 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 const ptx::F2 sum_lo = sum;
                 mx[0] = mx[1] = kNegInf;
                 sum = ptx::f2(0.f, 0.f);
-                exps(std::true_type{}, c0, c32, hi, m_run, sum, mx, pk);
+                exps(std::true_type{}, c0, c32, hi, m_run, sum, rounded, mx, pk);
                 ptx::tmem_st16_nowait(t_lo + 32, pk);
-                exps(std::true_type{}, c32, c32, hi, m_run, sum, mx, pk);
+                exps(std::true_type{}, c32, c32, hi, m_run, sum, rounded, mx, pk);
                 ptx::tmem_st16_nowait(t_lo + 48, pk);
                 mx2 = ptx::max_nan(mx[0], mx[1]) * sc;
                 float f = 1.f;
@@ -595,7 +611,8 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
         // Epilogue: both maps' 1/l through shared memory; this group joins
         // columns [map * D/2, +D/2) of O_1 and O_2.
         const uint32_t par = unit_iter & 1;
-        sm.inv_l[par][map][r] = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
+        const float l_o = l_run + l_fix;
+        sm.inv_l[par][map][r] = l_o > 0.f ? 1.f / l_o : (l_o == 0.f ? 0.f : l_o);
         ptx::mbar_arrive_warp(ptx::smem_addr(&sm.joined));
         if (p.lse != nullptr && valid) {
             const int64_t rows = static_cast<int64_t>(p.shape.N) + p.shape.G;
