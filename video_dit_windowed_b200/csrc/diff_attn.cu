@@ -100,7 +100,41 @@ struct DeltaPtr {
     float *delta;
 };
 
+// D_1 and D_2 of a row with at most kFewKeys keys, by a warp; others are left.
 template <typename T, int HD>
+__device__ __noinline__ void few_keys(const DeltaPtr<T> &p, const AttnGeom &g,
+                                      const geo::RowAt &at, int head, int64_t col, float &d1,
+                                      float &d2) {
+    int64_t a0 = 0, a1 = 0, b0 = 0, b1 = g.G;
+    if (at.detail) geo::global_keys(g, geo::window_at(g, at.local, a0, a1), b0, b1);
+    if (a1 - a0 + b1 - b0 > kFewKeys) return;
+    const int lane = threadIdx.x & 31, n_a = static_cast<int>(a1 - a0),
+              n = n_a + static_cast<int>(b1 - b0);
+    const int64_t off = (at.row * g.heads + head) * HD;
+    const T *q = p.q[at.detail ? 0 : 1] + off, *d = (at.detail ? p.do_d : p.do_g) + off;
+    const float l1 = p.lse[col], l2 = p.lse[col + g.N + g.G];
+    d1 = d2 = 0.f;
+    for (int j = 0; j < n; ++j) {
+        const int side = j < n_a ? 0 : 1;
+        const int64_t row = at.b * (side ? g.G : g.N) + (side ? b0 + j - n_a : a0 + j);
+        const T *k = p.k[side] + (row * g.heads + head) * HD;
+        const T *v = p.v[side] + (row * g.heads + head) * HD;
+        float s[2] = {0.f, 0.f}, dp = 0.f;
+#pragma unroll
+        for (int e = 0; e < HD / 32; ++e) {
+            const int c = lane + 32 * e;
+            s[e / (HD / 64)] = fmaf(to_f(q[c]), to_f(k[c]), s[e / (HD / 64)]);
+            dp = fmaf(to_f(d[c]), to_f(v[c]), dp);
+        }
+        dp = warp_sum(dp);
+        d1 = fmaf(expf(fmaf(warp_sum(s[0]), p.scale, -l1)), dp, d1);
+        d2 = fmaf(expf(fmaf(warp_sum(s[1]), p.scale, -l2)), dp, d2);
+    }
+}
+
+// FEW: rows with at most kFewKeys keys are possible, of bf16 (without: 720p, one
+// head, 21 us; with the test for them 49 us).
+template <typename T, int HD, bool FEW>
 __global__ void __launch_bounds__(kWarps * 32) diff_delta_kernel(const DeltaPtr<T> p,
                                                                  const AttnGeom g) {
     const int lane = threadIdx.x & 31;
@@ -124,38 +158,7 @@ __global__ void __launch_bounds__(kWarps * 32) diff_delta_kernel(const DeltaPtr<
     const int64_t col = (at.b * g.heads + head) * 2 * rows +
                         (at.detail ? at.local : g.N + at.local);
     float d1 = fmaf(p.lambda[p.n_lambda == 1 ? 0 : head], sum_s, sum_o);
-    if (sizeof(T) == 2 && (g.G <= kFewKeys || g.gwin_off != nullptr)) {
-        int64_t a0 = 0, a1 = 0, b0 = 0, b1 = g.G;
-        if (at.detail) geo::global_keys(g, geo::window_at(g, at.local, a0, a1), b0, b1);
-        const int n_a = static_cast<int>(a1 - a0), n = n_a + static_cast<int>(b1 - b0);
-        if (n <= kFewKeys) {
-            const T *q = p.q[at.detail ? 0 : 1] + off;
-            const float l1 = p.lse[col], l2 = p.lse[col + rows];
-            float few1 = 0.f, few2 = 0.f;
-            for (int j = 0; j < n; ++j) {
-                const int side = j < n_a ? 0 : 1;
-                const int64_t row_k = at.b * (side ? g.G : g.N) + (side ? b0 + j - n_a : a0 + j);
-                const T *k = p.k[side] + (row_k * g.heads + head) * HD;
-                const T *v = p.v[side] + (row_k * g.heads + head) * HD;
-                float s1 = 0.f, s2 = 0.f, dp = 0.f;
-#pragma unroll
-                for (int e = 0; e < HD / 32; ++e) {
-                    const int c = lane + 32 * e;
-                    const float x = to_f(q[c]) * to_f(k[c]);   // (exact: 8-bit factors)
-                    if (e < HD / 64) s1 += x;
-                    else s2 += x;
-                    dp = fmaf(to_f(d[c]), to_f(v[c]), dp);
-                }
-                s1 = warp_sum(s1);
-                s2 = warp_sum(s2);
-                dp = warp_sum(dp);
-                few1 = fmaf(expf(fmaf(s1, p.scale, -l1)), dp, few1);
-                few2 = fmaf(expf(fmaf(s2, p.scale, -l2)), dp, few2);
-            }
-            d1 = few1;
-            sum_s = few2;
-        }
-    }
+    if (FEW) few_keys<T, HD>(p, g, at, head, col, d1, sum_s);
     if (lane == 0) {
         // 0 for finite values, NaN otherwise
         const float mark = 0.f * p.lse[col] + 0.f * p.lse[col + rows] + 0.f * d1 + 0.f * sum_s;
@@ -241,7 +244,9 @@ atlas_status delta_hd(const DiffBwdArgs &b, cudaStream_t stream) {
     p.lse = a.lse;
     p.delta = b.delta;
     log_rows("diff_delta_kernel", a);
-    diff_delta_kernel<T, HD><<<row_grid(a), kWarps * 32, 0, stream>>>(p, attn_geom_of(a));
+    const bool few = sizeof(T) == 2 && (a.n_global <= kFewKeys || a.gwin_off != nullptr);
+    if (few) diff_delta_kernel<T, HD, true><<<row_grid(a), kWarps * 32, 0, stream>>>(p, attn_geom_of(a));
+    else diff_delta_kernel<T, HD, false><<<row_grid(a), kWarps * 32, 0, stream>>>(p, attn_geom_of(a));
     return launched();
 }
 

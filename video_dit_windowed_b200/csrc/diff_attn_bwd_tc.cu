@@ -497,12 +497,6 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
             const int32_t lo = j < U.n_a ? da : ga, hi = j < U.n_a ? db : gb;
             const int32_t t0 = units::tile_row<kStream>(U, j), c0 = t0 + part * kCols;   // column 0
             const bool partial = c0 < lo || c0 + kCols > hi;
-            // DKDV, a lone query at column lo: its dS is 0 unless it is marked (its
-            // range is one row, so the tile is partial).
-            int32_t hi_d = hi;
-            if (FORM == kDKDV && (j < U.n_a ? lone_a : lone_b) && lo >= t0 && lo < t0 + kStream &&
-                !isnan(sm.delta[stage][0][lo - t0]))
-                hi_d = lo;
             uint32_t pw[kPack], pd1[kPack], pd2[kPack];
 #pragma unroll
             for (int e = 0; e < kPack; ++e) {
@@ -528,18 +522,30 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
                     w[k] = FORM == kDQ ? 0.f : fmaf(dl[0], 0.f, fmaf(nlam, p2, p1));
                     d1[k] = p1 * (g - dl[0]);
                     d2[k] = p2 * (g - dl[1]);
+                    if (partial && (c0 + c < lo || c0 + c >= hi)) w[k] = d1[k] = d2[k] = 0.f;
                     if (FORM == kDQ) {
-                        if (partial && (c0 + c < lo || c0 + c >= hi)) d1[k] = d2[k] = 0.f;
                         sum_d[0] += d1[k];
                         sum_d[1] += d2[k];
-                    } else {
-                        if (partial && (c0 + c < lo || c0 + c >= hi)) w[k] = 0.f;
-                        if (partial && (c0 + c < lo || c0 + c >= hi_d)) d1[k] = d2[k] = 0.f;
                     }
                 }
                 pw[e] = ptx::pack_bf16x2(w[0], w[1]);
                 pd1[e] = ptx::pack_bf16x2(d1[0], d1[1]);
                 pd2[e] = ptx::pack_bf16x2(d2[0], d2[1]);
+            }
+            if (FORM == kDKDV) {
+                // A lone query (column lo) has dS = 0 unless it is marked.
+                const bool lone = (j < U.n_a ? lone_a : lone_b) && lo >= t0 && lo < t0 + kStream &&
+                                  !isnan(sm.delta[stage][0][lo - t0]);
+                if (__any_sync(kAll, lone)) {
+#pragma unroll
+                    for (int e = 0; e < kPack; ++e) {
+                        const uint32_t keep =
+                            !lone ? kAll : (c0 + 2 * e == lo ? 0xffff0000u
+                                                             : (c0 + 2 * e + 1 == lo ? 0xffffu : kAll));
+                        pd1[e] &= keep;
+                        pd2[e] &= keep;
+                    }
+                }
             }
             // The products of the previous tile have read the packed columns.
             if (cnt > 0 &&
