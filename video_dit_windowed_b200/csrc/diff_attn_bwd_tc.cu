@@ -29,7 +29,8 @@
 // D comes from outputs that were rounded to 16 bits, which dlambda = -sum D_2, a
 // sum of terms of both signs, would show (0.7% of it at head width 128). The sum of
 // a row's dS is what D lacks, so DQ, which runs first, adds it: D is then as exact
-// as P and dP. A query with one key has dS = 0 whatever D's rounding: set so.
+// as P and dP. A query with one key has dS = 0 whatever D's rounding: DQ sets it, DKDV
+// sets dK of a key that has such a query only (NaN stays).
 //
 // Warps (352 threads): 0-7 compute (thread = resident row = lane; warpgroup g
 // takes half of a tile's columns), 8 TMA producer, 9 / 10 MMA issuers (S and dP;
@@ -103,8 +104,8 @@ struct Smem {
     uint64_t x_full, x_empty;
     uint64_t st_full[kStages], st_empty[kStages];
     uint64_t s_full;     // S_1, S_2, dP of a tile in TMEM           (commit)
-    uint64_t s_read;     // ... loaded by the compute threads        (8 warps)
-    uint64_t p_full;     // packed P / dS in TMEM                    (8 warps)
+    uint64_t s_read;     // ... loaded by the compute threads        (256)
+    uint64_t p_full;     // packed P / dS in TMEM                    (256)
     uint64_t acc_done;   // the products that read them are done     (commit)
     uint64_t acc_full, acc_empty;
     uint64_t drain[2];
@@ -429,7 +430,7 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
         if constexpr (HD == 128) ptx::tmem_st64(dst, rv);
         else ptx::tmem_st32(dst, rv);
         ptx::tc_fence_before();
-        ptx::mbar_arrive_warp(ptx::smem_addr(&sm.x_full));
+        ptx::mbar_arrive(ptx::smem_addr(&sm.x_full));
     };
     bool resident_ready = false;   // DQ: this unit's rows were written ahead
 
@@ -453,7 +454,7 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
         int32_t da = 0, db = 0, ga = 0, gb = 0;   // streamed rows this row meets
         float own_l[2] = {__builtin_huge_valf(), __builtin_huge_valf()}, own_d[2] = {0.f, 0.f};
         float sum_d[2] = {0.f, 0.f};              // DQ: of this warpgroup's dS
-        bool lone_a = false, lone_b = false;      // DKDV: the query sees no other key
+        float dk_on = 1.f;                        // DKDV: 0 where dK is
         const int64_t col = (static_cast<int64_t>(U.b) * p.shape.heads + U.head) * 2 * per +
                             (U.detail ? row : static_cast<int64_t>(N) + row);
         if (valid) {
@@ -468,8 +469,10 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
                 if (db - da + gb - ga == 1 && !isnan(own_d[0])) da = db = ga = gb = 0;
             } else {
                 units::key_ranges(p.shape, U, row, da, db, ga, gb);
-                lone_a = U.detail && db - da == 1 && units::no_global_key(p.shape, U, row);
-                lone_b = !U.detail && G == 1;
+                // The key's one query sees no other key: P = 1 and dS = 0 (or NaN).
+                if (U.detail ? db - da == 1 && units::no_global_key(p.shape, U, row)
+                             : G == 1 && da == db)
+                    dk_on = 0.f;
             }
         }
         if (FORM == kDQ && !resident_ready) {
@@ -493,7 +496,7 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
             if constexpr (kCols == 32) ptx::tmem_ld3x32(src, src + 64, src + TM::kDP, s1, s2, dp);
             else ptx::tmem_ld3x24(src, src + 64, src + TM::kDP, s1, s2, dp);
             ptx::tc_fence_before();
-            ptx::mbar_arrive_warp(ptx::smem_addr(&sm.s_read));
+            ptx::mbar_arrive(ptx::smem_addr(&sm.s_read));
             const int32_t lo = j < U.n_a ? da : ga, hi = j < U.n_a ? db : gb;
             const int32_t t0 = units::tile_row<kStream>(U, j), c0 = t0 + part * kCols;   // column 0
             const bool partial = c0 < lo || c0 + kCols > hi;
@@ -531,21 +534,6 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
                 pw[e] = ptx::pack_bf16x2(w[0], w[1]);
                 pd1[e] = ptx::pack_bf16x2(d1[0], d1[1]);
                 pd2[e] = ptx::pack_bf16x2(d2[0], d2[1]);
-            }
-            if (FORM == kDKDV) {
-                // A lone query (column lo) has dS = 0 unless it is marked.
-                const bool lone = (j < U.n_a ? lone_a : lone_b) && lo >= t0 && lo < t0 + kStream &&
-                                  !isnan(sm.delta[stage][0][lo - t0]);
-                if (__any_sync(kAll, lone)) {
-#pragma unroll
-                    for (int e = 0; e < kPack; ++e) {
-                        const uint32_t keep =
-                            !lone ? kAll : (c0 + 2 * e == lo ? 0xffff0000u
-                                                             : (c0 + 2 * e + 1 == lo ? 0xffffu : kAll));
-                        pd1[e] &= keep;
-                        pd2[e] &= keep;
-                    }
-                }
             }
             // The products of the previous tile have read the packed columns.
             if (cnt > 0 &&
@@ -608,7 +596,7 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
                 sm.row_sum[unit_iter & 1][1][r] = sum_d[1];
             }
             ptx::tc_fence_before();
-            ptx::mbar_arrive_warp(ptx::smem_addr(&sm.p_full));
+            ptx::mbar_arrive(ptx::smem_addr(&sm.p_full));
         }
         if (FORM == kDQ) {
             // The next unit's resident rows go in as soon as this unit's
@@ -640,8 +628,9 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
         const int side = U.detail ? 0 : 1;
         const int64_t out_row = (static_cast<int64_t>(U.b) * (U.detail ? N : G) +
                                  (valid ? row : 0)) * p.shape.heads + U.head;
-        // ncol columns of tensor memory from `col`, times f, to channel ch0 on.
-        auto store = [&](__nv_bfloat16 *out, uint32_t col, int ch0, int ncol, float f) {
+        // ncol columns of tensor memory from `col`, times f (a part's sums: times
+        // on), to channel ch0 on.
+        auto store = [&](__nv_bfloat16 *out, uint32_t col, int ch0, int ncol, float f, float on) {
             uint8_t *dst = reinterpret_cast<uint8_t *>(out + out_row * HD + ch0);
 #pragma unroll 1
             for (int c = 0; c < ncol / 32; ++c) {
@@ -649,6 +638,9 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
                 ptx::tmem_ld32(t + col + c * 32, o);
                 if (sums != nullptr) {
                     uint4 *at = reinterpret_cast<uint4 *>(sums + ch0 + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * on);
 #pragma unroll
                     for (int v = 0; v < 8; ++v)
                         at[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
@@ -675,18 +667,18 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
         // half of its 64 columns that its channels are).
         auto store_map = [&](int m) {
             store(p.grad[side], TM::kGrad + 64 * m + (HD == 64 ? 32 * m : 0), m * (HD / 2), HD / 2,
-                  m == 0 ? p.scale : p.scale * nlam);
+                  (m == 0 ? p.scale : p.scale * nlam) * dk_on, dk_on);
         };
         if (FORM == kDQ) {
             store_map(part);
         } else if (part == 0) {
-            store(p.dv[side], TM::kDV, 0, HD, 1.f);
+            store(p.dv[side], TM::kDV, 0, HD, 1.f, 1.f);
         } else {
             store_map(0);
             store_map(1);
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive_warp(ptx::smem_addr(&sm.acc_empty));
+        ptx::mbar_arrive(ptx::smem_addr(&sm.acc_empty));
         ++unit_iter;
     }
 }
@@ -699,18 +691,18 @@ __global__ void __launch_bounds__(kThreads, 1) diff_bwd_tc_kernel(const __grid_c
                                      ~static_cast<uintptr_t>(1023));
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        ptx::mbar_init(ptx::smem_addr(&sm.x_full), FORM == kDQ ? kCompute / 32 : 1);
+        ptx::mbar_init(ptx::smem_addr(&sm.x_full), FORM == kDQ ? kCompute : 1);
         ptx::mbar_init(ptx::smem_addr(&sm.x_empty), 1);
         for (int s = 0; s < SM::kStages; ++s) {
             ptx::mbar_init(ptx::smem_addr(&sm.st_full[s]), 1);
             ptx::mbar_init(ptx::smem_addr(&sm.st_empty[s]), 1);
         }
         ptx::mbar_init(ptx::smem_addr(&sm.s_full), 1);
-        ptx::mbar_init(ptx::smem_addr(&sm.s_read), kCompute / 32);
-        ptx::mbar_init(ptx::smem_addr(&sm.p_full), kCompute / 32);
+        ptx::mbar_init(ptx::smem_addr(&sm.s_read), kCompute);
+        ptx::mbar_init(ptx::smem_addr(&sm.p_full), kCompute);
         ptx::mbar_init(ptx::smem_addr(&sm.acc_done), 1);
         ptx::mbar_init(ptx::smem_addr(&sm.acc_full), 1);
-        ptx::mbar_init(ptx::smem_addr(&sm.acc_empty), kCompute / 32);
+        ptx::mbar_init(ptx::smem_addr(&sm.acc_empty), kCompute);
         ptx::mbar_init(ptx::smem_addr(&sm.drain[0]), 1);
         ptx::mbar_init(ptx::smem_addr(&sm.drain[1]), 1);
         sm.abort = 0;

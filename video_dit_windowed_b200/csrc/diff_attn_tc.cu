@@ -65,6 +65,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8
+constexpr int kFewTiles = 4;   // of 128 keys (softmax_epilogue)
 
 template <int HD>
 struct Smem {
@@ -353,13 +354,13 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
 
     // Columns [B, B + N) of 64 keys' S: P = exp2(S*scale*log2e - m) as bf16 pairs
     // into pk (rounding P halves the product's operand and is 2^-8 of each weight;
-    // the row sum adds the fp32 P). Not FAST: `rounded` sums them as rounded. FAST: the maximum of the raw S joins mx, NaN
+    // the row sum adds the fp32 P). FAST: the maximum of the raw S joins mx, NaN
     // kept, and one pair of eight takes its exponentials on the FMA pipe (720p, D =
     // 128 / 32,760 global tokens, D = 64: none 1628 / 906-975 us, one 1612 / 889, two
     // 1597 / 920, three 1640 / 970, four 1703 / 1015: beyond one the issue slots cost
     // what the MUFU saves).
     auto exps = [&](auto fast, auto from, auto count, const uint32_t (&sr)[64], float m,
-                    ptx::F2 &sum, ptx::F2 &rounded, float (&mx)[2], uint32_t (&pk)[16]) {
+                    ptx::F2 &sum, float (&mx)[2], uint32_t (&pk)[16]) {
         constexpr bool kFast = decltype(fast)::value;
         constexpr int B = decltype(from)::value, N = decltype(count)::value;
         const ptx::F2 scale2 = ptx::f2(sc, sc), negm2 = ptx::f2(-m, -m);
@@ -378,23 +379,18 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 p1 = ptx::ex2(p1);
             }
             sum = ptx::add2(sum, ptx::f2(p0, p1));
-            const uint32_t pp = ptx::pack_bf16x2(p0, p1);
-            pk[(c % 32) / 2] = pp;
-            if constexpr (!kFast)
-                rounded = ptx::add2(rounded, ptx::f2(__uint_as_float(pp << 16),
-                                                     __uint_as_float(pp & 0xffff0000u)));
+            pk[(c % 32) / 2] = ptx::pack_bf16x2(p0, p1);
         }
     };
     constexpr std::integral_constant<int, 0> c0{};
     constexpr std::integral_constant<int, 32> c32{};
     // All 64 with ex2, stored (masked tiles, and rows whose reference moves).
-    ptx::F2 rounded = ptx::f2(0.f, 0.f);
     auto exps_all = [&](const uint32_t (&sr)[64], float m, uint32_t dst, ptx::F2 &sum) {
         float unused[2];
         uint32_t pk[16];
-        exps(std::false_type{}, c0, c32, sr, m, sum, rounded, unused, pk);
+        exps(std::false_type{}, c0, c32, sr, m, sum, unused, pk);
         ptx::tmem_st16_nowait(dst, pk);
-        exps(std::false_type{}, c32, c32, sr, m, sum, rounded, unused, pk);
+        exps(std::false_type{}, c32, c32, sr, m, sum, unused, pk);
         ptx::tmem_st16_nowait(dst + 16, pk);
     };
     auto row_max = [&](const uint32_t (&sr)[64]) -> float {
@@ -424,6 +420,24 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
         }
     };
 
+    // The sum of a tile's 128 weights as stored.
+    auto rounded_sum = [&](uint32_t src) -> float {
+        ptx::tmem_wait_st();
+        ptx::F2 sum = ptx::f2(0.f, 0.f);
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+            uint32_t w[32];
+            ptx::tmem_ld32(src + c * 32, w);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                sum = ptx::add2(sum, ptx::f2(__uint_as_float(w[e] << 16),
+                                             __uint_as_float(w[e] & 0xffff0000u)));
+        }
+        float s0, s1;
+        ptx::unpack(sum, s0, s1);
+        return s0 + s1;
+    };
+
     // PACK: tiles whose keys not every row of the unit sees.
     auto scanned = [&](const Unit &U, int32_t j) {
         return PACK && U.detail && U.win < 0 && (j < U.n_a || p.shape.gwin_off != nullptr);
@@ -451,11 +465,11 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
         const float lam = __ldg(p.lambda + (p.n_lambda == 1 ? 0 : U.head));
         // The reference m_run (log2 units) is whole, so that moving it scales by a
         // power of two, exactly.
-        // l_fix: what the sum of the rounded weights of masked tiles differs by. O is
-        // divided by the sum of the weights as its products had them, so that a row
-        // with one key gets its V exactly and a row with few keys no common error,
-        // which o_1 - lambda o_2 would enlarge; over full tiles it averages out (and
-        // would cost two instructions a weight).
+        // l_fix: what the sum of the weights changes by their rounding, in units of
+        // few tiles. O is divided by the sum of the weights as its products had them,
+        // so that a row with one key gets its V exactly and a row with few keys no
+        // common error, which o_1 - lambda o_2 would enlarge. Over many tiles it
+        // averages out (and two instructions a weight cost 2%).
         float m_run = kNegInf, l_run = 0.f, l_fix = 0.f;
         bool bad = false;
         // The bad rows of tile j (tile count c), which this map's threads wrote
@@ -496,7 +510,7 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 ptx::tc_fence_after();
                 ptx::tmem_ld64(t_hi, hi);
                 ptx::tc_fence_before();
-                ptx::mbar_arrive_warp(ptx::smem_addr(&sm.s_read[map]));
+                ptx::mbar_arrive(ptx::smem_addr(&sm.s_read[map]));
                 if (PACK && j > 0) check_bad(j - 1, cnt - 1);
                 if (masked) {
 #pragma unroll
@@ -508,21 +522,21 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 }
                 move(fmaxf(row_max(lo), row_max(hi)) * sc, j == 0);
                 const float m = m_run == kNegInf ? 0.f : m_run;
-                rounded = ptx::f2(0.f, 0.f);
                 exps_all(lo, m, t_lo, sum);
                 exps_all(hi, m, t_lo + 32, sum);
-                float s0, s1, r0, r1;
-                ptx::unpack(sum, s0, s1);
-                ptx::unpack(rounded, r0, r1);
-                l_fix += (r0 - s0) + (r1 - s1);
+                if (n <= kFewTiles) {
+                    float s0, s1;
+                    ptx::unpack(sum, s0, s1);
+                    l_fix += rounded_sum(t_lo) - (s0 + s1);
+                }
             } else {
                 // Exponentials against the running reference right away; a half
                 // whose maximum turns out past the threshold (or NaN) is redone.
                 float mx[2] = {kNegInf, kNegInf};
                 uint32_t pk[16];
-                exps(std::true_type{}, c0, c32, lo, m_run, sum, rounded, mx, pk);
+                exps(std::true_type{}, c0, c32, lo, m_run, sum, mx, pk);
                 ptx::tmem_st16_nowait(t_lo, pk);
-                exps(std::true_type{}, c32, c32, lo, m_run, sum, rounded, mx, pk);
+                exps(std::true_type{}, c32, c32, lo, m_run, sum, mx, pk);
                 ptx::tmem_st16_nowait(t_lo + 16, pk);
                 if (!__all_sync(kAll, wait_phase(sm, sm.s_hi[map], cnt & 1, err))) return;
                 ptx::tc_fence_after();
@@ -535,14 +549,14 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 }
                 ptx::tmem_ld64(t_hi, hi);
                 ptx::tc_fence_before();
-                ptx::mbar_arrive_warp(ptx::smem_addr(&sm.s_read[map]));
+                ptx::mbar_arrive(ptx::smem_addr(&sm.s_read[map]));
                 if (PACK && j > 0) check_bad(j - 1, cnt - 1);
                 const ptx::F2 sum_lo = sum;
                 mx[0] = mx[1] = kNegInf;
                 sum = ptx::f2(0.f, 0.f);
-                exps(std::true_type{}, c0, c32, hi, m_run, sum, rounded, mx, pk);
+                exps(std::true_type{}, c0, c32, hi, m_run, sum, mx, pk);
                 ptx::tmem_st16_nowait(t_lo + 32, pk);
-                exps(std::true_type{}, c32, c32, hi, m_run, sum, rounded, mx, pk);
+                exps(std::true_type{}, c32, c32, hi, m_run, sum, mx, pk);
                 ptx::tmem_st16_nowait(t_lo + 48, pk);
                 mx2 = ptx::max_nan(mx[0], mx[1]) * sc;
                 float f = 1.f;
@@ -606,14 +620,14 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
             ptx::unpack(sum, sum0, sum1);
             l_run += sum0 + sum1;
             ptx::tc_fence_before();
-            ptx::mbar_arrive_warp(ptx::smem_addr(&sm.p_full[map]));
+            ptx::mbar_arrive(ptx::smem_addr(&sm.p_full[map]));
         }
         // Epilogue: both maps' 1/l through shared memory; this group joins
         // columns [map * D/2, +D/2) of O_1 and O_2.
         const uint32_t par = unit_iter & 1;
         const float l_o = l_run + l_fix;
         sm.inv_l[par][map][r] = l_o > 0.f ? 1.f / l_o : (l_o == 0.f ? 0.f : l_o);
-        ptx::mbar_arrive_warp(ptx::smem_addr(&sm.joined));
+        ptx::mbar_arrive(ptx::smem_addr(&sm.joined));
         if (p.lse != nullptr && valid) {
             const int64_t rows = static_cast<int64_t>(p.shape.N) + p.shape.G;
             p.lse[((static_cast<int64_t>(U.b) * p.shape.heads + U.head) * 2 + map) * rows +
@@ -638,7 +652,7 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
             ptx::tmem_ld32(t_o2, o2);
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive_warp(ptx::smem_addr(&sm.o_empty));
+        ptx::mbar_arrive(ptx::smem_addr(&sm.o_empty));
         ++unit_iter;
         if (!valid) continue;
         const int side = U.detail ? 0 : 1;
@@ -688,14 +702,14 @@ __global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_const
         for (int m = 0; m < kMaps; ++m) {
             ptx::mbar_init(ptx::smem_addr(&sm.s_lo[m]), 1);
             ptx::mbar_init(ptx::smem_addr(&sm.s_hi[m]), 1);
-            ptx::mbar_init(ptx::smem_addr(&sm.s_read[m]), kBM / 32);
-            ptx::mbar_init(ptx::smem_addr(&sm.p_full[m]), kBM / 32);
+            ptx::mbar_init(ptx::smem_addr(&sm.s_read[m]), kBM);
+            ptx::mbar_init(ptx::smem_addr(&sm.p_full[m]), kBM);
             ptx::mbar_init(ptx::smem_addr(&sm.drain[m]), 1);
         }
         ptx::mbar_init(ptx::smem_addr(&sm.o_final), kMaps);
         for (int i = 0; i < 4 * kBM; ++i) sm.mark[i / kBM][i % kBM] = 0;
-        ptx::mbar_init(ptx::smem_addr(&sm.joined), kMaps * kBM / 32);
-        ptx::mbar_init(ptx::smem_addr(&sm.o_empty), kMaps * kBM / 32);
+        ptx::mbar_init(ptx::smem_addr(&sm.joined), kMaps * kBM);
+        ptx::mbar_init(ptx::smem_addr(&sm.o_empty), kMaps * kBM);
         sm.abort = 0;
         sm.max_len = 0;
         sm.err_word = p.err_word;
