@@ -908,7 +908,7 @@ ATLAS_API int64_t atlas_diff_attn_bwd_workspace(int64_t batch, int64_t n_detail,
         n_detail > kMaxRows / batch || n_global > kMaxRows / batch || heads < 1 ||
         heads > 65535 || (head_dim != 64 && head_dim != 128) || elem_bytes(dtype) == 0)
         return 0;
-    const int parts = dtype == ATLAS_BF16 ? diff_split_plan(batch, n_detail, n_global, heads) : 1;
+    const int parts = diff_split_plan(batch, n_detail, n_global, heads, elem_bytes(dtype));
     return 4 * (2 * batch * heads * (n_detail + n_global) +
                 static_cast<int64_t>(heads) * kDiffLambdaParts +
                 (parts > 1 ? parts * batch * heads * n_global * 2 * head_dim : 0));

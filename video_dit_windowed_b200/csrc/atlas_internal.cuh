@@ -192,7 +192,7 @@ struct DiffBwdArgs {
     const void *do_d, *do_g;
     float *delta;               // [batch, heads, 2, N+G]: D_1, D_2
     float *part;                // [heads, kDiffLambdaParts]
-    float *split;               // bf16: sums of diff_split_plan's parts (see there)
+    float *split;               // sums of diff_split_plan's parts (see there)
     void *dq_d, *dk_d, *dv_d, *dq_g, *dk_g, *dv_g;
     float *dlambda;
 };
@@ -205,9 +205,12 @@ struct DiffLambdaArgs {
     int32_t n, d, elem_bytes;
 };
 constexpr int kDiffLambdaParts = 64;
-// Parts of the bf16 backward pass' units over global keys; with more than one,
-// split holds [parts][batch * heads][n_global][2 * head_dim] floats.
-int diff_split_plan(int64_t batch, int64_t n_detail, int64_t n_global, int32_t heads);
+// Parts that the queries of a backward block over global keys are cut into; with
+// more than one, split holds [parts][batch * heads][n_global][dV | dK] floats, dK
+// without its factor, and the launch below joins them.
+int diff_split_plan(int64_t batch, int64_t n_detail, int64_t n_global, int32_t heads,
+                    int elem_bytes);
+atlas_status launch_diff_split_join(const DiffBwdArgs &a, int parts, cudaStream_t stream);
 atlas_status launch_diff_lambda(const DiffLambdaArgs &a, bool bwd, cudaStream_t stream);
 atlas_status launch_diff_attn_tc(const DiffArgs &a, cudaStream_t stream);   // bf16
 atlas_status launch_diff_attn_simt_f32(const DiffArgs &a, cudaStream_t stream);

@@ -202,6 +202,48 @@ __global__ void __launch_bounds__(32) dlambda_join_kernel(const float *part, flo
     if (threadIdx.x == 0) dlambda[blockIdx.x] = static_cast<float>(-acc);
 }
 
+// Global rows' dV and dK from the parts' sums: one thread per four channels of a
+// (row, head), parts added in order.
+template <typename T>
+struct JoinPtr {
+    const float *split, *lambda;
+    T *dv, *dk;
+    int64_t batch, rows;
+    int32_t heads, n_lambda, parts;
+    float scale;
+};
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(256) diff_split_join_kernel(const JoinPtr<T> p) {
+    constexpr int kVecs = 2 * HD / 4;
+    const int64_t cells = p.batch * p.heads;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= cells * p.rows * kVecs) return;
+    const int64_t at = i / kVecs;   // (cell, row)
+    const int c = static_cast<int>(i - at * kVecs) * 4;
+    const int64_t cell = at / p.rows, row = at - cell * p.rows;
+    const int64_t b = cell / p.heads, head = cell - b * p.heads;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int part = 0; part < p.parts; ++part) {
+        const float4 x = __ldcs(reinterpret_cast<const float4 *>(
+            p.split + (part * cells * p.rows + at) * (2 * HD) + c));
+        s.x += x.x;
+        s.y += x.y;
+        s.z += x.z;
+        s.w += x.w;
+    }
+    const bool dv = c < HD;
+    const int ch = dv ? c : c - HD;
+    const float f = dv ? 1.f
+                       : (ch < HD / 2 ? p.scale
+                                      : -p.scale * __ldg(p.lambda + (p.n_lambda == 1 ? 0 : head)));
+    T *out = (dv ? p.dv : p.dk) + ((b * p.rows + row) * p.heads + head) * HD + ch;
+    out[0] = from_f<T>(s.x * f);
+    out[1] = from_f<T>(s.y * f);
+    out[2] = from_f<T>(s.z * f);
+    out[3] = from_f<T>(s.w * f);
+}
+
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
@@ -250,7 +292,61 @@ atlas_status delta_hd(const DiffBwdArgs &b, cudaStream_t stream) {
     return launched();
 }
 
+template <typename T, int HD>
+atlas_status join_hd(const DiffBwdArgs &b, int parts, cudaStream_t stream) {
+    const AttnArgs &a = b.fwd.attn;
+    JoinPtr<T> p;
+    p.split = b.split;
+    p.lambda = b.fwd.lambda;
+    p.dv = static_cast<T *>(b.dv_g);
+    p.dk = static_cast<T *>(b.dk_g);
+    p.batch = a.batch;
+    p.rows = a.n_global;
+    p.heads = a.heads;
+    p.n_lambda = b.fwd.n_lambda;
+    p.parts = parts;
+    p.scale = a.scale;
+    const int64_t vecs = a.batch * a.n_global * a.heads * (2 * HD / 4);
+    diff_split_join_kernel<T, HD><<<static_cast<unsigned>((vecs + 255) / 256), 256, 0, stream>>>(p);
+    return launched();
+}
+
 }  // namespace
+
+// The count, up to 16 (bf16) or 64 (fp32), with the fewest tiles on the busiest of
+// a B200's 148 SMs, a block's start and end taken as four tiles and the joining
+// launch as eight. bf16 at 720p: with one head 40 units of 1,785 tiles kept 40 SMs
+// busy for 2,423 us, cut into 11 parts 440 units take all of them 805 us; from four
+// heads on the uncut units fill the SMs.
+int diff_split_plan(int64_t batch, int64_t n_detail, int64_t n_global, int32_t heads,
+                    int elem_bytes) {
+    constexpr int64_t kSms = 148;
+    const int64_t rows = elem_bytes == 2 ? 128 : 64;   // key rows of a block
+    const int64_t tile = elem_bytes == 2 ? 48 : 64;    // streamed rows of a tile
+    const int most = elem_bytes == 2 ? 16 : 64;
+    const int64_t units = (n_global + rows - 1) / rows * batch * heads;
+    const int64_t len = (n_detail + n_global + tile - 1) / tile;
+    if (units == 0 || units > 16 * kSms) return 1;
+    const int64_t whole = (units + kSms - 1) / kSms * (len + 4);
+    int best = 1;
+    int64_t least = whole;
+    for (int s = 2; s <= most; ++s) {
+        const int64_t load = (units * s + kSms - 1) / kSms * ((len + s - 1) / s + 4) + 8;
+        if (load < least) {
+            best = s;
+            least = load;
+        }
+    }
+    return 10 * least < 9 * whole ? best : 1;
+}
+
+atlas_status launch_diff_split_join(const DiffBwdArgs &b, int parts, cudaStream_t stream) {
+    if (b.fwd.elem_bytes == 2)
+        return b.fwd.attn.head_dim == 128 ? join_hd<__nv_bfloat16, 128>(b, parts, stream)
+                                          : join_hd<__nv_bfloat16, 64>(b, parts, stream);
+    return b.fwd.attn.head_dim == 128 ? join_hd<float, 128>(b, parts, stream)
+                                      : join_hd<float, 64>(b, parts, stream);
+}
 
 atlas_status launch_diff_lambda(const DiffLambdaArgs &a, bool bwd, cudaStream_t stream) {
     LambdaPtr p;

@@ -16,7 +16,7 @@
 //         of Q and dO with their lse and D; accumulates dV and dK. With few heads
 //         the units over global keys are few and long (each streams every query):
 //         their queries are cut into parts, whose fp32 sums a second kernel joins
-//         in order (diff_split_plan).
+//         in order (diff_attn.cu, diff_split_plan).
 // Tensor memory holds S_1 | S_2 | dP of one tile, the packed bf16 dS_1 | dS_2 (and
 // W) in columns of their own, and the accumulators:
 //   DQ    3 x 64 + 64 + 128 (dQ) + 128 (resident Q, dO) = 512,
@@ -748,39 +748,6 @@ __global__ void __launch_bounds__(kThreads, 1) diff_bwd_tc_kernel(const __grid_c
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Global rows' dV and dK from the parts' sums: one thread per four channels of a
-// (row, head), parts added in order.
-template <int HD>
-__global__ void __launch_bounds__(256) diff_split_join_kernel(const Params p) {
-    constexpr int kVecs = 2 * HD / 4;
-    const int64_t cells = static_cast<int64_t>(p.shape.batch) * p.shape.heads;
-    const int64_t total = cells * p.shape.G * kVecs;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= total) return;
-    const int64_t at = i / kVecs;   // (cell, row)
-    const int c = static_cast<int>(i - at * kVecs) * 4;
-    const int64_t cell = at / p.shape.G, row = at - cell * p.shape.G;
-    const int64_t b = cell / p.shape.heads, head = cell - b * p.shape.heads;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int part = 0; part < p.shape.n_split; ++part) {
-        const float4 x = __ldcs(reinterpret_cast<const float4 *>(
-            p.split + (part * cells * p.shape.G + at) * (2 * HD) + c));
-        s.x += x.x;
-        s.y += x.y;
-        s.z += x.z;
-        s.w += x.w;
-    }
-    const bool dv = c < HD;
-    const int ch = dv ? c : c - HD;
-    const float f = dv ? 1.f
-                       : (ch < HD / 2 ? p.scale
-                                      : -p.scale * __ldg(p.lambda + (p.n_lambda == 1 ? 0 : head)));
-    __nv_bfloat16 *out = (dv ? p.dv[1] : p.grad[1]) +
-                         ((b * p.shape.G + row) * p.shape.heads + head) * HD + ch;
-    *reinterpret_cast<uint2 *>(out) =
-        make_uint2(ptx::pack_bf16x2(s.x * f, s.y * f), ptx::pack_bf16x2(s.z * f, s.w * f));
-}
-
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
@@ -824,7 +791,7 @@ atlas_status launch_form(const DiffBwdArgs &b, const DeviceInfo &dev, cudaStream
     p.scale = a.scale;
     p.scale_log2 = a.scale * kLog2e;
     if (!dq) {
-        p.shape.n_split = diff_split_plan(a.batch, a.n_detail, a.n_global, a.heads);
+        p.shape.n_split = diff_split_plan(a.batch, a.n_detail, a.n_global, a.heads, 2);
         n_units += static_cast<int64_t>(p.shape.n_split - 1) * p.shape.n_long;
         p.split = b.split;
     }
@@ -839,37 +806,11 @@ atlas_status launch_form(const DiffBwdArgs &b, const DeviceInfo &dev, cudaStream
                    static_cast<long long>(n_units), p.shape.n_split, p.shape.batch, p.shape.heads,
                    p.shape.N, p.shape.G);
     diff_bwd_tc_kernel<HD, FORM><<<grid, kThreads, smem, stream>>>(p);
-    if (p.shape.n_split > 1) {
-        const int64_t vecs = rows[1] * a.heads * (2 * HD / 4);
-        diff_split_join_kernel<HD><<<static_cast<unsigned>((vecs + 255) / 256), 256, 0, stream>>>(p);
-    }
-    return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) return ATLAS_ERR_CUDA;
+    return p.shape.n_split > 1 ? launch_diff_split_join(b, p.shape.n_split, stream) : ATLAS_OK;
 }
 
 }  // namespace
-
-// Parts that the units over global keys are cut into (1: none): the count, up to
-// 16, with the fewest tiles on the busiest of a B200's 148 SMs, a unit's start and
-// end taken as four tiles and the joining launch as eight. 720p: with one head 40
-// units of 1,785 tiles kept 40 SMs busy for 2,423 us, cut into 11 parts 440 units
-// take all of them 805 us; from four heads on the uncut units fill the SMs.
-int diff_split_plan(int64_t batch, int64_t n_detail, int64_t n_global, int32_t heads) {
-    constexpr int64_t kSms = 148;
-    const int64_t units = (n_global + kRows - 1) / kRows * batch * heads;
-    const int64_t len = (n_detail + n_global + Tile<kDKDV>::kStream - 1) / Tile<kDKDV>::kStream;
-    if (units == 0 || units > 16 * kSms) return 1;
-    const int64_t whole = (units + kSms - 1) / kSms * (len + 4);
-    int best = 1;
-    int64_t least = whole;
-    for (int s = 2; s <= 16; ++s) {
-        const int64_t load = (units * s + kSms - 1) / kSms * ((len + s - 1) / s + 4) + 8;
-        if (load < least) {
-            best = s;
-            least = load;
-        }
-    }
-    return 10 * least < 9 * whole ? best : 1;
-}
 
 atlas_status launch_diff_bwd_tc(const DiffBwdArgs &b, cudaStream_t stream) {
     DeviceInfo dev;

@@ -50,14 +50,17 @@ struct Span {
     }
 };
 
-__device__ __forceinline__ Span rows_of_block(const AttnGeom &g) {
+// Blocks of global rows come first, in `parts` each: over keys they are the longest.
+__device__ __forceinline__ Span rows_of_block(const AttnGeom &g, int parts, int &part) {
     Span s;
     s.head = blockIdx.y;
     const int64_t td = (g.N + kRows - 1) / kRows, tg = (g.G + kRows - 1) / kRows;
-    s.b = blockIdx.x / (td + tg);
-    const int64_t t = blockIdx.x - s.b * (td + tg);
-    s.detail = t < td;
-    s.r0 = (s.detail ? t : t - td) * kRows;
+    const int64_t n_long = g.batch * tg * parts, x = blockIdx.x;
+    s.detail = x >= n_long;
+    const int64_t v = s.detail ? x - n_long : x / parts, span = s.detail ? td : tg;
+    part = s.detail ? 0 : static_cast<int>(x - v * parts);
+    s.b = v / span;
+    s.r0 = (v - s.b * span) * kRows;
     const int64_t n = s.detail ? g.N : g.G;
     s.rend = s.r0 + kRows < n ? s.r0 + kRows : n;
     return s;
@@ -65,7 +68,8 @@ __device__ __forceinline__ Span rows_of_block(const AttnGeom &g) {
 
 // Queries: the union of the rows' windows and global keys.
 __device__ __forceinline__ Span query_span(const AttnGeom &g) {
-    Span s = rows_of_block(g);
+    int unused_part;
+    Span s = rows_of_block(g, 1, unused_part);
     s.a0 = s.a1 = s.b0 = 0;
     s.b1 = g.G;
     if (s.detail) {
@@ -80,9 +84,9 @@ __device__ __forceinline__ Span query_span(const AttnGeom &g) {
     return s;
 }
 
-// Keys: the queries that see them.
-__device__ __forceinline__ Span key_span(const AttnGeom &g) {
-    Span s = rows_of_block(g);
+// Keys: the queries that see them, or (of global keys) one part of their tiles.
+__device__ __forceinline__ Span key_span(const AttnGeom &g, int parts, int &part) {
+    Span s = rows_of_block(g, parts, part);
     s.b0 = s.b1 = 0;
     int64_t lo, hi;
     if (s.detail) {
@@ -105,6 +109,15 @@ __device__ __forceinline__ Span key_span(const AttnGeom &g) {
         }
     }
     s.cut();
+    if (!s.detail && parts > 1) {
+        const int64_t n = s.na + s.nb;
+        const int t0 = static_cast<int>(n * part / parts), t1 = static_cast<int>(n * (part + 1) / parts);
+        const int a = max(min(t1, s.na) - min(t0, s.na), 0);
+        s.a0 += static_cast<int64_t>(min(t0, s.na)) * kTile;
+        s.b0 += static_cast<int64_t>(max(t0 - s.na, 0)) * kTile;
+        s.na = a;
+        s.nb = t1 - t0 - a;
+    }
     return s;
 }
 
@@ -296,6 +309,8 @@ struct Ptr {
     const float *delta, *lambda;
     int32_t n_lambda;
     float scale;
+    float *split;                              // dK/dV: the parts' sums, with n_split > 1
+    int32_t n_split;
 };
 
 template <int HD>
@@ -459,7 +474,8 @@ __global__ void __launch_bounds__(kThreads) diff_dkdv_simt_kernel(const Ptr p, c
           *gs = qs + kTile * (HD + 4), *w = gs + kTile * (HD + 4);
     __shared__ float lse[2][kTile], del[2][kTile];
     __shared__ uint8_t bad[2][kTile];
-    const Span S = key_span(g);
+    int part;
+    const Span S = key_span(g, p.n_split, part);
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, side = S.detail ? 0 : 1;
     const int64_t stride = static_cast<int64_t>(g.heads) * HD, rows = g.N + g.G;
     const int64_t own = (S.b * (S.detail ? g.N : g.G) + S.r0) * stride + S.head * HD;
@@ -531,6 +547,13 @@ __global__ void __launch_bounds__(kThreads) diff_dkdv_simt_kernel(const Ptr p, c
     for (int i = 0; i < 4; ++i) {
         if (S.r0 + 4 * ty + i >= S.rend) continue;
         const int64_t off = own + (4 * ty + i) * stride;
+        if (!S.detail && p.n_split > 1) {
+            float *sums = p.split + (((static_cast<int64_t>(part) * g.batch + S.b) * g.heads + S.head) *
+                                         g.G + S.r0 + 4 * ty + i) * (2 * HD);
+            store<HD>(sums, dv, i, 1.f, 1.f);
+            store<HD>(sums + HD, dk, i, 1.f, 1.f);
+            continue;
+        }
         store<HD>(p.dk[side] + off, dk, i, p.scale, -lam * p.scale);
         store<HD>(p.dv[side] + off, dv, i, 1.f, 1.f);
     }
@@ -553,6 +576,7 @@ Ptr ptr_of(const DiffArgs &d) {
     p.lambda = d.lambda;
     p.n_lambda = d.n_lambda;
     p.scale = a.scale;
+    p.n_split = 1;
     return p;
 }
 
@@ -568,7 +592,8 @@ atlas_status launch(K kernel, const char *name, const Ptr &p, const AttnArgs &a,
     const size_t smem = n_floats * sizeof(float);
     if (!set_smem_limit(reinterpret_cast<const void *>(kernel), static_cast<int>(smem)))
         return ATLAS_ERR_CUDA;
-    const int64_t blocks = a.batch * ((a.n_detail + kRows - 1) / kRows + (a.n_global + kRows - 1) / kRows);
+    const int64_t blocks = a.batch * ((a.n_detail + kRows - 1) / kRows +
+                                      (a.n_global + kRows - 1) / kRows * p.n_split);
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(a.heads));
     if (log_enabled())
         log_launch(name, static_cast<int>(grid.x * grid.y), kThreads, smem, "head_dim %d rows %lld heads %d",
@@ -590,10 +615,12 @@ atlas_status bwd_hd(const DiffBwdArgs &b, cudaStream_t stream) {
     p.dk[1] = static_cast<float *>(b.dk_g);
     p.dv[0] = static_cast<float *>(b.dv_d);
     p.dv[1] = static_cast<float *>(b.dv_g);
-    const atlas_status st = launch(diff_dq_simt_kernel<HD>, "diff_dq_simt_kernel", p, a,
-                                   floats<HD>(2, 2), stream);
-    return st != ATLAS_OK ? st : launch(diff_dkdv_simt_kernel<HD>, "diff_dkdv_simt_kernel", p, a,
-                                        floats<HD>(2, 3), stream);
+    atlas_status st = launch(diff_dq_simt_kernel<HD>, "diff_dq_simt_kernel", p, a, floats<HD>(2, 2), stream);
+    if (st != ATLAS_OK) return st;
+    p.n_split = diff_split_plan(a.batch, a.n_detail, a.n_global, a.heads, 4);
+    p.split = b.split;
+    st = launch(diff_dkdv_simt_kernel<HD>, "diff_dkdv_simt_kernel", p, a, floats<HD>(2, 3), stream);
+    return st != ATLAS_OK || p.n_split == 1 ? st : launch_diff_split_join(b, p.n_split, stream);
 }
 
 }  // namespace
