@@ -192,9 +192,9 @@ def test_diff_workspace(lib):
     assert atlas.diff_attn_bwd_workspace(2, 100, 7, 3, 64, atlas.BF16) == rows   # too short to cut
     # 40 long units of one head: cut into parts of dV and dK sums
     base, cut = 4 * (2 * 85680 + 64), 4 * 5040 * 2 * 128
-    extra = atlas.diff_attn_bwd_workspace(1, 80640, 5040, 1, 128, atlas.BF16) - base
-    assert extra > cut and extra % cut == 0
-    assert atlas.diff_attn_bwd_workspace(1, 80640, 5040, 1, 128, atlas.FP32) == base
+    for dtype in (atlas.BF16, atlas.FP32):
+        extra = atlas.diff_attn_bwd_workspace(1, 80640, 5040, 1, 128, dtype) - base
+        assert extra > cut and extra % cut == 0
     for bad in ((0, 1, 1, 1, 64), (1, -1, 1, 1, 64), (1, 1, 1, 0, 64), (1, 1 << 31, 0, 1, 64),
                 (2, 1 << 30, 0, 1, 64), (1, 1, 1, 1, 32)):
         assert atlas.diff_attn_bwd_workspace(*bad, atlas.BF16) == 0

@@ -13,7 +13,7 @@
 #include <stdint.h>
 
 #include "atlas_internal.cuh"
-#include "sm100_ptx.cuh"
+#include "sm100_diff.cuh"
 
 namespace atlas {
 namespace units {

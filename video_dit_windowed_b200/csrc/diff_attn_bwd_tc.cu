@@ -47,7 +47,7 @@
 #include <cuda_bf16.h>
 
 #include "attn_units.cuh"
-#include "sm100_ptx.cuh"
+#include "sm100_diff.cuh"
 
 namespace atlas {
 namespace {
@@ -262,7 +262,7 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD, FORM> &sm) {
 }
 
 // ---------------------------------------------------------------------------
-// MMA issuers, each one converged warp (sm100_ptx.cuh, mma_ss_elect): S and dP of
+// MMA issuers, each one converged warp (sm100_diff.cuh): S and dP of
 // tile t as soon as tile t-1 was loaded; the products of P and dS when they are
 // stored. They share no accumulator, and each one's waits and issues take the
 // time of the other's MMAs. Tensor memory starts at column 0, so its addresses

@@ -42,7 +42,7 @@
 #include <type_traits>
 
 #include "attn_units.cuh"
-#include "sm100_ptx.cuh"
+#include "sm100_diff.cuh"
 
 namespace atlas {
 namespace {
@@ -219,7 +219,7 @@ __device__ void producer(const Params &p, const Sched &S, Smem<HD> &sm) {
 }
 
 // ---------------------------------------------------------------------------
-// MMA issuer of map m: one converged warp (sm100_ptx.cuh, mma_ss_elect). Each
+// MMA issuer of map m: one converged warp (sm100_diff.cuh). Each
 // map's products depend only on its own, so each map has a warp to issue them; one
 // warp for both took 3550 clk of waits and issues per tile (D = 128). Tensor
 // memory starts at column 0, so its addresses are constants.
