@@ -83,58 +83,16 @@ __global__ void __launch_bounds__(kWarps * 32) lambda_kernel(const LambdaPtr p) 
 // NaN where the row's lse is not finite (as <do, .> is where do is not), so a NaN
 // here marks every query row that holds a non-finite value: the tensor-core
 // kernel tells such a row from its neighbours in a tile by it.
-// bf16 rows of at most kFewKeys keys: o and s were rounded to 8 bits, and where few
-// keys share the weight dP - D = sum of the others' weights times differences is
-// often far smaller than D, so those rows' D is summed from P and dP themselves
-// (two keys, D = 128: dq's error 0.59% with the stored outputs; eight: 0.28%).
 // ---------------------------------------------------------------------------
-constexpr int kFewKeys = 8;
-
 template <typename T>
 struct DeltaPtr {
     const T *o_d, *s_d, *do_d, *o_g, *s_g, *do_g;
-    const T *q[2], *k[2], *v[2];   // [0] detail, [1] global
     const float *lambda, *lse;
-    float scale;
     int32_t n_lambda;
     float *delta;
 };
 
-// D_1 and D_2 of a row with at most kFewKeys keys, by a warp; others are left.
 template <typename T, int HD>
-__device__ __noinline__ void few_keys(const DeltaPtr<T> &p, const AttnGeom &g,
-                                      const geo::RowAt &at, int head, int64_t col, float &d1,
-                                      float &d2) {
-    int64_t a0 = 0, a1 = 0, b0 = 0, b1 = g.G;
-    if (at.detail) geo::global_keys(g, geo::window_at(g, at.local, a0, a1), b0, b1);
-    if (a1 - a0 + b1 - b0 > kFewKeys) return;
-    const int lane = threadIdx.x & 31, n_a = static_cast<int>(a1 - a0),
-              n = n_a + static_cast<int>(b1 - b0);
-    const int64_t off = (at.row * g.heads + head) * HD;
-    const T *q = p.q[at.detail ? 0 : 1] + off, *d = (at.detail ? p.do_d : p.do_g) + off;
-    const float l1 = p.lse[col], l2 = p.lse[col + g.N + g.G];
-    d1 = d2 = 0.f;
-    for (int j = 0; j < n; ++j) {
-        const int side = j < n_a ? 0 : 1;
-        const int64_t row = at.b * (side ? g.G : g.N) + (side ? b0 + j - n_a : a0 + j);
-        const T *k = p.k[side] + (row * g.heads + head) * HD;
-        const T *v = p.v[side] + (row * g.heads + head) * HD;
-        float s[2] = {0.f, 0.f}, dp = 0.f;
-#pragma unroll
-        for (int e = 0; e < HD / 32; ++e) {
-            const int c = lane + 32 * e;
-            s[e / (HD / 64)] = fmaf(to_f(q[c]), to_f(k[c]), s[e / (HD / 64)]);
-            dp = fmaf(to_f(d[c]), to_f(v[c]), dp);
-        }
-        dp = warp_sum(dp);
-        d1 = fmaf(expf(fmaf(warp_sum(s[0]), p.scale, -l1)), dp, d1);
-        d2 = fmaf(expf(fmaf(warp_sum(s[1]), p.scale, -l2)), dp, d2);
-    }
-}
-
-// FEW: rows with at most kFewKeys keys are possible, of bf16 (without: 720p, one
-// head, 21 us; with the test for them 49 us).
-template <typename T, int HD, bool FEW>
 __global__ void __launch_bounds__(kWarps * 32) diff_delta_kernel(const DeltaPtr<T> p,
                                                                  const AttnGeom g) {
     const int lane = threadIdx.x & 31;
@@ -157,13 +115,71 @@ __global__ void __launch_bounds__(kWarps * 32) diff_delta_kernel(const DeltaPtr<
     const int64_t rows = g.N + g.G;
     const int64_t col = (at.b * g.heads + head) * 2 * rows +
                         (at.detail ? at.local : g.N + at.local);
-    float d1 = fmaf(p.lambda[p.n_lambda == 1 ? 0 : head], sum_s, sum_o);
-    if (FEW) few_keys<T, HD>(p, g, at, head, col, d1, sum_s);
     if (lane == 0) {
+        const float d1 = fmaf(p.lambda[p.n_lambda == 1 ? 0 : head], sum_s, sum_o);
         // 0 for finite values, NaN otherwise
         const float mark = 0.f * p.lse[col] + 0.f * p.lse[col + rows] + 0.f * d1 + 0.f * sum_s;
         p.delta[col] = d1 + mark;
         p.delta[col + rows] = sum_s + mark;
+    }
+}
+
+// bf16 rows of at most kFewKeys keys again: o and s were rounded to 8 bits, and where
+// few keys share the weight dP - D, the other keys' weights times differences, is
+// often far smaller than D, so those rows' D is summed from P and dP themselves
+// (two keys, D = 128: dq's error 0.59% with the stored outputs; eight: 0.28%).
+// A block per window (and one for the global rows), a warp per row: as a test in the
+// kernel above it cost every row the search of its window (6 -> 25 us for 2 x 4 heads
+// of 2,641 rows with offsets).
+constexpr int kFewKeys = kWarps;
+
+struct FewPtr {
+    const __nv_bfloat16 *q[2], *k[2], *v[2], *go[2];   // [0] detail, [1] global
+    const float *lse;
+    float *delta;
+    float scale;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kWarps * 32) diff_few_keys_kernel(const FewPtr p,
+                                                                    const AttnGeom g,
+                                                                    int64_t n_win) {
+    const int lane = threadIdx.x & 31, slot = threadIdx.x / 32, head = blockIdx.y;
+    const int64_t b = blockIdx.x / (n_win + 1), w = blockIdx.x - b * (n_win + 1);
+    const bool detail = w < n_win;
+    int64_t a0 = 0, a1 = 0, b0 = 0, b1 = g.G;
+    if (detail) {
+        a0 = g.win_off ? geo::clamp64(__ldg(g.win_off + w), 0, g.N) : w * g.L;
+        a1 = g.win_off ? geo::clamp64(__ldg(g.win_off + w + 1), a0, g.N) : a0 + g.L;
+        geo::global_keys(g, w, b0, b1);
+    }
+    if (a1 - a0 + b1 - b0 > kFewKeys || slot >= (detail ? a1 - a0 : b1 - b0)) return;
+    const int n_a = static_cast<int>(a1 - a0), n = n_a + static_cast<int>(b1 - b0);
+    const int64_t rows = g.N + g.G, local = (detail ? a0 : b0) + slot;
+    const int64_t off = ((b * (detail ? g.N : g.G) + local) * g.heads + head) * HD;
+    const int64_t col = (b * g.heads + head) * 2 * rows + (detail ? local : g.N + local);
+    const __nv_bfloat16 *q = p.q[detail ? 0 : 1] + off, *d = p.go[detail ? 0 : 1] + off;
+    const float l1 = p.lse[col], l2 = p.lse[col + rows];
+    float d1 = 0.f, d2 = 0.f;
+    for (int j = 0; j < n; ++j) {
+        const int side = j < n_a ? 0 : 1;
+        const int64_t row = b * (side ? g.G : g.N) + (side ? b0 + j - n_a : a0 + j);
+        const __nv_bfloat16 *k = p.k[side] + (row * g.heads + head) * HD;
+        const __nv_bfloat16 *v = p.v[side] + (row * g.heads + head) * HD;
+        float s[2] = {0.f, 0.f}, dp = 0.f;
+#pragma unroll
+        for (int e = 0; e < HD / 32; ++e) {
+            const int c = lane + 32 * e;
+            s[e / (HD / 64)] = fmaf(to_f(q[c]), to_f(k[c]), s[e / (HD / 64)]);
+            dp = fmaf(to_f(d[c]), to_f(v[c]), dp);
+        }
+        dp = warp_sum(dp);
+        d1 = fmaf(expf(fmaf(warp_sum(s[0]), p.scale, -l1)), dp, d1);
+        d2 = fmaf(expf(fmaf(warp_sum(s[1]), p.scale, -l2)), dp, d2);
+    }
+    if (lane == 0) {   // (NaN marks stay)
+        p.delta[col] = d1 + 0.f * p.delta[col];
+        p.delta[col + rows] = d2 + 0.f * p.delta[col + rows];
     }
 }
 
@@ -274,21 +290,43 @@ atlas_status delta_hd(const DiffBwdArgs &b, cudaStream_t stream) {
     p.o_g = static_cast<const T *>(a.o_g);
     p.s_g = static_cast<const T *>(b.fwd.s_g);
     p.do_g = static_cast<const T *>(b.do_g);
-    p.q[0] = static_cast<const T *>(a.q_d);
-    p.q[1] = static_cast<const T *>(a.q_g);
-    p.k[0] = static_cast<const T *>(a.k_d);
-    p.k[1] = static_cast<const T *>(a.k_g);
-    p.v[0] = static_cast<const T *>(a.v_d);
-    p.v[1] = static_cast<const T *>(a.v_g);
-    p.scale = a.scale;
     p.lambda = b.fwd.lambda;
     p.n_lambda = b.fwd.n_lambda;
     p.lse = a.lse;
     p.delta = b.delta;
     log_rows("diff_delta_kernel", a);
-    const bool few = sizeof(T) == 2 && (a.n_global <= kFewKeys || a.gwin_off != nullptr);
-    if (few) diff_delta_kernel<T, HD, true><<<row_grid(a), kWarps * 32, 0, stream>>>(p, attn_geom_of(a));
-    else diff_delta_kernel<T, HD, false><<<row_grid(a), kWarps * 32, 0, stream>>>(p, attn_geom_of(a));
+    diff_delta_kernel<T, HD><<<row_grid(a), kWarps * 32, 0, stream>>>(p, attn_geom_of(a));
+    return launched();
+}
+
+// Launched where rows with few keys are possible.
+template <int HD>
+atlas_status few_hd(const DiffBwdArgs &b, cudaStream_t stream) {
+    const AttnArgs &a = b.fwd.attn;
+    const bool global_rows = a.n_global > 0 && a.n_global <= kFewKeys;
+    const bool detail_rows = a.n_detail > 0 && (a.win_off || a.window_len <= kFewKeys) &&
+                             (a.n_global <= kFewKeys || a.gwin_off);
+    if (!global_rows && !detail_rows) return ATLAS_OK;
+    const int64_t n_win = !detail_rows ? 0 : a.win_off ? a.n_win : a.n_detail / a.window_len;
+    FewPtr p;
+    p.q[0] = static_cast<const __nv_bfloat16 *>(a.q_d);
+    p.q[1] = static_cast<const __nv_bfloat16 *>(a.q_g);
+    p.k[0] = static_cast<const __nv_bfloat16 *>(a.k_d);
+    p.k[1] = static_cast<const __nv_bfloat16 *>(a.k_g);
+    p.v[0] = static_cast<const __nv_bfloat16 *>(a.v_d);
+    p.v[1] = static_cast<const __nv_bfloat16 *>(a.v_g);
+    p.go[0] = static_cast<const __nv_bfloat16 *>(b.do_d);
+    p.go[1] = static_cast<const __nv_bfloat16 *>(b.do_g);
+    p.lse = a.lse;
+    p.delta = b.delta;
+    p.scale = a.scale;
+    const int64_t blocks = a.batch * (n_win + 1);
+    if (blocks > INT32_MAX) return ATLAS_ERR_SHAPE;
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(a.heads));
+    if (log_enabled())
+        log_launch("diff_few_keys_kernel", static_cast<int>(grid.x * grid.y), kWarps * 32, 0,
+                   "head_dim %d windows %lld heads %d", HD, static_cast<long long>(n_win), a.heads);
+    diff_few_keys_kernel<HD><<<grid, kWarps * 32, 0, stream>>>(p, attn_geom_of(a), n_win);
     return launched();
 }
 
@@ -374,9 +412,13 @@ atlas_status launch_diff_lambda(const DiffLambdaArgs &a, bool bwd, cudaStream_t 
 }
 
 atlas_status launch_diff_bwd_delta(const DiffBwdArgs &b, cudaStream_t stream) {
-    if (b.fwd.elem_bytes == 2)
-        return b.fwd.attn.head_dim == 128 ? delta_hd<__nv_bfloat16, 128>(b, stream)
-                                          : delta_hd<__nv_bfloat16, 64>(b, stream);
+    if (b.fwd.elem_bytes == 2) {
+        const bool wide = b.fwd.attn.head_dim == 128;
+        const atlas_status st = wide ? delta_hd<__nv_bfloat16, 128>(b, stream)
+                                     : delta_hd<__nv_bfloat16, 64>(b, stream);
+        if (st != ATLAS_OK) return st;
+        return wide ? few_hd<128>(b, stream) : few_hd<64>(b, stream);
+    }
     return b.fwd.attn.head_dim == 128 ? delta_hd<float, 128>(b, stream)
                                       : delta_hd<float, 64>(b, stream);
 }

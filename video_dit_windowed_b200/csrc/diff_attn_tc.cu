@@ -65,7 +65,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8
-constexpr int kFewTiles = 4;   // of 128 keys (softmax_epilogue)
+constexpr int kFewKeys = 32;   // softmax_epilogue
 
 template <int HD>
 struct Smem {
@@ -465,11 +465,13 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
         const float lam = __ldg(p.lambda + (p.n_lambda == 1 ? 0 : U.head));
         // The reference m_run (log2 units) is whole, so that moving it scales by a
         // power of two, exactly.
-        // l_fix: what the sum of the weights changes by their rounding, in units of
-        // few tiles. O is divided by the sum of the weights as its products had them,
-        // so that a row with one key gets its V exactly and a row with few keys no
-        // common error, which o_1 - lambda o_2 would enlarge. Over many tiles it
-        // averages out (and two instructions a weight cost 2%).
+        // l_fix: what the sum of the weights changes by their rounding, in warps with a
+        // row of at most kFewKeys keys (which only masked tiles hold). O is divided by
+        // the sum of the weights as its products had them, so that a row with one key
+        // gets its V exactly and a row with few keys no common error, which o_1 -
+        // lambda o_2 would enlarge. Over many keys it averages out (and two
+        // instructions more for every weight cost 2%).
+        const bool few = __any_sync(kAll, valid && db - da + gb - ga <= kFewKeys);
         float m_run = kNegInf, l_run = 0.f, l_fix = 0.f;
         bool bad = false;
         // The bad rows of tile j (tile count c), which this map's threads wrote
@@ -524,7 +526,7 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                 const float m = m_run == kNegInf ? 0.f : m_run;
                 exps_all(lo, m, t_lo, sum);
                 exps_all(hi, m, t_lo + 32, sum);
-                if (n <= kFewTiles) {
+                if (few) {
                     float s0, s1;
                     ptx::unpack(sum, s0, s1);
                     l_fix += rounded_sum(t_lo) - (s0 + s1);
