@@ -34,6 +34,11 @@
 // zeroed in shared memory before the product. In packed units (PACK), whose rows
 // see different windows, so are V rows with a non-finite value, and the rows that
 // do see such a key become NaN in the epilogue.
+// Measured: 720p (80,640 + 5,040 rows, windows of 768), 4 heads, D = 128: 1,613 us,
+// 0.94 PFLOP/s (products alone 923 us, exponentials alone 878); 32,760 tokens, D = 64:
+// 860-930 us (exponentials 477). What is left is issue: a softmax warp's other
+// instructions (fma, maximum, sum, pack, store) share its scheduler with the
+// exponentials.
 // Every wait is bounded: on expiry a bit is set in the device error word, the
 // CTA drains its copies and MMAs, frees its tensor memory and returns.
 #include <cuda.h>

@@ -17,6 +17,10 @@
 //             whole GPU, partial sums per channel are joined by a second kernel,
 //             and a third writes the result, walking the rows backwards so that
 //             it starts with the rows that are still in L2.
+// Measured: 80,640 tokens of 40 heads of 128, bf16, 348 us for 1.65 GB (4.7 TB/s,
+// 72% of a copy); decoder latents 2 x 322,560 x 128, SiLU, forward and backward 308 us
+// (0.83 GB: 2.7 TB/s; the sums' passes and their joins are launches of their own);
+// 3 x 1,001 x 60, fp32, 37 us, launches.
 // Variances are sums of squared deviations: from the mean where the values are
 // held (heads, resident), else from a value of the same channel, joined in fp64, so
 // a large mean costs no digits of the deviations.
