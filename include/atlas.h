@@ -609,7 +609,8 @@ atlas_status atlas_diff_lambda_bwd(const void *q1, const void *k1, const void *q
  * both maps' softmax denominators.
  * BF16: tcgen05 kernel, both maps' softmax and both outputs in fp32, each map's
  * unnormalised weights rounded to bf16 before their product with v (rows of at most
- * 32 keys are divided by the sum of the rounded weights), o rounded once. FP32: exact fp32 products. head_dim 64 or 128.
+ * 32 keys are divided by the sum of the rounded weights), o rounded once. FP32:
+ * exact fp32 products. head_dim 64 or 128.
  * A row's result depends on no key that it does not see, whatever that key holds
  * (infinities and NaN included). BF16, windows below 128 rows: a row that sees a
  * key whose v is not finite is NaN in all its channels.
@@ -633,9 +634,9 @@ atlas_status atlas_diff_attn(const void *q_d, const void *k_d, const void *v_d,
  * (summed over the heads as well when n_lambda is 1). dS is 0, exactly, for a query
  * with one key. BF16: D_m of the stored outputs is corrected by the row sums of dS_m
  * before dlambda and dk; W = P_1 - lambda P_2 and dS are rounded to bf16 before their
- * products. As in the forward pass, a row
- * that is not met by a query or key does not reach its gradients; a query whose
- * do is not finite makes the whole dv rows (BF16) of the keys it sees NaN.
+ * products. As in the forward pass, a row that is not met by a query or key does
+ * not reach its gradients; a query whose do is not finite makes the whole dv rows
+ * (BF16) of the keys it sees NaN.
  * o_*, s_*, lse: the forward's. workspace: DEVICE fp32, 16-byte aligned, of
  * atlas_diff_attn_bwd_workspace bytes, overwritten; calls that overlap on the
  * GPU need one each. dq_*, dk_*, dv_*: as q_*; dlambda: fp32 [n_lambda]. All sums
