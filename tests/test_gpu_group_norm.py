@@ -35,6 +35,7 @@ CASES = [
     (1, 20011, 128, 32),
     (3, 5000, 320, 32),      # groups of ten
     (2, 2500, 2048, 4),      # more than one slice of columns
+    (2, 600, 5120, 4),       # slices of several rows a block
     (1, 3, 8200, 1),
 ]
 

@@ -17,8 +17,8 @@
 //             whole GPU, partial sums per channel are joined by a second kernel,
 //             and a third writes the result, walking the rows backwards so that
 //             it starts with the rows that are still in L2.
-// Measured: 80,640 tokens of 40 heads of 128, bf16, 348 us for 1.65 GB (4.7 TB/s,
-// 72% of a copy); decoder latents 2 x 322,560 x 128, SiLU, forward and backward 308 us
+// Measured: 80,640 tokens of 40 heads of 128, bf16, 314 us for 1.65 GB (5.3 TB/s,
+// 80% of a copy); decoder latents 2 x 322,560 x 128, SiLU, forward and backward 308 us
 // (0.83 GB: 2.7 TB/s; the sums' passes and their joins are launches of their own);
 // 3 x 1,001 x 60, fp32, 37 us, launches.
 // Variances are sums of squared deviations: from the mean where the values are
@@ -632,11 +632,23 @@ struct Plan {
     int64_t part_bytes, coef_bytes;
 };
 
-// nv columns in slices of at most a block's threads, as even as whole warps allow.
+// nv columns in slices of at most a block's threads: the width of whole warps that
+// leaves the fewest threads idle, several rows at a time where it is half a block or
+// less (640 columns: 5 slices of 128, two rows, 314 us for the 40 heads above; 3 of
+// 224, one row, 350). With very many columns the last slice does not matter.
 void slice_columns(int64_t nv, Plan *p) {
-    p->slices_y = (nv + kThreads - 1) / kThreads;
-    const int64_t even = (nv + p->slices_y - 1) / p->slices_y;
-    p->width = static_cast<int32_t>(p->slices_y == 1 ? nv : (even + 31) / 32 * 32);
+    int64_t width = nv <= kThreads ? nv : kThreads, best = 0;
+    if (nv > kThreads && nv <= 64 * kThreads)
+        for (int64_t w = kThreads; w >= 64; w -= 32) {
+            // threads in use, per 2^20
+            const int64_t use = (nv << 20) / ((nv + w - 1) / w * w) * (kThreads / w * w) / kThreads;
+            if (use > best) {
+                best = use;
+                width = w;
+            }
+        }
+    p->slices_y = (nv + width - 1) / width;
+    p->width = static_cast<int32_t>(width);
     p->per_block = kThreads / p->width;
 }
 
@@ -654,7 +666,8 @@ Plan plan_of(const NormArgs &a, bool bwd) {
             p.lanes = static_cast<int>(lanes);
             slice_columns(a.channels / vec, &p);
             const int64_t tokens = (a.samples + p.per_block - 1) / p.per_block;
-            p.grid = std::min<int64_t>(tokens, bwd ? kPartBlocks : 8 * kSms);
+            // (forward, a slice: 2, 4, 5 and 8 blocks an SM 334, 314, 327 and 325 us)
+            p.grid = std::min<int64_t>(tokens, bwd ? kPartBlocks : 4 * kSms);
             p.parts = static_cast<int32_t>(p.grid);
             p.part_bytes = bwd ? p.parts * a.channels * 8 : 0;
             return p;
