@@ -280,3 +280,15 @@ def test_binding_refuses_host_tensors(lib):
         atlas.diff_lambda(x[0], x[0], x[0], x[0], 0.5, torch.ones(2))
     with pytest.raises(ValueError):
         atlas.group_norm(x[:, 0], None, None, x[:, 0], 1, 1)
+
+
+def test_rotary_rows_of_a_tensor():
+    """Row strides as the library takes them: 0 there means contiguous, so a tensor
+    whose rows share memory is refused."""
+    x = torch.zeros(6, 3, 8)
+    assert atlas._rows(x)[1] == 24 and atlas._rows(x[:, 1:])[1] == 24 and atlas._rows(x[::2])[1] == 48
+    assert atlas._rows(x[:1].expand(1, 3, 8))[1] == 24
+    for bad in (x[:1].expand(6, 3, 8), x[:, :1].expand(6, 3, 8), x.transpose(0, 1), x[..., ::2],
+                x.as_strided((6, 3, 8), (8, 8, 1))):
+        with pytest.raises(ValueError):
+            atlas._rows(bad)

@@ -607,8 +607,9 @@ def _rows(t):
     are contiguous, as a slice of a wider buffer's columns is."""
     n, heads, hd = t.shape
     s0, s1, s2 = t.stride()
-    _require((hd == 1 or s2 == 1) and (heads == 1 or s1 == hd),
-             "tensors must be [rows, heads, head_dim] with contiguous rows")
+    # (a row stride of 0, an expanded tensor's, would mean contiguous rows below)
+    _require((hd == 1 or s2 == 1) and (heads == 1 or s1 == hd) and (n <= 1 or s0 >= heads * hd),
+             "tensors must be [rows, heads, head_dim] with contiguous rows, none of them shared")
     return t.data_ptr(), s0 if n > 1 else heads * hd
 
 
