@@ -8,7 +8,7 @@
 // accumulators stay in registers; the weights pass through shared memory within
 // the warp whose rows they are. The row pitch of D + 4 floats spreads the 32 rows
 // that a warp reads side by side over the banks. Bound by latency, not by the FMA
-// pipe or shared memory (2 x 3 heads of 3,600 + 1,000 rows, D = 128, training: 4.0
+// pipe or shared memory (2 x 3 heads of 3,600 + 1,000 rows, D = 128, training: 3.7
 // ms; 256 threads with 4 x 4 scores each took 4.43 ms at 50 % issue, 4 x 2 over
 // 32-row tiles 5.37 ms). dK/dV: the queries of a block over global keys are cut into
 // parts where such blocks are few and long (diff_attn.cu, diff_split_plan; 2 heads of
