@@ -81,7 +81,7 @@ struct Smem {
     alignas(1024) uint8_t kv[kSlots][kTileBytes];
     float inv_l[2][kMaps][kBM];  // by unit parity
     uint32_t bad[kMaps][4][4];   // PACK: non-finite V rows of the last four tiles,
-    uint32_t mark[4][kBM];       // and the tile count of those that map 0 zeroed
+    uint32_t mark[kMaps][4][kBM];   // and the tile count of those that a map zeroed
     uint64_t q_full, q_empty;
     uint64_t kv_full[kSlots];
     uint64_t kv_empty[kSlots];   // (and q_empty, o_final: a commit by each map's issuer)
@@ -589,8 +589,11 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
             ptx::tmem_wait_st();
             // V rows to zero, by both maps' threads (thread = V row), each before
             // its own product. V(j) is load 2 cnt + 1 of the ring, and stays until
-            // both products ran. Of a non-finite row (PACK), map 1's thread may
-            // find the zeros that map 0's wrote: that one leaves its mark first.
+            // both products ran. Nothing orders the maps within a tile, so a thread
+            // that scans a non-finite row (PACK) may find the zeros of the other
+            // map's thread: each leaves its mark before its zeros, and looks for the
+            // other's after its scan. (Four tiles' marks are enough: with at most
+            // eight slots, V(j + 4) is not loaded before both maps are done with V(j).)
             const int32_t seen = units::tile_rows<kBN>(U, j);
             if (seen < kBN || scanned(U, j)) {
                 const uint32_t it = 2 * cnt + 1, slot = it % kSlots;
@@ -608,11 +611,11 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
 #pragma unroll
                         for (int i = 0; i < kVecs; ++i)
                             b |= not_finite(ptx::ld_shared_v4(vec(i)));
+                        volatile uint32_t &own = sm.mark[map][cnt & 3][r];
+                        volatile uint32_t &other = sm.mark[1 - map][cnt & 3][r];
+                        if (b) own = cnt + 1;
                         __threadfence_block();
-                        volatile uint32_t &mark = sm.mark[cnt & 3][r];
-                        if (map == 0 && b) mark = cnt + 1;
-                        if (map == 1) b |= mark == cnt + 1;
-                        __threadfence_block();
+                        b |= other == cnt + 1;
                     }
                     const uint32_t rows = __ballot_sync(kAll, b);
                     if ((r & 31) == 0) sm.bad[map][cnt & 3][r / 32] = rows;
@@ -715,7 +718,6 @@ __global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_const
             ptx::mbar_init(ptx::smem_addr(&sm.drain[m]), 1);
         }
         ptx::mbar_init(ptx::smem_addr(&sm.o_final), kMaps);
-        for (int i = 0; i < 4 * kBM; ++i) sm.mark[i / kBM][i % kBM] = 0;
         ptx::mbar_init(ptx::smem_addr(&sm.joined), kMaps * kBM);
         ptx::mbar_init(ptx::smem_addr(&sm.o_empty), kMaps * kBM);
         sm.abort = 0;
@@ -723,6 +725,9 @@ __global__ void __launch_bounds__(kThreads, 1) diff_tc_kernel(const __grid_const
         sm.err_word = p.err_word;
         ptx::fence_mbar_init();
     }
+    if (PACK)
+        for (int i = threadIdx.x; i < kMaps * 4 * kBM; i += kThreads)
+            sm.mark[i / (4 * kBM)][i / kBM % 4][i % kBM] = 0;
     if (warp == kMmaWarp) {
         ptx::tmem_alloc(ptx::smem_addr(&sm.tmem_base), kTmemCols);
         ptx::tmem_relinquish();
