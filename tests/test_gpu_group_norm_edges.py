@@ -1,0 +1,30 @@
+"""Group norm: addresses, lengths and values at the edges of what the call allows."""
+import pytest
+import torch
+
+from test_gpu_group_norm import DEV, DT, rnd
+from video_dit_windowed_b200 import atlas
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", [(301, 1, 1280, 10), (5, 9, 24, 3), (2, 9000, 64, 4)], ids=str)
+def test_fp32_arrays_on_a_4_byte_boundary(case, dtype):
+    """stats, gamma, beta, dgamma and dbeta one float behind a 16-byte boundary: the
+    same bits as on one, in each of the three forms."""
+    S, R, C, K = case
+    x, dy = rnd(S * R, C, dtype=DT[dtype]), rnd(S * R, C, seed=1, dtype=DT[dtype])
+
+    def run(shift):
+        at = lambda n: torch.full((n + shift,), 9.0, device=DEV)[shift:]  # noqa: E731
+        gamma, beta = at(C).copy_(1 + 0.2 * rnd(C, seed=2)), at(C).copy_(0.2 * rnd(C, seed=3))
+        stats, dg, db = at(2 * S * K), at(C), at(C)
+        assert all(t.data_ptr() % 16 == 4 * shift for t in (gamma, beta, stats, dg, db))
+        y, dx = torch.empty_like(x), torch.empty_like(x)
+        atlas.group_norm(x, gamma, beta, y, R, K, activation="silu", stats=stats)
+        atlas.group_norm_bwd(dy, x, gamma, beta, stats, dx, dg, db, R, K, activation="silu")
+        return y, stats, dx, dg, db
+
+    for a, b in zip(run(0), run(1)):
+        assert torch.equal(a, b)

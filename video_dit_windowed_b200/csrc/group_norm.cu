@@ -50,7 +50,7 @@ struct Params {
     const void *x, *dy;
     void *out;                      // y or dx
     const float *gamma, *beta;
-    float2 *stats;                  // (mean, rstd) of every (sample, group); may be NULL forward
+    float *stats;                   // (mean, rstd) of every (sample, group); may be NULL forward
     float *dgamma, *dbeta;
     int64_t samples, rows, channels;
     int32_t groups, cg, silu;
@@ -109,6 +109,14 @@ struct Pack {
 template <typename T, int V>
 struct alignas(V > 1 ? 16 : sizeof(T)) Vec : Pack<T, V> {};
 
+// The caller's statistics lie on a 4-byte boundary, not on a float2's.
+__device__ __forceinline__ float2 stat_of(const Params &p, int64_t i) {
+    return make_float2(__ldg(p.stats + 2 * i), __ldg(p.stats + 2 * i + 1));
+}
+__device__ __forceinline__ void put_stat(const Params &p, int64_t i, float mean, float rstd) {
+    p.stats[2 * i] = mean;
+    p.stats[2 * i + 1] = rstd;
+}
 __device__ __forceinline__ float gamma_of(const Params &p, int64_t c) {
     return p.gamma ? __ldg(p.gamma + c) : 1.f;
 }
@@ -178,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) norm_heads_kernel(const Params p) {
             xv[f].load_last(x + at);
             if (BWD) {
                 gv[f].load_last(dy + at);
-                st[f] = __ldg(p.stats + (on ? s * p.groups + group : 0));
+                st[f] = stat_of(p, on ? s * p.groups + group : 0);
             }
         }
 #pragma unroll
@@ -198,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) norm_heads_kernel(const Params p) {
                 for (int e = 0; e < V; ++e)
                     o.set(e, act(fmaf((xv[f][e] - mean) * rstd, ga[e], be[e]), p.silu));
                 if (on && p.stats != nullptr && col % LANES == 0)
-                    p.stats[s * p.groups + group] = make_float2(mean, rstd);
+                    put_stat(p, s * p.groups + group, mean, rstd);
             } else {
                 float hat[V], dh[V], s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -319,9 +327,9 @@ __global__ void __launch_bounds__(kThreads) norm_resident_kernel(const Params p)
                                       beta_of(p, ch0 + c + e)), p.silu));
                 o.store(out + at);
             }
-            if (on && lane == 0 && p.stats != nullptr) p.stats[stat] = make_float2(mean, rstd);
+            if (on && lane == 0 && p.stats != nullptr) put_stat(p, stat, mean, rstd);
         } else {
-            const float2 st = on ? __ldg(p.stats + stat) : make_float2(0.f, 0.f);
+            const float2 st = on ? stat_of(p, stat) : make_float2(0.f, 0.f);
             float s1 = 0.f, s2 = 0.f;
             for (int64_t i = lane; i < n_items; i += team) {
                 place(i, at, in, c);
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) norm_resident_kernel(const Params p)
                 // dgamma, dbeta: thread = channel, rows in order
                 __syncthreads();
                 for (int k = threadIdx.x; k < ng * p.cg; k += kThreads) {
-                    const float2 sk = __ldg(p.stats + s * p.groups + g0 + k / p.cg);
+                    const float2 sk = stat_of(p, s * p.groups + g0 + k / p.cg);
                     const float ga = gamma_of(p, ch0 + k), be = beta_of(p, ch0 + k);
                     float2 a = acc[k];
                     for (int64_t r = 0; r < p.rows; ++r) {
@@ -421,7 +429,7 @@ __global__ void __launch_bounds__(kThreads) norm_split_sums_kernel(const Params 
             if (BWD) {
                 ga[e] = gamma_of(p, ch + e);
                 be[e] = beta_of(p, ch + e);
-                st[e] = __ldg(p.stats + s * p.groups + (ch + e) / p.cg);
+                st[e] = stat_of(p, s * p.groups + (ch + e) / p.cg);
             } else {
                 st[e].x = first[e];
             }
@@ -559,7 +567,7 @@ __global__ void __launch_bounds__(kThreads) norm_split_join_kernel(const Params 
     if (threadIdx.x == 0) {
         const float2 st = make_float2(static_cast<float>(s1), rsqrtf(static_cast<float>(s2) + p.eps));
         p.coef[w] = st;
-        if (p.stats != nullptr) p.stats[w] = st;
+        if (p.stats != nullptr) put_stat(p, w, st.x, st.y);
     }
 }
 
@@ -583,7 +591,7 @@ __global__ void __launch_bounds__(kThreads) norm_split_apply_kernel(const Params
         const int64_t w = s * p.groups + (ch + e) / p.cg;
         ga[e] = gamma_of(p, ch + e);
         be[e] = beta_of(p, ch + e);
-        st[e] = BWD ? __ldg(p.stats + w) : p.coef[w];
+        st[e] = BWD ? stat_of(p, w) : p.coef[w];
         mm[e] = BWD ? p.coef[w] : make_float2(0.f, 0.f);
     }
     for (int64_t r = r1 - 1 - t.sub; r >= r0; r -= kFlight * p.per_block) {
@@ -788,7 +796,7 @@ atlas_status launch_group_norm(const NormArgs &a, bool bwd, cudaStream_t stream)
     p.out = a.out;
     p.gamma = a.gamma;
     p.beta = a.beta;
-    p.stats = reinterpret_cast<float2 *>(a.stats);
+    p.stats = a.stats;
     p.dgamma = a.dgamma;
     p.dbeta = a.dbeta;
     p.samples = a.samples;
