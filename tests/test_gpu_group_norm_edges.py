@@ -28,3 +28,25 @@ def test_fp32_arrays_on_a_4_byte_boundary(case, dtype):
 
     for a, b in zip(run(0), run(1)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", [(400, 20000, 32, 8, 1), (400, 20000, 32, 8, 9000), (200, 1500, 1024, 64, 1),
+                                  (2, 60000, 64, 4, 1), (30, 5000, 60, 12, 700)], ids=str)
+def test_variance_after_unlike_first_rows(case, dtype):
+    """The first rows of every sample are zeros (padding), the others lie around 1000
+    with deviation 1. A thread sums at most 1,024 rows, of squares below four times
+    what stays when it re-centres (2^-24 of each, 4 + 16 + .. rows): 8 * 1024 * 2^-24
+    of the variance; half of it in rstd. The mean: 2^-23 of its magnitude a step."""
+    S, R, C, K, zeros = case
+    x = (1000 + rnd(S * R, C)).to(DT[dtype])
+    x.view(S, R, C)[:, :zeros] = 0
+    y, stats = torch.empty_like(x), torch.empty(S, K, 2, device=DEV)
+    atlas.group_norm(x, None, None, y, R, K, stats=stats)
+    for s in range(0, S, 50):
+        part = x.view(S, R, K, C // K)[s:s + 50].double()
+        mean = part.mean((1, 3))
+        rstd = ((part - mean[:, None, :, None]).square().mean((1, 3)) + 1e-5).rsqrt()
+        got = stats[s:s + 50].double()
+        assert float((got[..., 1] / rstd - 1).abs().max()) <= 4 * 1024 * 2.0 ** -24
+        assert float((got[..., 0] / mean - 1).abs().max()) <= 2.0 ** -21

@@ -22,8 +22,9 @@
 // (0.83 GB: 2.7 TB/s; the sums' passes and their joins are launches of their own);
 // 3 x 1,001 x 60, fp32, 37 us, launches.
 // Variances are sums of squared deviations: from the mean where the values are
-// held (heads, resident), else from a value of the same channel, joined in fp64, so
-// a large mean costs no digits of the deviations.
+// held (heads, resident), else from a pivot that a thread moves to the mean of its
+// rows so far (split), joined in fp64, so that neither a large mean nor a first row
+// unlike the others costs digits of the deviations.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -403,9 +404,12 @@ __device__ __forceinline__ Slot slot_of(const Params &p, int64_t nv) {
     return t;
 }
 
-// Forward: part [sample][chunk][channel] = (mean, M2) of the chunk's rows, from
-// sums of deviations from the chunk's first value of the channel. Backward: (sum
-// dz xhat, sum dz).
+// Forward: part [sample][chunk][channel] = (mean, M2) of the chunk's rows. A thread
+// sums deviations from a pivot, its first value of the channel, and their squares.
+// M2 = sum d^2 - (sum d)^2 / n loses what a pivot far from the mean makes the two
+// share, so after 4, 16, 64, .. rows the pivot moves to their mean: among n rows of
+// which k have mean 0 (about the pivot), M2 is at least k/n of sum d^2, so no move and
+// no end takes away more than two bits. Backward: (sum dz xhat, sum dz).
 template <typename T, int V, bool BWD>
 __global__ void __launch_bounds__(kThreads) norm_split_sums_kernel(const Params p) {
     constexpr int kFlight = 4;
@@ -423,7 +427,8 @@ __global__ void __launch_bounds__(kThreads) norm_split_sums_kernel(const Params 
         float ga[V], be[V];
         float2 st[V];   // forward: the pivot
         Vec<T, V> first;
-        first.load(x + r0 * p.channels);
+        first.load(x + min(r0 + t.sub, r1 - 1) * p.channels);
+        int64_t n = 0, move_at = kFlight;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             if (BWD) {
@@ -457,6 +462,27 @@ __global__ void __launch_bounds__(kThreads) norm_split_sums_kernel(const Params 
                         b[e] = fmaf(d, d, b[e]);
                     }
                 }
+                ++n;
+            }
+            if (!BWD && n == move_at) {
+                const float fn = static_cast<float>(n), inv = 1.f / fn;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float to = fmaf(a[e], inv, st[e].x), by = to - st[e].x;
+                    b[e] = fmaxf(fmaf(-by, 2.f * a[e] - fn * by, b[e]), 0.f);
+                    a[e] = fmaf(-fn, by, a[e]);
+                    st[e].x = to;
+                }
+                move_at *= 4;
+            }
+        }
+        if (!BWD && n > 0) {   // to (mean, M2)
+            const float inv = 1.f / static_cast<float>(n);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float d = a[e] * inv;
+                b[e] = fmaxf(fmaf(-d, a[e], b[e]), 0.f);
+                a[e] = st[e].x + d;
             }
         }
     }
@@ -468,14 +494,28 @@ __global__ void __launch_bounds__(kThreads) norm_split_sums_kernel(const Params 
         const int64_t c = static_cast<int64_t>(blockIdx.y) * p.width * V + i;
         if (c >= p.channels) break;
         float2 q = sums[i / V][i % V];
-        for (int k = 1; k < p.per_block; ++k) {
-            q.x += sums[k * p.width + i / V][i % V].x;
-            q.y += sums[k * p.width + i / V][i % V].y;
-        }
-        if (!BWD) {
-            const float d = q.x / static_cast<float>(r1 - r0);
-            q.y = fmaxf(fmaf(-d, q.x, q.y), 0.f);
-            q.x = Io<T>::get(static_cast<const T *>(p.x)[(s * p.rows + r0) * p.channels + c]) + d;
+        if (BWD) {
+            for (int k = 1; k < p.per_block; ++k) {
+                q.x += sums[k * p.width + i / V][i % V].x;
+                q.y += sums[k * p.width + i / V][i % V].y;
+            }
+        } else {
+            // The threads' (mean, M2), about the first one's mean; thread k has
+            // `each` rows, the first `more` threads one more.
+            const int rows = static_cast<int>(r1 - r0), each = rows / p.per_block;
+            const int more = rows - each * p.per_block, last = min(p.per_block, rows);
+            const float inv = 1.f / static_cast<float>(rows);
+            float d = 0.f, m2 = 0.f;
+            for (int k = 1; k < last; ++k)
+                d = fmaf(static_cast<float>(each + (k < more)),
+                         sums[k * p.width + i / V][i % V].x - q.x, d);
+            d *= inv;
+            for (int k = 0; k < last; ++k) {
+                const float2 w = sums[k * p.width + i / V][i % V];
+                const float off = w.x - q.x - d;
+                m2 += fmaf(static_cast<float>(each + (k < more)) * off, off, w.y);
+            }
+            q = make_float2(q.x + d, m2);
         }
         p.part[blockIdx.x * p.channels + c] = q;
     }
