@@ -50,3 +50,38 @@ def test_variance_after_unlike_first_rows(case, dtype):
         got = stats[s:s + 50].double()
         assert float((got[..., 1] / rstd - 1).abs().max()) <= 4 * 1024 * 2.0 ** -24
         assert float((got[..., 0] / mean - 1).abs().max()) <= 2.0 ** -21
+
+
+def test_samples_longer_than_a_chunk():
+    """Many samples, each in chunks of 1,024 rows and a rest: statistics and all
+    gradients. fp32 sums of at most 1,024 terms a thread and a few hundred parts:
+    2^-24 * 1,536 of the terms' magnitudes, as test_variance_after_unlike_first_rows."""
+    S, R, C, K = 40, 1100, 8192, 64
+    x, dy = rnd(S * R, C) + 3, rnd(S * R, C, seed=1)
+    gamma = 1 + 0.2 * rnd(C, seed=2)
+    y, dx, stats = torch.empty_like(x), torch.empty_like(x), torch.empty(S, K, 2, device=DEV)
+    dg, db = torch.empty(C, device=DEV), torch.empty(C, device=DEV)
+    atlas.group_norm(x, gamma, None, y, R, K, stats=stats)
+    atlas.group_norm_bwd(dy, x, gamma, None, stats, dx, dg, db, R, K)
+    tol = 1536 * 2.0 ** -24
+    want_g, size_g, want_b, size_b = torch.zeros(4, C, dtype=torch.float64, device=DEV)
+    for s in range(S):
+        rows = slice(s * R, (s + 1) * R)
+        a, g = x[rows].double().view(R, K, -1), dy[rows].double()
+        mean, var = a.mean((0, 2), keepdim=True), a.var((0, 2), unbiased=False, keepdim=True)
+        rstd = (var + 1e-5).rsqrt()
+        assert float((stats[s, :, 1].double() / rstd.flatten() - 1).abs().max()) <= tol / 2
+        hat = ((a - mean) * rstd).view(R, C)
+        # y: xhat's own roundings and the statistics' errors (of means of order 3)
+        assert float((y[rows].double() - hat * gamma.double()).abs().max()) <= 10 * tol
+        want_g += (g * hat).sum(0)
+        size_g += (g * hat).abs().sum(0)
+        want_b += g.sum(0)
+        size_b += g.abs().sum(0)
+        dh = (g * gamma.double()).view(R, K, -1)
+        h = hat.view(R, K, -1)
+        want = rstd * (dh - dh.mean((0, 2), keepdim=True) - h * (dh * h).mean((0, 2), keepdim=True))
+        assert float((dx[rows].double() - want.view(R, C)).abs().max()) <= 20 * tol
+    # (dgamma also carries xhat's error, 4 tol of dy at most)
+    assert bool(((dg.double() - want_g).abs() <= tol * size_g + 4 * tol * size_b).all())
+    assert bool(((db.double() - want_b).abs() <= tol * size_b).all())

@@ -45,6 +45,10 @@ constexpr int64_t kResidentBytes = 96 * 1024;
 // four passes: 2, 4, 8 and 16 blocks an SM 294, 299, 309 and 412: few blocks with
 // long loops. Four fill the SMs at every register count.
 constexpr int64_t kSplitBlocks = 4 * kSms;
+// Rows that one thread of a split pass sums in fp32, at most: each sum is then within
+// 1,024 * 2^-24 of its terms' magnitudes, however many samples fill the GPU by
+// themselves. The parts it adds are 8 bytes a channel for 1,024 rows or more.
+constexpr int64_t kThreadRows = 1024;
 constexpr int64_t kPartBlocks = 4 * kSms;    // blocks of a backward pass that keep dgamma sums
 
 struct Params {
@@ -754,7 +758,7 @@ Plan plan_of(const NormArgs &a, bool bwd) {
     p.vec = aligned;
     slice_columns(a.channels / (aligned ? vec : 1), &p);
     const int64_t want = std::max<int64_t>(1, kSplitBlocks / (a.samples * p.slices_y));
-    p.chunk_rows = std::max<int64_t>((a.rows + want - 1) / want, 1);
+    p.chunk_rows = std::min((a.rows + want - 1) / want, kThreadRows * p.per_block);
     p.chunks = static_cast<int32_t>((a.rows + p.chunk_rows - 1) / p.chunk_rows);
     p.grid = a.samples * p.chunks;
     p.parts = static_cast<int32_t>(p.grid);
