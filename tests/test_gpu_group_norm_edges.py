@@ -85,3 +85,34 @@ def test_samples_longer_than_a_chunk():
     # (dgamma also carries xhat's error, 4 tol of dy at most)
     assert bool(((dg.double() - want_g).abs() <= tol * size_g + 4 * tol * size_b).all())
     assert bool(((db.double() - want_b).abs() <= tol * size_b).all())
+
+
+@pytest.mark.parametrize("case", [(2, 1, 64, 8), (3, 16, 60, 12), (2, 9000, 64, 16)], ids=str)
+def test_fp32_silu_far_from_zero(case):
+    """x = +-1 (mean 0, variance 1, eps 0: xhat = x exactly), gamma and beta whole, so
+    z is exact down to -80. y = z / (1 + exp(-z)), in units of 2^-24: the power of two
+    4 (2 ulp), its correction and their product 2, the sum 1, the reciprocal 2, y's
+    product 1: 10. The slope s (1 + z (1 - s)) takes 6 more roundings: 2^-20."""
+    S, R, C, K = case
+    x = torch.ones(S * R, C, device=DEV)
+    x.view(S * R, C)[:, ::2] = -1
+    if C // K % 2:
+        x.view(S, R, C)[:, 1::2] *= -1
+    gamma = torch.ones(C, device=DEV)
+    beta = -(torch.arange(C, device=DEV) % 80).float()
+    y, stats = torch.empty_like(x), torch.empty(S, K, 2, device=DEV)
+    atlas.group_norm(x, gamma, beta, y, R, K, eps=0.0, activation="silu", stats=stats)
+    assert torch.equal(stats, torch.tensor([0.0, 1.0], device=DEV).expand(S, K, 2))
+    z = (x * gamma + beta).double()
+    want = z / (1 + torch.exp(-z))
+    assert float(((y.double() - want).abs() / want.abs().clamp_min(1e-40)).max()) <= 10 * 2.0 ** -24
+    # dbeta of one row with dy = 1 at a time: the slope itself
+    dy = torch.zeros_like(x)
+    dy[S * R // 2] = 1
+    dx, db = torch.empty_like(x), torch.empty(C, device=DEV)
+    atlas.group_norm_bwd(dy, x, gamma, beta, stats, dx, None, db, R, K, activation="silu")
+    zr = z[S * R // 2]
+    s = 1 / (1 + torch.exp(-zr))
+    slope = s * (1 + zr * (1 - s))
+    terms = s * (1 + zr.abs() * (1 - s))
+    assert bool(((db.double() - slope).abs() <= 2.0 ** -20 * terms).all())

@@ -128,22 +128,43 @@ __device__ __forceinline__ float gamma_of(const Params &p, int64_t c) {
 __device__ __forceinline__ float beta_of(const Params &p, int64_t c) {
     return p.beta ? __ldg(p.beta + c) : 0.f;
 }
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 2^x, 2 ulp.
+__device__ __forceinline__ float exp2f_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 / (1 + exp(-z)). bf16 takes the fast exponential, whose relative error of 2^-21 +
+// 2^-22 |z| is far inside the output's rounding wherever the value is not negligible
+// beside the others. fp32 keeps the digits of small values too: -z log2(e) as a
+// rounded product and, by fma, what it lacks; 2^(h + l) = 2^h (1 + l ln 2). Below z =
+// -87 the quotient may be 0 (silu there: below 2^-119).
+template <typename T>
+__device__ __forceinline__ float sigmoid(float z) {
+    if constexpr (sizeof(T) == 2) return __fdividef(1.f, 1.f + __expf(-z));
+    constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
+    const float y = fminf(fmaxf(-z, -200.f), 200.f);   // (l of an infinite one would be NaN)
+    const float h = y * kLog2e, l = fmaf(y, kRest, fmaf(y, kLog2e, -h));
+    return __fdividef(1.f, fmaf(exp2f_fast(h), fmaf(l, kLn2, 1.f), 1.f));
+}
 // act(z), and dy act'(z).
-__device__ __forceinline__ float act(float z, int silu) { return silu ? z * sigmoid(z) : z; }
+template <typename T>
+__device__ __forceinline__ float act(float z, int silu) { return silu ? z * sigmoid<T>(z) : z; }
+template <typename T>
 __device__ __forceinline__ float act_grad(float dy, float z, int silu) {
     if (!silu) return dy;
-    const float s = sigmoid(z);
+    const float s = sigmoid<T>(z);
     return dy * (s * fmaf(z, 1.f - s, 1.f));
 }
 // xhat and dz of one element.
 struct Grad {
     float hat, dz;
 };
+template <typename T>
 __device__ __forceinline__ Grad grad_of(float x, float dy, float2 st, float ga, float be, int silu) {
     Grad g;
     g.hat = (x - st.x) * st.y;
-    g.dz = act_grad(dy, fmaf(g.hat, ga, be), silu);
+    g.dz = act_grad<T>(dy, fmaf(g.hat, ga, be), silu);
     return g;
 }
 // dh: its own rounding, so that a group of one value gives exactly 0.
@@ -209,14 +230,14 @@ __global__ void __launch_bounds__(kThreads) norm_heads_kernel(const Params p) {
                 const float rstd = rsqrtf(fmaf(lanes_sum(sq, LANES), inv_n, p.eps));
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    o.set(e, act(fmaf((xv[f][e] - mean) * rstd, ga[e], be[e]), p.silu));
+                    o.set(e, act<T>(fmaf((xv[f][e] - mean) * rstd, ga[e], be[e]), p.silu));
                 if (on && p.stats != nullptr && col % LANES == 0)
                     put_stat(p, s * p.groups + group, mean, rstd);
             } else {
                 float hat[V], dh[V], s1 = 0.f, s2 = 0.f;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const Grad g = grad_of(xv[f][e], gv[f][e], st[f], ga[e], be[e], p.silu);
+                    const Grad g = grad_of<T>(xv[f][e], gv[f][e], st[f], ga[e], be[e], p.silu);
                     hat[e] = g.hat;
                     dh[e] = dh_of(g.dz, ga[e]);
                     s1 += dh[e];
@@ -328,7 +349,7 @@ __global__ void __launch_bounds__(kThreads) norm_resident_kernel(const Params p)
                 v.load(xs + in);
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    o.set(e, act(fmaf((v[e] - mean) * rstd, gamma_of(p, ch0 + c + e),
+                    o.set(e, act<T>(fmaf((v[e] - mean) * rstd, gamma_of(p, ch0 + c + e),
                                       beta_of(p, ch0 + c + e)), p.silu));
                 o.store(out + at);
             }
@@ -346,7 +367,7 @@ __global__ void __launch_bounds__(kThreads) norm_resident_kernel(const Params p)
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float ga = gamma_of(p, ch0 + c + e);
-                    const Grad d = grad_of(v[e], w[e], st, ga, beta_of(p, ch0 + c + e), p.silu);
+                    const Grad d = grad_of<T>(v[e], w[e], st, ga, beta_of(p, ch0 + c + e), p.silu);
                     s1 += dh_of(d.dz, ga);
                     s2 = fmaf(dh_of(d.dz, ga), d.hat, s2);
                 }
@@ -360,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) norm_resident_kernel(const Params p)
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float ga = gamma_of(p, ch0 + c + e);
-                    const Grad d = grad_of(v[e], w[e], st, ga, beta_of(p, ch0 + c + e), p.silu);
+                    const Grad d = grad_of<T>(v[e], w[e], st, ga, beta_of(p, ch0 + c + e), p.silu);
                     o.set(e, st.y * (dh_of(d.dz, ga) - m1 - d.hat * m2));
                 }
                 o.store(out + at);
@@ -373,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) norm_resident_kernel(const Params p)
                     const float ga = gamma_of(p, ch0 + k), be = beta_of(p, ch0 + k);
                     float2 a = acc[k];
                     for (int64_t r = 0; r < p.rows; ++r) {
-                        const Grad d = grad_of(Io<T>::get(xs[r * width + k]),
+                        const Grad d = grad_of<T>(Io<T>::get(xs[r * width + k]),
                                                Io<T>::get(gs[r * width + k]), sk, ga, be, p.silu);
                         a.x = fmaf(d.dz, d.hat, a.x);
                         a.y += d.dz;
@@ -457,7 +478,7 @@ __global__ void __launch_bounds__(kThreads) norm_split_sums_kernel(const Params 
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     if (BWD) {
-                        const Grad d = grad_of(v[f][e], w[f][e], st[e], ga[e], be[e], p.silu);
+                        const Grad d = grad_of<T>(v[f][e], w[f][e], st[e], ga[e], be[e], p.silu);
                         a[e] = fmaf(d.dz, d.hat, a[e]);
                         b[e] += d.dz;
                     } else {
@@ -615,9 +636,13 @@ __global__ void __launch_bounds__(kThreads) norm_split_join_kernel(const Params 
     }
 }
 
-// The result, rows of all samples last to first.
+// The result, rows of all samples last to first. (fp32: three blocks an SM; left
+// alone, the compiler takes 106 registers for eight rows' sigmoids side by side, two
+// blocks: 400 x 20,000 x 32 without an activation 570 us, 540 with three; 2 x 322,560
+// x 128 with SiLU 187, 196 with three.)
 template <typename T, int V, bool BWD>
-__global__ void __launch_bounds__(kThreads) norm_split_apply_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && V > 1 ? 3 : 1)
+norm_split_apply_kernel(const Params p) {
     constexpr int kFlight = BWD ? 4 : 8;
     const Slot t = slot_of(p, p.channels / V);
     if (!t.active) return;
@@ -654,10 +679,10 @@ __global__ void __launch_bounds__(kThreads) norm_split_apply_kernel(const Params
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 if (BWD) {
-                    const Grad d = grad_of(v[f][e], w[f][e], st[e], ga[e], be[e], p.silu);
+                    const Grad d = grad_of<T>(v[f][e], w[f][e], st[e], ga[e], be[e], p.silu);
                     o.set(e, st[e].y * (dh_of(d.dz, ga[e]) - mm[e].x - d.hat * mm[e].y));
                 } else {
-                    o.set(e, act(fmaf((v[f][e] - st[e].x) * st[e].y, ga[e], be[e]), p.silu));
+                    o.set(e, act<T>(fmaf((v[f][e] - st[e].x) * st[e].y, ga[e], be[e]), p.silu));
                 }
             }
             o.store_last(out + rr * p.channels);
