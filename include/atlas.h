@@ -613,7 +613,8 @@ atlas_status atlas_diff_lambda_bwd(const void *q1, const void *k1, const void *q
  * exact fp32 products. head_dim 64 or 128.
  * A row's result depends on no key that it does not see, whatever that key holds
  * (infinities and NaN included). BF16, windows below 128 rows: a row that sees a
- * key whose v is not finite is NaN in all its channels.
+ * key whose v is not finite is NaN in all its channels. A row whose logits are all
+ * -inf in a map is NaN (0 / 0), with lse -inf there.
  * Errors: as atlas_local_global_attn_ex; NULL lambda (NULL), n_lambda neither 1
  * nor heads (SHAPE), lambda not 4-byte aligned (ALIGN).
  */

@@ -48,3 +48,35 @@ def test_non_finite_value_reaches_every_channel_of_its_rows(hd, steep):
             first = first or out
             for n in ("o_d", "s_d"):
                 assert torch.equal(first[n][~rows], out[n][~rows]), n
+
+
+def rest_of(N, w, L):
+    keep = torch.ones(N, dtype=torch.bool, device=DEV)
+    keep[w * L:(w + 1) * L] = False
+    return keep
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("L", [20, 160])
+def test_rows_whose_logits_are_all_minus_infinity(L, hd, dtype):
+    """0 / 0 in the softmax's definition: NaN in o (and in s for the second map),
+    in the gradients that the row reaches, and lse -inf, in both types."""
+    B, N, G, H = 1, 320, 0, 1
+    lam = torch.tensor([0.6], device=DEV)
+    for ch, both in ((3, False), (hd // 2 + 3, True)):
+        t = make(B, N, G, H, hd, dtype)
+        mine = slice(L, 2 * L)
+        t["k_d"][mine, 0, ch] = float("-inf")
+        t["q_d"][mine, 0, ch] = 1.0
+        t["q_d"][L + 7, 0, ch] = 2.0
+        out = run(t, lam, B, N, G, H, window_len=L)
+        m = 1 if both else 0
+        assert bool((out["lse"][0, 0, m, mine] == float("-inf")).all())
+        assert bool(torch.isfinite(out["lse"][0, 0, 1 - m]).all())
+        assert bool(torch.isnan(out["o_d"][mine]).all())
+        assert bool(torch.isnan(out["s_d"][mine]).all()) == both
+        assert bool(torch.isnan(out["dq_d"][mine]).all())
+        keep = rest_of(N, 1, L)
+        for n in ("o_d", "s_d", "dq_d", "dk_d", "dv_d"):
+            assert bool(torch.isfinite(out[n][keep]).all()), n

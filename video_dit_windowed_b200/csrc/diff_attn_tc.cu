@@ -636,8 +636,10 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
         // Epilogue: both maps' 1/l through shared memory; this group joins
         // columns [map * D/2, +D/2) of O_1 and O_2.
         const uint32_t par = unit_iter & 1;
-        const float l_o = l_run + l_fix;
-        sm.inv_l[par][map][r] = l_o > 0.f ? 1.f / l_o : (l_o == 0.f ? 0.f : l_o);
+        // (a sum of 0: every logit is -inf, and 0 / 0 is NaN; rows past the unit have
+        // none to store)
+        const float l_o = l_run + l_fix, nan = __uint_as_float(0x7fffffffu);
+        sm.inv_l[par][map][r] = l_o > 0.f ? 1.f / l_o : nan;
         ptx::mbar_arrive(ptx::smem_addr(&sm.joined));
         if (p.lse != nullptr && valid) {
             const int64_t rows = static_cast<int64_t>(p.shape.N) + p.shape.G;
@@ -650,7 +652,6 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
             return;
         ptx::tc_fence_after();
         if (PACK) check_bad(n - 1, cnt - 1);
-        const float nan = __uint_as_float(0x7fffffffu);
         const float f1 = bad ? nan : sm.inv_l[par][0][r], f2 = bad ? nan : sm.inv_l[par][1][r];
         constexpr int kHalf = HD / 2;
         uint32_t o1[kHalf], o2[kHalf];
