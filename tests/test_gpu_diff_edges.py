@@ -80,3 +80,40 @@ def test_rows_whose_logits_are_all_minus_infinity(L, hd, dtype):
         keep = rest_of(N, 1, L)
         for n in ("o_d", "s_d", "dq_d", "dk_d", "dv_d"):
             assert bool(torch.isfinite(out[n][keep]).all()), n
+
+
+SHORT = {
+    # what changes in the rows of one window: tensor, row in it, channel, value
+    "nan key": lambda t, a, b: t["k_d"][a + 3, 0].__setitem__(3, float("nan")),
+    "inf query": lambda t, a, b: t["q_d"][a + 5, 0].__setitem__(40, float("inf")),
+    "large keys": lambda t, a, b: t["k_d"][a:b].mul_(12.0),
+    "large queries": lambda t, a, b: t["q_d"][a:b].mul_(16.0),
+    "nan queries": lambda t, a, b: t["q_d"][a:b].fill_(float("nan")),
+    # logits of -inf for all of the window's own keys, in the first map
+    "own keys at -inf": lambda t, a, b: (t["q_d"][a:b, 0, 3].fill_(1.0),
+                                         t["k_d"][a:b, 0, 3].fill_(float("-inf"))),
+}
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("grow", [1.0, 9.0], ids=["level", "growing"])
+@pytest.mark.parametrize("change", SHORT, ids=str)
+def test_rows_keep_their_bits_beside_a_changed_window(hd, change, grow):
+    """bf16, windows that share a 128-row tile and see 300 global keys, whose whole
+    tiles take no mask: whatever one window's rows hold, the others' bits stay."""
+    B, N, L, G, H, w = 1, 200, 20, 300, 1, 4
+    lam = torch.tensor([0.6], device=DEV)
+    t = make(B, N, G, H, hd, "bf16")
+    # level global keys: no other row moves its reference; growing ones: each does now and then
+    t["k_g"] = (t["k_g"].float() * torch.linspace(0.5, grow, G, device=DEV)[:, None, None]).to(torch.bfloat16)
+    clean = run(t, lam, B, N, G, H, window_len=L)
+    bad = {n: x.clone() for n, x in t.items()}
+    SHORT[change](bad, w * L, (w + 1) * L)
+    out = run(bad, lam, B, N, G, H, window_len=L)
+    keep = rest_of(N, w, L)
+    for n in ("o", "s", "dq", "dk", "dv"):
+        assert torch.equal(out[n + "_d"][keep], clean[n + "_d"][keep]), n
+    for n in ("o", "s", "dq"):
+        assert torch.equal(out[n + "_g"], clean[n + "_g"]), n
+    every = torch.cat([keep, torch.ones(G, dtype=torch.bool, device=DEV)])
+    assert torch.equal(out["lse"][..., every], clean["lse"][..., every])

@@ -390,7 +390,7 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
     };
     constexpr std::integral_constant<int, 0> c0{};
     constexpr std::integral_constant<int, 32> c32{};
-    // All 64 with ex2, stored (masked tiles, and rows whose reference moves).
+    // All 64 with ex2, stored (masked tiles).
     auto exps_all = [&](const uint32_t (&sr)[64], float m, uint32_t dst, ptx::F2 &sum) {
         float unused[2];
         uint32_t pk[16];
@@ -513,7 +513,9 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
             ptx::tc_fence_after();
             ptx::tmem_ld64(t_lo, lo);
             ptx::F2 sum = ptx::f2(0.f, 0.f);
-            if (__any_sync(kAll, m_run == kNegInf || masked)) {
+            // (which form a tile takes follows from the layout alone, not from what
+            // the keys hold)
+            if (__any_sync(kAll, j == 0 || masked)) {
                 if (!__all_sync(kAll, wait_phase(sm, sm.s_hi[map], cnt & 1, err))) return;
                 ptx::tc_fence_after();
                 ptx::tmem_ld64(t_hi, hi);
@@ -538,37 +540,44 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                     l_fix += rounded_sum(t_lo) - (s0 + s1);
                 }
             } else {
-                // Exponentials against the running reference right away; a half
-                // whose maximum turns out past the threshold (or NaN) is redone.
-                float mx[2] = {kNegInf, kNegInf};
+                // Exponentials against the running reference right away. Where a row's
+                // maximum turns out past the threshold its warp repeats the half: the
+                // rows whose reference stays get the same bits again, so that no row's
+                // weights depend on its neighbours' keys.
+                float mx[2], mx2;
                 uint32_t pk[16];
-                exps(std::true_type{}, c0, c32, lo, m_run, sum, mx, pk);
-                ptx::tmem_st16_nowait(t_lo, pk);
-                exps(std::true_type{}, c32, c32, lo, m_run, sum, mx, pk);
-                ptx::tmem_st16_nowait(t_lo + 16, pk);
-                if (!__all_sync(kAll, wait_phase(sm, sm.s_hi[map], cnt & 1, err))) return;
-                ptx::tc_fence_after();
-                float mx2 = ptx::max_nan(mx[0], mx[1]) * sc;
-                if (__any_sync(kAll, !(mx2 <= m_run + kRescaleThreshold))) {
+                for (;;) {
+                    const float m = m_run == kNegInf ? 0.f : m_run;
+                    mx[0] = mx[1] = kNegInf;
+                    sum = ptx::f2(0.f, 0.f);
+                    exps(std::true_type{}, c0, c32, lo, m, sum, mx, pk);
+                    ptx::tmem_st16_nowait(t_lo, pk);
+                    exps(std::true_type{}, c32, c32, lo, m, sum, mx, pk);
+                    ptx::tmem_st16_nowait(t_lo + 16, pk);
+                    if (!__all_sync(kAll, wait_phase(sm, sm.s_hi[map], cnt & 1, err))) return;
+                    ptx::tc_fence_after();
+                    mx2 = ptx::max_nan(mx[0], mx[1]) * sc;
+                    if (!__any_sync(kAll, mx2 > m_run + kRescaleThreshold)) break;
                     ptx::tmem_wait_st();
                     move(mx2, false);
-                    sum = ptx::f2(0.f, 0.f);
-                    exps_all(lo, m_run, t_lo, sum);
                 }
                 ptx::tmem_ld64(t_hi, hi);
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(ptx::smem_addr(&sm.s_read[map]));
                 if (PACK && j > 0) check_bad(j - 1, cnt - 1);
                 const ptx::F2 sum_lo = sum;
-                mx[0] = mx[1] = kNegInf;
-                sum = ptx::f2(0.f, 0.f);
-                exps(std::true_type{}, c0, c32, hi, m_run, sum, mx, pk);
-                ptx::tmem_st16_nowait(t_lo + 32, pk);
-                exps(std::true_type{}, c32, c32, hi, m_run, sum, mx, pk);
-                ptx::tmem_st16_nowait(t_lo + 48, pk);
-                mx2 = ptx::max_nan(mx[0], mx[1]) * sc;
+                const float mx_lo = mx2;
                 float f = 1.f;
-                if (__any_sync(kAll, !(mx2 <= m_run + kRescaleThreshold))) {
+                for (;;) {
+                    const float m = m_run == kNegInf ? 0.f : m_run;
+                    mx[0] = mx[1] = kNegInf;
+                    sum = ptx::f2(0.f, 0.f);
+                    exps(std::true_type{}, c0, c32, hi, m, sum, mx, pk);
+                    ptx::tmem_st16_nowait(t_lo + 32, pk);
+                    exps(std::true_type{}, c32, c32, hi, m, sum, mx, pk);
+                    ptx::tmem_st16_nowait(t_lo + 48, pk);
+                    mx2 = ptx::max_nan(mx[0], mx[1]) * sc;
+                    if (!__any_sync(kAll, mx2 > m_run + kRescaleThreshold)) break;
                     ptx::tmem_wait_st();
                     f = move(mx2, false);
                     uint32_t plo[32];
@@ -581,9 +590,10 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
                         plo[e] = *reinterpret_cast<const uint32_t *>(&v);
                     }
                     ptx::tmem_st32_nowait(t_lo, plo);
-                    sum = ptx::f2(0.f, 0.f);
-                    exps_all(hi, m_run, t_lo + 32, sum);
                 }
+                // +inf and NaN make the row NaN (exp2_pair need not).
+                if (!(ptx::max_nan(mx_lo, mx2) < __builtin_huge_valf()))
+                    l_run = __uint_as_float(0x7fffffffu);
                 sum = ptx::fma2(sum_lo, ptx::f2(f, f), sum);
             }
             ptx::tmem_wait_st();
@@ -636,10 +646,10 @@ __device__ void softmax_epilogue(const Params &p, const Sched &S, Smem<HD> &sm, 
         // Epilogue: both maps' 1/l through shared memory; this group joins
         // columns [map * D/2, +D/2) of O_1 and O_2.
         const uint32_t par = unit_iter & 1;
-        // (a sum of 0: every logit is -inf, and 0 / 0 is NaN; rows past the unit have
+        // (no reference: every logit is -inf, and 0 / 0 is NaN; rows past the unit have
         // none to store)
         const float l_o = l_run + l_fix, nan = __uint_as_float(0x7fffffffu);
-        sm.inv_l[par][map][r] = l_o > 0.f ? 1.f / l_o : nan;
+        sm.inv_l[par][map][r] = l_o > 0.f && m_run != kNegInf ? 1.f / l_o : nan;
         ptx::mbar_arrive(ptx::smem_addr(&sm.joined));
         if (p.lse != nullptr && valid) {
             const int64_t rows = static_cast<int64_t>(p.shape.N) + p.shape.G;
