@@ -637,7 +637,8 @@ atlas_status atlas_diff_attn(const void *q_d, const void *k_d, const void *v_d,
  * before dlambda and dk; W = P_1 - lambda P_2 and dS are rounded to bf16 before their
  * products. As in the forward pass, a row that is not met by a query or key does
  * not reach its gradients; a query whose do is not finite makes the whole dv rows
- * (BF16) of the keys it sees NaN.
+ * (BF16) of the keys it sees NaN, a key with a k that is not finite the dq of the
+ * queries that see it (FP32, and BF16 windows below 128 rows: the whole rows).
  * o_*, s_*, lse: the forward's. workspace: DEVICE fp32, 16-byte aligned, of
  * atlas_diff_attn_bwd_workspace bytes, overwritten; calls that overlap on the
  * GPU need one each. dq_*, dk_*, dv_*: as q_*; dlambda: fp32 [n_lambda]. All sums

@@ -117,3 +117,25 @@ def test_rows_keep_their_bits_beside_a_changed_window(hd, change, grow):
         assert torch.equal(out[n + "_g"], clean[n + "_g"]), n
     every = torch.cat([keep, torch.ones(G, dtype=torch.bool, device=DEV)])
     assert torch.equal(out["lse"][..., every], clean["lse"][..., every])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("L", [20, 160])
+def test_key_at_minus_infinity_reaches_dq(L, hd, dtype):
+    """A key with -inf in a channel where its queries are positive has weight 0, so
+    o is finite, but dq = sum dS k holds 0 * -inf: NaN, as the formula gives it.
+    Queries of other windows keep finite gradients."""
+    B, N, G, H = 1, 320, 30, 2
+    lam = torch.tensor([0.6, 0.3], device=DEV)
+    t = make(B, N, G, H, hd, dtype)
+    t["q_d"][L:2 * L, :, 3] = 1.0
+    t["k_d"][L + 7, :, 3] = float("-inf")
+    out = run(t, lam, B, N, G, H, window_len=L)
+    for n in ("o", "s", "dv"):
+        for p in "dg":
+            assert bool(torch.isfinite(out[f"{n}_{p}"]).all()), (n, p)
+    assert bool(torch.isnan(out["dq_d"][L:2 * L, :, 3]).all())
+    keep = rest_of(N, 1, L)
+    assert bool(torch.isfinite(out["dq_d"][keep]).all()) and bool(torch.isfinite(out["dq_g"]).all())
+    assert bool(torch.isfinite(out["dk_d"]).all()) and bool(torch.isfinite(out["dlam"]).all())

@@ -45,8 +45,9 @@
 // before those products where they hold a non-finite value: rows past the unit's
 // ranges always; in DKDV the query rows whose D is NaN (diff_attn.cu; W and dS of
 // the keys that do see such a query are NaN); in DQ's packed units the K rows with
-// a non-finite channel (dS of the queries that see one is NaN). Every wait is
-// bounded, as in the forward.
+// a non-finite channel (dQ of the queries that see one is made NaN in the epilogue:
+// their dS is 0 where such a key has weight 0). Every wait is bounded, as in the
+// forward.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -105,6 +106,8 @@ struct Smem {
     alignas(16) float lse[kStages][2][FORM == kDQ ? 4 : kStream];     // DKDV: of the streamed queries
     alignas(16) float delta[kStages][2][FORM == kDQ ? 4 : kStream];
     float row_sum[2][2][FORM == kDQ ? kRows : 1];   // DQ: [unit & 1][map], of warpgroup 1
+    uint32_t bad_k[2][8];   // DQ: [tile & 1][K row / 8], bit 4 (row % 8): not finite
+    volatile uint32_t any_bad_k;   // set with the first such row
     uint64_t x_full, x_empty;
     uint64_t st_full[kStages], st_empty[kStages];
     uint64_t s_full;     // S_1, S_2, dP of a tile in TMEM           (commit)
@@ -437,6 +440,14 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
         ptx::mbar_arrive(ptx::smem_addr(&sm.x_full));
     };
     bool resident_ready = false;   // DQ: this unit's rows were written ahead
+    // DQ, packed units: whether keys [lo, hi) of the tile at t0, tile count c, hold a
+    // bad K row. Read behind the tile's products (acc_done, acc_full), which follow
+    // every thread's p_full; written again two tiles on, behind the p_full in between.
+    auto sees_bad = [&](int32_t t0, int32_t lo, int32_t hi, uint32_t c) -> bool {
+        for (int k = max(lo - t0, 0); k < min(hi - t0, kStream); ++k)
+            if ((sm.bad_k[c & 1][k / 8] >> (4 * (k % 8))) & 1u) return true;
+        return false;
+    };
 
     for (int32_t u = blockIdx.x; u < S.n_units; u += gridDim.x) {
         const Unit U = unit_at<FORM>(p, S, u);
@@ -458,7 +469,12 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
         int32_t da = 0, db = 0, ga = 0, gb = 0;   // streamed rows this row meets
         float own_l[2] = {__builtin_huge_valf(), __builtin_huge_valf()}, own_d[2] = {0.f, 0.f};
         float sum_d[2] = {0.f, 0.f};              // DQ: of this warpgroup's dS
-        float dk_on = 1.f;                        // DKDV: 0 where dK is
+        float dk_on = 1.f;                        // DKDV: 0 where dK is; DQ: NaN where dQ is
+        const bool scan = FORM == kDQ && U.detail && U.win < 0;
+        auto check_bad = [&](int32_t j, uint32_t c) {
+            if (sees_bad(units::tile_row<kStream>(U, j), j < U.n_a ? da : ga, j < U.n_a ? db : gb, c))
+                dk_on = __uint_as_float(0x7fffffffu);
+        };
         const int64_t col = (static_cast<int64_t>(U.b) * p.shape.heads + U.head) * 2 * per +
                             (U.detail ? row : static_cast<int64_t>(N) + row);
         if (valid) {
@@ -544,6 +560,7 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
                 !__all_sync(kAll, wait_phase(sm, sm.acc_done, (cnt - 1) & 1, kErrTimeoutSoftmax)))
                 return;
             ptx::tc_fence_after();
+            const uint32_t any_bad = scan && j > 0 ? sm.any_bad_k : 0;
             const uint32_t dst = t + TM::kDS + part * kPack;
             if constexpr (FORM == kDQ) {
                 ptx::tmem_st16_nowait(dst, pd1);
@@ -554,7 +571,9 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
                 ptx::tmem_st12_nowait(dst + TM::kPackedStride, pd2);
             }
             ptx::tmem_wait_st();
-            // Rows to zero (S and dP of this tile are done with them).
+            if (any_bad != 0) check_bad(j - 1, cnt - 1);
+            // Rows to zero (S and dP of this tile are done with them; s_full, which
+            // follows the issuer's wait for the loads, orders them before).
             constexpr int kVecs = HD / 64 * 8;   // 16-byte vectors of a row
             auto vec_at = [&](int sr, int v) {
                 return (v / 8) * kStream * 128 + sr * 128 + (v % 8) * 16;
@@ -578,7 +597,7 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
                     }
                     wrote = true;
                 }
-            } else if (U.detail && U.win < 0) {
+            } else if (scan) {
                 // four threads per K row (8 rows of a warp's LDS: no conflicts)
                 const int sr = threadIdx.x / 4, q = threadIdx.x & 3;
                 bool bad = false;
@@ -586,6 +605,11 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
                     bad |= not_finite(*reinterpret_cast<const uint4 *>(sm.xs[stage] + vec_at(sr, v)));
                 bad |= __shfl_xor_sync(kAll, static_cast<int>(bad), 1) != 0;
                 bad |= __shfl_xor_sync(kAll, static_cast<int>(bad), 2) != 0;
+                const uint32_t rows = __ballot_sync(kAll, bad && sr < seen);
+                if ((threadIdx.x & 31) == 0) {
+                    sm.bad_k[cnt & 1][warp] = rows;
+                    if (rows != 0) sm.any_bad_k = 1;
+                }
                 if (bad) {
                     for (int v = q; v < kVecs; v += 4)
                         ptx::st_shared_v4(sm.xs[stage] + vec_at(sr, v), 0, 0, 0, 0);
@@ -623,6 +647,7 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
         if (!__all_sync(kAll, wait_phase(sm, sm.acc_full, unit_iter & 1, kErrTimeoutSoftmax)))
             return;
         ptx::tc_fence_after();
+        if (scan && sm.any_bad_k != 0) check_bad(n - 1, cnt - 1);
         if (FORM == kDQ && part == 0 && valid) {
             // dS sums to P (dP - D) = <do, P v> - D: what D lacks.
 #pragma unroll
@@ -711,6 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_bwd_tc_kernel(const __grid_c
         ptx::mbar_init(ptx::smem_addr(&sm.drain[1]), 1);
         sm.abort = 0;
         sm.max_len = 0;
+        sm.any_bad_k = 0;
         sm.err_word = p.err_word;
         ptx::fence_mbar_init();
     }
