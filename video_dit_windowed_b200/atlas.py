@@ -691,6 +691,10 @@ def _diff_sides(batch, detail, glob, window_offsets, global_window_offsets, wind
     ref = next((t for t in (*detail, *glob) if t is not None and t.shape[0] > 0), None)
     _require(ref is not None and ref.dim() == 3 and batch >= 1,
              "diff_attn: [rows, heads, head_dim] tensors and batch >= 1")
+    for side in (detail, glob):   # what such a side holds would be neither read nor written
+        _require(side[0] is not None and side[0].shape[0] > 0 or
+                 all(t is None or t.shape[0] == 0 for t in side),
+                 "diff_attn: rows for a side without queries")
     dev, dtype, tail = ref.get_device(), ref.dtype, ref.shape[1:]
     counts, sides = [], []
     for side in (detail, glob):
