@@ -609,8 +609,9 @@ atlas_status atlas_diff_lambda_bwd(const void *q1, const void *k1, const void *q
  * both maps' softmax denominators.
  * BF16: tcgen05 kernel, both maps' softmax and both outputs in fp32, each map's
  * unnormalised weights rounded to bf16 before their product with v (rows of at most
- * 32 keys are divided by the sum of the rounded weights), o rounded once. FP32:
- * exact fp32 products. head_dim 64 or 128.
+ * 32 keys are divided by the sum of the rounded weights), o rounded once. One weight
+ * pair of eight comes from a polynomial within 2.7e-6 (2^-18.5), in the sums and lse
+ * too. FP32: exact fp32 products. head_dim 64 or 128.
  * A row's result depends on no key that it does not see, whatever that key holds
  * (infinities and NaN included). BF16, windows below 128 rows: a row that sees a
  * key whose v is not finite is NaN in all its channels. A row whose logits are all
@@ -677,7 +678,8 @@ typedef enum { ATLAS_ACT_NONE = 0, ATLAS_ACT_SILU = 1 } atlas_activation;
  * skip (the backward pass needs it). workspace: DEVICE, 16-byte aligned, of
  * atlas_group_norm_workspace bytes (NULL when that is 0); calls that overlap on
  * the GPU need one each. y may equal x. Statistics and arithmetic in fp32
- * (partial statistics joined in fp64), one rounding to dtype.
+ * (partial statistics joined in fp64; no sum of one thread has more than 1,024
+ * rows), one rounding to dtype. BF16: the sigmoid within 2^-20 + 2^-22 |z|.
  * Errors: NULL; samples, rows, channels or groups < 1, channels not a multiple of
  * groups, samples*rows or channels above 2^31-1 (SHAPE); x or y not 16-byte
  * aligned, fp32 arrays not 4-byte aligned (ALIGN); dtype, act, eps < 0 or not

@@ -17,10 +17,10 @@
 //         the units over global keys are few and long (each streams every query):
 //         their queries are cut into parts, whose fp32 sums a second kernel joins
 //         in order (diff_attn.cu, diff_split_plan).
-// Measured at 720p, one head of 128: dQ 595 us, dK/dV 778 us (their products alone 230
+// Measured at 720p, one head of 128: dQ 584 us, dK/dV 777 us (their products alone 230
 // and 307: S, dP and the accumulations, 6 D and 8 D flops a pair); bound by the compute
-// warps' instructions, two exponentials and two gradients a pair (issue slots 57 to
-// 59 % busy with two such warps a scheduler; tensor 31 to 33 %).
+// warps' instructions, two exponentials and two gradients a pair (issue slots 58 to
+// 60 % busy with two such warps a scheduler; tensor 31 to 33 %).
 // Tensor memory holds S_1 | S_2 | dP of one tile, the packed bf16 dS_1 | dS_2 (and
 // W) in columns of their own, and the accumulators:
 //   DQ    3 x 64 + 64 + 128 (dQ) + 128 (resident Q, dO) = 512,

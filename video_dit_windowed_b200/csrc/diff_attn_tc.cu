@@ -34,12 +34,14 @@
 // zeroed in shared memory before the product. In packed units (PACK), whose rows
 // see different windows, so are V rows with a non-finite value, and the rows that
 // do see such a key become NaN in the epilogue.
-// Measured: 720p (80,640 + 5,040 rows, windows of 768), 4 heads, D = 128: 1,613 us,
-// 0.94 PFLOP/s (products alone 923 us, exponentials alone 878); 32,760 tokens, D = 64:
-// 860-930 us (exponentials 477). No pipe is saturated (MUFU 52 %, tensor 44 %, issue
-// slots 43 % busy): a scheduler has two softmax warps, whose dependent steps (logits
-// from tensor memory, exponentials, conversion, P back, hand-over) do not hide one
-// another; more warps would need the registers that hold 128 logits a thread.
+// Measured: 720p (80,640 + 5,040 rows, windows of 768), 4 heads, D = 128: 1,580-1,590
+// us at 1,965 MHz, 0.96 PFLOP/s (products alone 923 us, exponentials alone 878), and
+// 1,740 in a row, when the power cap holds the clock at 1,780-1,800 MHz; 32,760 tokens,
+// D = 64: 850-860 us (exponentials 477). No pipe is saturated (MUFU 54 %, tensor and
+// issue slots 45 % busy): a scheduler has two softmax warps, whose dependent steps
+// (logits from tensor memory, exponentials, conversion, P back, hand-over) do not hide
+// one another. Warps of half a tile's columns each, four a scheduler, as the backward
+// splits them, have not been tried.
 // Every wait is bounded: on expiry a bit is set in the device error word, the
 // CTA drains its copies and MMAs, frees its tensor memory and returns.
 #include <cuda.h>
@@ -87,11 +89,11 @@ struct Smem {
     uint64_t kv_empty[kSlots];   // (and q_empty, o_final: a commit by each map's issuer)
     uint64_t s_lo[kMaps];        // first half of S_m(j) in TMEM            (commit)
     uint64_t s_hi[kMaps];        // second half, and O_m += P_m(j-1) V done (commit)
-    uint64_t s_read[kMaps];      // second half loaded                      (4 warps)
-    uint64_t p_full[kMaps];      // P_m(j) in TMEM, O_m rescaled            (4 warps)
+    uint64_t s_read[kMaps];      // second half loaded                      (128 threads)
+    uint64_t p_full[kMaps];      // P_m(j) in TMEM, O_m rescaled            (128 threads)
     uint64_t o_final;            // every MMA of the unit done              (commit)
-    uint64_t joined;             // both maps' inv_l written                (8 warps)
-    uint64_t o_empty;            // both accumulators read                  (8 warps)
+    uint64_t joined;             // both maps' inv_l written                (256 threads)
+    uint64_t o_empty;            // both accumulators read                  (256 threads)
     uint64_t drain[kMaps];
     uint32_t tmem_base;
     int32_t max_len;

@@ -19,8 +19,8 @@
 //             it starts with the rows that are still in L2.
 // Measured: 80,640 tokens of 40 heads of 128, bf16, 314 us for 1.65 GB (5.3 TB/s,
 // 80% of a copy); decoder latents 2 x 322,560 x 128, SiLU, forward and backward 308 us
-// (0.83 GB: 2.7 TB/s; the sums' passes and their joins are launches of their own);
-// 3 x 1,001 x 60, fp32, 37 us, launches.
+// (0.83 GB: 2.7 TB/s; sums 35 and 84 us, results 73 and 101, joins 8 each); 3 x 1,001 x
+// 60, fp32, 39 us, of which the forward's nine resident blocks are 28.
 // Variances are sums of squared deviations: from the mean where the values are
 // held (heads, resident), else from a pivot that a thread moves to the mean of its
 // rows so far (split), joined in fp64, so that neither a large mean nor a first row

@@ -21,10 +21,10 @@
 //                whole heads in shared memory, rotates pair by pair there (lane
 //                = pair, so neighbouring lanes touch neighbouring channels) and
 //                writes them out as vectors.
-// Measured: Q, K, V of 40 heads at 720p, half layout, cube order, 864 us for 4.95 GB
-// (5.7 TB/s, 87% of a copy); 1.61 GB at given positions 258 us (95%); two heads' Q
-// and K of partial cubes, where the angles are half of the work, 418 us for 2.12 GB
-// (77%).
+// Measured, whole calls: Q, K, V of 40 heads at 720p, half layout, cube order, 885 us
+// for 4.95 GB (5.6 TB/s, 86% of a copy); 1.61 GB at given positions 261 us (94%); two
+// heads' Q and K of partial cubes, where the angles are half of the work, 432 us for
+// 2.12 GB (75%).
 #include <cuda_bf16.h>
 
 #include <algorithm>
