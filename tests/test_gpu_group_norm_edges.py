@@ -116,3 +116,21 @@ def test_fp32_silu_far_from_zero(case):
     slope = s * (1 + zr * (1 - s))
     terms = s * (1 + zr.abs() * (1 - s))
     assert bool(((db.double() - slope).abs() <= 2.0 ** -20 * terms).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", [(40, 1, 128, 2), (4, 50, 64, 4), (1, 20011, 128, 32), (300, 3000, 32, 8),
+                                  (20, 4, 32800, 1)], ids=str)
+def test_deviations_whose_squares_overflow(case, dtype):
+    """Deviations of 1e25: their squares pass the range of the fp32 statistics. The
+    variance is infinite and rstd 0 in every form, so y is beta: never a small
+    variance and large values."""
+    S, R, C, K = case
+    x = (rnd(S * R, C).sign() * 1e25).to(DT[dtype])
+    if R == 4:   # the same mean in every channel, far from the first row
+        x.view(S, R, C)[:] = torch.tensor([1.0, -1, -1, -1], device=DEV)[:, None] * 1e25
+    beta = rnd(C, seed=1)
+    y, stats = torch.empty_like(x), torch.empty(S, K, 2, device=DEV)
+    atlas.group_norm(x, None, beta, y, R, K, stats=stats)
+    assert not stats[..., 1].any()
+    assert torch.equal(y, beta.to(DT[dtype]).expand(S * R, C))
