@@ -648,6 +648,7 @@ __device__ void compute(const Params &p, const Sched &S, Smem<HD, FORM> &sm, uin
             return;
         ptx::tc_fence_after();
         if (scan && sm.any_bad_k != 0) check_bad(n - 1, cnt - 1);
+        __syncwarp();   // (a search may end early; tensor-memory loads want the whole warp)
         if (FORM == kDQ && part == 0 && valid) {
             // dS sums to P (dP - D) = <do, P v> - D: what D lacks.
 #pragma unroll
